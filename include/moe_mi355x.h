@@ -404,6 +404,144 @@ int moe_forward_mxfp8(const uint16_t* x, const uint16_t* w_router, const float* 
                       float* topk_weights_out, void* workspace, size_t ws_bytes,
                       moe_dispatch_info* info, void* stream);
 
+/*
+ * Scored routing: the rule by which a token's experts are chosen and
+ * weighted (host struct; select_bias is a device pointer).  With logits l
+ * of one token:
+ *
+ *   s_e = sigmoid(l_e)  or  softmax(l)_e                the score
+ *   c_e = s_e + select_bias_e                           the choice score
+ *   groups: the E experts are n_group groups of E/n_group consecutive ids;
+ *           a group's score is its largest c (group_top 1) or the sum of its
+ *           two largest (group_top 2); the topk_group best groups stay
+ *   ids   = the top_k largest c among the groups that stay, in descending
+ *           order
+ *   w_j   = scale * s_j / sum_i s_i  (renormalize 1)  or  scale * s_j
+ *
+ * The bias steers the choice alone (a bias that balances the experts'
+ * load); the weights come from the scores without it.
+ *   - Exact ties go to the lower expert id, and to the lower group.  Choice
+ *     scores and group sums are compared as double precision gives them (no
+ *     fp32 rounding decides a choice).  Without select_bias experts are
+ *     ordered by their logits, which order the scores.
+ *   - Logits may be -inf (a masked expert: score 0).  Ids are always top_k
+ *     different ones in [0, E): where fewer experts can be told apart, the
+ *     lowest ids that are left follow.  Renormalized weights stay exact
+ *     where every chosen score underflows; a row whose chosen logits are all
+ *     -inf gets weights 0.  A NaN choice score ranks below all others;
+ *     weights follow the formula, NaN included.
+ *   - select_bias may hold -inf (such an expert comes after all others), not
+ *     +inf.
+ */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+typedef struct moe_routing {
+  int score;                  /* MOE_SCORE_*                                     */
+  int top_k;                  /* experts per token                               */
+  int renormalize;            /* 0 or 1                                          */
+  int n_group;                /* groups, a divisor of E, at most 64; 1: no groups */
+  int topk_group;             /* groups that stay (1..n_group); they must hold
+                                 at least top_k experts                          */
+  int group_top;              /* 1 or 2 (at most E/n_group where n_group > 1)    */
+  float scale;                /* finite factor of every weight                   */
+  const float* select_bias;   /* [E] fp32 or NULL                                */
+} moe_routing;
+
+/*
+ * moe_select -- expert ids and weights from router logits (one launch).
+ *   logits       [M, E] fp32, 16-byte aligned
+ *   topk_ids     [M, top_k] int32 out
+ *   topk_weights [M, top_k] fp32 out
+ */
+int moe_select(const float* logits, const moe_routing* routing, int M, int E, int32_t* topk_ids,
+               float* topk_weights, void* stream);
+
+/*
+ * moe_select_backward -- gradient of moe_select's weights with respect to
+ * the logits (one launch).  The choice itself has no gradient, so
+ * select_bias and the groups take no part and select_bias is not read.
+ *   logits       [M, E] fp32, as given to moe_select, 16-byte aligned
+ *   topk_ids     [M, top_k] int32, as moe_select wrote them; an id outside
+ *                [0, E) takes no part, an id that a row holds more than once
+ *                gets the sum of its slots' gradients
+ *   grad_weights [M, top_k] fp32: dL/dw
+ *   grad_logits  [M, E] fp32 out: dL/dl, every entry written; 16-byte
+ *                aligned, and not logits itself
+ */
+int moe_select_backward(const float* logits, const int32_t* topk_ids, const float* grad_weights,
+                        const moe_routing* routing, int M, int E, float* grad_logits,
+                        void* stream);
+
+/*
+ * moe_route_scored -- moe_route with a routing rule: router logits, then
+ * moe_select on them.  Operands, logits_out and workspace as for moe_route,
+ * all 16-byte aligned.
+ */
+int moe_route_scored(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
+                     const moe_routing* routing, int M, int H, int E, int32_t* topk_ids,
+                     float* topk_weights, float* logits_out, void* workspace, size_t ws_bytes,
+                     void* stream);
+
+/*
+ * The three layers with a routing rule in the place of top_k and
+ * renormalize; everything else, workspace sizes included (with
+ * routing->top_k), as for the calls without `_scored`.  The selection is a
+ * launch of its own: info->launches counts it.
+ */
+int moe_forward_scored(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
+                       const moe_routing* routing, const uint16_t* w13, const uint16_t* w2, int M,
+                       int E, int H, int I, uint16_t* out, int32_t* topk_ids_out,
+                       float* topk_weights_out, void* workspace, size_t ws_bytes,
+                       moe_dispatch_info* info, void* stream);
+int moe_forward_quantized_scored(const uint16_t* x, const uint16_t* w_router,
+                                 const float* logit_bias, const moe_routing* routing,
+                                 const moe_quantized_weights* qw, int M, int E, int H, int I,
+                                 uint16_t* out, int32_t* topk_ids_out, float* topk_weights_out,
+                                 void* workspace, size_t ws_bytes, moe_dispatch_info* info,
+                                 void* stream);
+int moe_forward_mxfp8_scored(const uint16_t* x, const uint16_t* w_router,
+                             const float* logit_bias, const moe_routing* routing,
+                             const moe_mx_weights* w, int M, int E, int H, int I, uint16_t* out,
+                             int32_t* topk_ids_out, float* topk_weights_out, void* workspace,
+                             size_t ws_bytes, moe_dispatch_info* info, void* stream);
+
+/*
+ * One dense matrix [N, K] in the affine group format of
+ * moe_quantized_weights (host struct of device pointers, 16-byte aligned):
+ * element k of a row is bits [4k, 4k+4) of the row's bit stream, and
+ * w = s*q + b with one bf16 scale and bias per group_size elements.
+ */
+typedef struct moe_quantized_matrix {
+  int bits;                  /* 4                                */
+  int group_size;            /* 32, 64 or 128                    */
+  const uint32_t* q;         /* [N, K/8] packed codes            */
+  const uint16_t* scales;    /* [N, K/group_size] bf16           */
+  const uint16_t* biases;    /* [N, K/group_size] bf16           */
+} moe_quantized_matrix;
+
+/*
+ * moe_linear_quantized -- a dense product with 4-bit weights, from one row
+ * (a matrix-vector product) to many: projections, an output head, and a
+ * shared expert beside the routed ones.
+ *
+ *   y[m, n]   = sum_k x[m, k] w[n, k]           fp32 accumulation, codes exact
+ *   gated 0:  f = y, n_out = N
+ *   gated 1:  f[m, i] = SiLU(y[m, i]) * y[m, N/2 + i], n_out = N/2 (gate rows
+ *             first, as in W13)
+ *   out[m, i] = bf16(addend[m, i] + row_scale[m] * f[m, i])
+ *
+ *   x         [M, K] bf16;  K a multiple of group_size
+ *   row_scale [M] fp32 or NULL (1): e.g. a shared expert's sigmoid gate, the
+ *             weights that moe_route_scored gives for E = top_k = 1
+ *   addend    [M, n_out] bf16 or NULL (0): e.g. the routed experts' output;
+ *             may be out itself (added to in place)
+ *   out       [M, n_out] bf16 out
+ * One launch.  M, N, K < 2^24.
+ */
+int moe_linear_quantized(const uint16_t* x, const moe_quantized_matrix* w, int M, int N, int K,
+                         int gated, const float* row_scale, const uint16_t* addend, uint16_t* out,
+                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif

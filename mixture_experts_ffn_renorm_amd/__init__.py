@@ -10,7 +10,10 @@ Function names match the C ABI: moe_route, moe_align,
 moe_grouped_gemm_w13_act, moe_grouped_gemm_w2_combine, moe_forward,
 moe_forward_quantized, moe_forward_mxfp8, moe_mx_quantize, plus
 moe_workspace_size, moe_mx_workspace_size, moe_pick_block_m,
-moe_forward_list_offsets and moe_strerror.
+moe_forward_list_offsets and moe_strerror; and, with a :class:`Routing` rule,
+moe_select, moe_select_backward, moe_route_scored, moe_forward_scored,
+moe_forward_quantized_scored and moe_forward_mxfp8_scored; and
+moe_linear_quantized.
 """
 
 from __future__ import annotations
@@ -72,6 +75,19 @@ class QuantizedWeights(ctypes.Structure):
                 ("w2_q", _c_void_p), ("w2_scales", _c_void_p), ("w2_biases", _c_void_p)]
 
 
+class RoutingRule(ctypes.Structure):
+    """moe_routing: score, sizes, flags, scale and the device pointer of the bias."""
+    _fields_ = [("score", _c_int), ("top_k", _c_int), ("renormalize", _c_int),
+                ("n_group", _c_int), ("topk_group", _c_int), ("group_top", _c_int),
+                ("scale", ctypes.c_float), ("select_bias", _c_void_p)]
+
+
+class QuantizedMatrix(ctypes.Structure):
+    """moe_quantized_matrix: bits, group size and three device pointers."""
+    _fields_ = [("bits", _c_int), ("group_size", _c_int), ("q", _c_void_p),
+                ("scales", _c_void_p), ("biases", _c_void_p)]
+
+
 _SIGNATURES = {
     "moe_workspace_size": (_c_size_t, [_c_int] * 5),
     "moe_strerror": (ctypes.c_char_p, [_c_int]),
@@ -103,6 +119,19 @@ _SIGNATURES = {
                               [_c_int] * 6 +
                               [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_size_t,
                                ctypes.POINTER(DispatchInfo), _c_void_p]),
+    "moe_select": (_c_int, [_c_void_p, _c_void_p, _c_int, _c_int] + [_c_void_p] * 3),
+    "moe_select_backward": (_c_int, [_c_void_p] * 4 + [_c_int] * 2 + [_c_void_p] * 2),
+    "moe_route_scored": (_c_int, [_c_void_p] * 4 + [_c_int] * 3 + [_c_void_p] * 4 +
+                         [_c_size_t, _c_void_p]),
+    "moe_forward_scored": (_c_int, [_c_void_p] * 6 + [_c_int] * 4 + [_c_void_p] * 4 +
+                           [_c_size_t, ctypes.POINTER(DispatchInfo), _c_void_p]),
+    "moe_forward_quantized_scored": (_c_int, [_c_void_p] * 4 + [ctypes.POINTER(QuantizedWeights)] +
+                                     [_c_int] * 4 + [_c_void_p] * 4 +
+                                     [_c_size_t, ctypes.POINTER(DispatchInfo), _c_void_p]),
+    "moe_forward_mxfp8_scored": (_c_int, [_c_void_p] * 4 + [ctypes.POINTER(MxWeights)] +
+                                 [_c_int] * 4 + [_c_void_p] * 4 +
+                                 [_c_size_t, ctypes.POINTER(DispatchInfo), _c_void_p]),
+    "moe_linear_quantized": (_c_int, [_c_void_p] * 2 + [_c_int] * 4 + [_c_void_p] * 4),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -523,3 +552,341 @@ def moe_forward_mxfp8(x, w_router, mxw: dict, top_k: int, renormalize: bool = Tr
         _ptr(ws), ws.numel(), ctypes.byref(info), _stream(stream))
     _raise("moe_forward_mxfp8", st)
     return out, info.as_dict()
+
+
+# ---------------------------------------------------------------------------
+# scored routing and dense 4-bit products
+# ---------------------------------------------------------------------------
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class Routing:
+    """A routing rule (moe_routing in the header): how a token's experts are
+    chosen from its logits and weighted.  Built once and given to every call
+    of a layer.
+
+    ``score``: "softmax" or "sigmoid"; ``select_bias``: [E] fp32 device tensor
+    added to the scores for the choice alone, or None (read at every call, so
+    it may be updated in place between calls); ``n_group`` groups of
+    consecutive experts, of which the ``topk_group`` best stay (default: all),
+    scored by their best expert (``group_top`` 1) or the sum of their best two
+    (2); ``scale``: a factor of every weight."""
+
+    __slots__ = ("_c", "select_bias")
+
+    def __init__(self, top_k: int, score: str = "softmax", renormalize: bool = True,
+                 select_bias=None, n_group: int = 1, topk_group: Optional[int] = None,
+                 group_top: int = 1, scale: float = 1.0):
+        if score not in _SCORES:
+            raise ValueError(f"score must be one of {tuple(_SCORES)}, got {score!r}")
+        if select_bias is not None:
+            _check(select_bias, "select_bias", (_torch().float32,))
+        self.select_bias = select_bias
+        self._c = RoutingRule(_SCORES[score], int(top_k), int(bool(renormalize)), int(n_group),
+                              int(n_group if topk_group is None else topk_group),
+                              int(group_top), float(scale), None)
+
+    @property
+    def top_k(self) -> int:
+        return self._c.top_k
+
+    @property
+    def score(self) -> str:
+        return "sigmoid" if self._c.score else "softmax"
+
+    @property
+    def renormalize(self) -> bool:
+        return bool(self._c.renormalize)
+
+    @property
+    def n_group(self) -> int:
+        return self._c.n_group
+
+    @property
+    def topk_group(self) -> int:
+        return self._c.topk_group
+
+    @property
+    def group_top(self) -> int:
+        return self._c.group_top
+
+    @property
+    def scale(self) -> float:
+        return self._c.scale
+
+    def _arg(self, E: int, device: int) -> int:
+        """Address of the C struct for a layer of E experts on a device."""
+        b = self.select_bias
+        if b is not None:
+            _need(b, "select_bias", _torch().float32, (E,), device)
+            self._c.select_bias = b.data_ptr()
+        return ctypes.addressof(self._c)
+
+
+def _need(t, name, dtype, shape, device: int):
+    """Raise unless t is a dense aligned tensor of that kind on that device."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device and
+            t.is_contiguous() and t.data_ptr() % 16 == 0):
+        torch = _torch()
+        _check(t, name, _bf16_types() if dtype is torch.bfloat16 else (dtype,), shape)
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on device {t.get_device()}, expected {device}")
+
+
+def _device_of(t, name) -> int:
+    if t is None or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.get_device()
+
+
+class _On:
+    """The device of a call's tensors made current, and the stream that the
+    call goes to: ``stream``, or that device's current one."""
+
+    __slots__ = ("device", "stream", "guard", "given")
+
+    def __init__(self, device: int, stream):
+        self.device, self.given = device, stream
+
+    def __enter__(self):
+        torch = _torch()
+        self.guard = None
+        if self.given is not None and self.given.device_index != self.device:
+            raise ValueError(f"the stream is on device {self.given.device_index}, the tensors "
+                             f"on {self.device}")
+        if torch.cuda.current_device() != self.device:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        self.stream = (torch.cuda.current_stream() if self.given is None
+                       else self.given).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+    def empty(self, shape, dtype):
+        """A new tensor that the given stream may use."""
+        t = _torch().empty(shape, dtype=dtype, device=self.device)
+        if self.given is not None:
+            t.record_stream(self.given)
+        return t
+
+
+def moe_select(logits, routing: Routing, topk_ids=None, topk_weights=None, stream=None):
+    """Expert ids [M, top_k] int32 and weights [M, top_k] fp32 of logits
+    [M, E] fp32 under a routing rule."""
+    torch = _torch()
+    M, E = logits.shape
+    k = routing.top_k
+    dev = _device_of(logits, "logits")
+    _need(logits, "logits", torch.float32, (M, E), dev)
+    rule = routing._arg(E, dev)
+    with _On(dev, stream) as on:
+        if topk_ids is None:
+            topk_ids = on.empty((M, k), torch.int32)
+        if topk_weights is None:
+            topk_weights = on.empty((M, k), torch.float32)
+        _need(topk_ids, "topk_ids", torch.int32, (M, k), dev)
+        _need(topk_weights, "topk_weights", torch.float32, (M, k), dev)
+        st = library().moe_select(logits.data_ptr(), rule, M, E, topk_ids.data_ptr(),
+                                  topk_weights.data_ptr(), on.stream)
+    _raise("moe_select", st)
+    return topk_ids, topk_weights
+
+
+def moe_select_backward(logits, topk_ids, grad_weights, routing: Routing, grad_logits=None,
+                        stream=None):
+    """Gradient [M, E] fp32 of moe_select's weights with respect to its
+    logits, for the ids it gave and the weights' gradient [M, top_k] fp32."""
+    torch = _torch()
+    M, E = logits.shape
+    k = routing.top_k
+    dev = _device_of(logits, "logits")
+    _need(logits, "logits", torch.float32, (M, E), dev)
+    _need(topk_ids, "topk_ids", torch.int32, (M, k), dev)
+    _need(grad_weights, "grad_weights", torch.float32, (M, k), dev)
+    rule = routing._arg(E, dev)
+    with _On(dev, stream) as on:
+        if grad_logits is None:
+            grad_logits = on.empty((M, E), torch.float32)
+        _need(grad_logits, "grad_logits", torch.float32, (M, E), dev)
+        st = library().moe_select_backward(logits.data_ptr(), topk_ids.data_ptr(),
+                                           grad_weights.data_ptr(), rule, M, E,
+                                           grad_logits.data_ptr(), on.stream)
+    _raise("moe_select_backward", st)
+    return grad_logits
+
+
+def moe_route_scored(x, w_router, routing: Routing, logit_bias=None, topk_ids=None,
+                     topk_weights=None, logits_out=None, ws=None, stream=None):
+    """moe_route with a routing rule: (topk_ids, topk_weights)."""
+    torch = _torch()
+    M, H = x.shape
+    E = w_router.shape[0]
+    k = routing.top_k
+    dev = _device_of(x, "x")
+    _need(x, "x", torch.bfloat16, (M, H), dev)
+    _need(w_router, "w_router", torch.bfloat16, (E, H), dev)
+    if logit_bias is not None:
+        _need(logit_bias, "logit_bias", torch.float32, (E,), dev)
+    rule = routing._arg(E, dev)
+    with _On(dev, stream) as on:
+        if topk_ids is None:
+            topk_ids = on.empty((M, k), torch.int32)
+        if topk_weights is None:
+            topk_weights = on.empty((M, k), torch.float32)
+        _need(topk_ids, "topk_ids", torch.int32, (M, k), dev)
+        _need(topk_weights, "topk_weights", torch.float32, (M, k), dev)
+        if logits_out is not None:
+            _need(logits_out, "logits_out", torch.float32, (M, E), dev)
+        elif ws is None:
+            ws = on.empty((max(M * E * 4, 16),), torch.uint8)
+        if ws is not None:
+            _need(ws, "ws", torch.uint8, (ws.numel(),), dev)
+        st = library().moe_route_scored(
+            x.data_ptr(), w_router.data_ptr(), _ptr(logit_bias), rule, M, H, E,
+            topk_ids.data_ptr(), topk_weights.data_ptr(), _ptr(logits_out), _ptr(ws),
+            0 if ws is None else ws.numel(), on.stream)
+    _raise("moe_route_scored", st)
+    return topk_ids, topk_weights
+
+
+def _layer_scored(call: str, x, w_router, routing: Routing, weights, weight_args, I: int, ws_size,
+                  logit_bias, out, topk_ids_out, topk_weights_out, ws, stream):
+    """A layer call with a routing rule: ``weights`` are (name, tensor, dtype
+    or None for int32/uint32 words, shape) to check, ``weight_args`` what the C call
+    takes for them."""
+    torch = _torch()
+    M, H = x.shape
+    E = w_router.shape[0]
+    k = routing.top_k
+    dev = _device_of(x, "x")
+    _need(x, "x", torch.bfloat16, (M, H), dev)
+    _need(w_router, "w_router", torch.bfloat16, (E, H), dev)
+    for name, t, dtype, shape in weights:
+        _need(t, name, t.dtype if dtype is None and t.dtype in _words() else dtype or torch.int32,
+              shape, dev)
+    if logit_bias is not None:
+        _need(logit_bias, "logit_bias", torch.float32, (E,), dev)
+    rule = routing._arg(E, dev)
+    with _On(dev, stream) as on:
+        if out is None:
+            out = on.empty((M, H), torch.bfloat16)
+        _need(out, "out", torch.bfloat16, (M, H), dev)
+        if topk_ids_out is not None:
+            _need(topk_ids_out, "topk_ids_out", torch.int32, (M, k), dev)
+        if topk_weights_out is not None:
+            _need(topk_weights_out, "topk_weights_out", torch.float32, (M, k), dev)
+        if ws is None:
+            n = ws_size(M, E, k, H, I)
+            if n == 0:
+                raise MoeError(call, -2)
+            ws = on.empty((n,), torch.uint8)
+        _need(ws, "ws", torch.uint8, (ws.numel(),), dev)
+        info = DispatchInfo()
+        st = getattr(library(), call)(
+            x.data_ptr(), w_router.data_ptr(), _ptr(logit_bias), rule, *weight_args, M, E, H, I,
+            out.data_ptr(), _ptr(topk_ids_out), _ptr(topk_weights_out), ws.data_ptr(), ws.numel(),
+            ctypes.byref(info), on.stream)
+    _raise(call, st)
+    return out, info.as_dict()
+
+
+def _words():
+    torch = _torch()
+    return (torch.int32, getattr(torch, "uint32", torch.int32))
+
+
+def moe_forward_scored(x, w_router, w13, w2, routing: Routing, logit_bias=None, out=None,
+                       topk_ids_out=None, topk_weights_out=None, ws=None, stream=None):
+    """moe_forward with a routing rule.  Returns (out [M, H] bf16, dispatch
+    info dict)."""
+    bf16 = _torch().bfloat16
+    E, H = w_router.shape
+    I = w2.shape[2]
+    return _layer_scored(
+        "moe_forward_scored", x, w_router, routing,
+        (("w13", w13, bf16, (E, 2 * I, H)), ("w2", w2, bf16, (E, H, I))),
+        (w13.data_ptr(), w2.data_ptr()), I, moe_workspace_size, logit_bias, out, topk_ids_out,
+        topk_weights_out, ws, stream)
+
+
+def moe_forward_quantized_scored(x, w_router, qweights: dict, routing: Routing, logit_bias=None,
+                                 out=None, topk_ids_out=None, topk_weights_out=None, ws=None,
+                                 stream=None):
+    """moe_forward_quantized with a routing rule; ``qweights`` as there."""
+    bf16 = _torch().bfloat16
+    E, H = w_router.shape
+    bits = int(qweights["bits"])
+    if bits not in (4, 8):
+        raise MoeError("moe_forward_quantized_scored", -2)
+    I = qweights["w2_q"].shape[2] * 32 // bits
+    names = ("w13_q", "w13_scales", "w13_biases", "w2_q", "w2_scales", "w2_biases")
+    shapes = ((E, 2 * I, H * bits // 32), (E, 2 * I, H // 64), (E, 2 * I, H // 64),
+              (E, H, I * bits // 32), (E, H, I // 64), (E, H, I // 64))
+    qw = QuantizedWeights(bits, int(qweights.get("group_size", 64)),
+                          *(qweights[n].data_ptr() for n in names))
+    return _layer_scored(
+        "moe_forward_quantized_scored", x, w_router, routing,
+        tuple((n, qweights[n], None if n.endswith("_q") else bf16, s)
+              for n, s in zip(names, shapes)),
+        (ctypes.byref(qw),), I, moe_workspace_size, logit_bias, out, topk_ids_out,
+        topk_weights_out, ws, stream)
+
+
+def moe_forward_mxfp8_scored(x, w_router, mxw: dict, routing: Routing, logit_bias=None, out=None,
+                             topk_ids_out=None, topk_weights_out=None, ws=None, stream=None):
+    """moe_forward_mxfp8 with a routing rule; ``mxw`` as there."""
+    u8 = _torch().uint8
+    E, H = w_router.shape
+    I = mxw["w2_codes"].shape[2]
+    names = ("w13_codes", "w13_scales", "w2_codes", "w2_scales")
+    shapes = ((E, 2 * I, H), (E, 2 * I, H // 32), (E, H, I), (E, H, I // 32))
+    w = MxWeights(*(mxw[n].data_ptr() for n in names))
+    return _layer_scored(
+        "moe_forward_mxfp8_scored", x, w_router, routing,
+        tuple((n, mxw[n], u8, s) for n, s in zip(names, shapes)), (ctypes.byref(w),), I,
+        moe_mx_workspace_size, logit_bias, out, topk_ids_out, topk_weights_out, ws, stream)
+
+
+def moe_linear_quantized(x, weight: dict, gated: bool = False, row_scale=None, addend=None,
+                         out=None, stream=None):
+    """out [M, n_out] bf16 = addend + row_scale * f(x W^T) for one dense
+    matrix with 4-bit affine weights: ``weight`` holds ``bits`` (4),
+    ``group_size`` (32, 64 or 128; default 64), ``q`` [N, K/8] (int32 or
+    uint32 words of packed codes), ``scales`` and ``biases``
+    [N, K/group_size] (bf16).  ``gated``: the first N/2 rows are gates and
+    f = SiLU(gate) * up, n_out = N/2; else f is the identity, n_out = N.
+    ``row_scale`` [M] fp32 and ``addend`` [M, n_out] bf16 (``out`` itself, to
+    add in place) are optional."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    M, K = x.shape
+    q, scales, biases = weight["q"], weight["scales"], weight["biases"]
+    bits, group = int(weight["bits"]), int(weight.get("group_size", 64))
+    if bits != 4 or group not in (32, 64, 128) or K % group != 0:
+        raise MoeError("moe_linear_quantized", -2)
+    N = q.shape[0]
+    n_out = N // 2 if gated else N
+    dev = _device_of(x, "x")
+    _need(x, "x", bf16, (M, K), dev)
+    _need(q, "q", q.dtype if q.dtype in _words() else torch.int32, (N, K // 8), dev)
+    _need(scales, "scales", bf16, (N, K // group), dev)
+    _need(biases, "biases", bf16, (N, K // group), dev)
+    if row_scale is not None:
+        _need(row_scale, "row_scale", torch.float32, (M,), dev)
+    if addend is not None:
+        _need(addend, "addend", bf16, (M, n_out), dev)
+    w = QuantizedMatrix(bits, group, q.data_ptr(), scales.data_ptr(), biases.data_ptr())
+    with _On(dev, stream) as on:
+        if out is None:
+            out = on.empty((M, n_out), bf16)
+        _need(out, "out", bf16, (M, n_out), dev)
+        st = library().moe_linear_quantized(x.data_ptr(), ctypes.addressof(w), M, N, K,
+                                            int(bool(gated)), _ptr(row_scale), _ptr(addend),
+                                            out.data_ptr(), on.stream)
+    _raise("moe_linear_quantized", st)
+    return out

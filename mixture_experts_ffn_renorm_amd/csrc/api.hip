@@ -2,6 +2,7 @@
 // kernel choice and launches.  Declarations and the contract of every call
 // are in include/moe_mi355x.h.
 #include <algorithm>
+#include <cmath>
 
 #include "moe_common.h"
 #include "moe_mi355x.h"
@@ -12,6 +13,7 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr long long kMaxPairs = 1LL << 24;
+constexpr int kMaxGroups = 64;   // expert groups of a routing rule
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
@@ -116,6 +118,62 @@ void fill_info(moe_dispatch_info* info, int B, int H, int I, int launches, int s
   do {                                               \
     if ((expr) != hipSuccess) return MOE_ERR_HIP;    \
   } while (0)
+
+// A routing rule for a layer of E experts.
+int check_routing(const moe_routing* r, int E) {
+  if (r == nullptr) return MOE_ERR_INVALID_ARG;
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (r->renormalize != 0 && r->renormalize != 1) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(r->scale)) return MOE_ERR_INVALID_ARG;
+  const int G = r->n_group;
+  if (G <= 0 || E % G != 0 || r->topk_group <= 0 || r->topk_group > G) return MOE_ERR_INVALID_ARG;
+  if (r->group_top != 1 && r->group_top != 2) return MOE_ERR_INVALID_ARG;
+  if (G > 1 && r->group_top > E / G) return MOE_ERR_INVALID_ARG;
+  // the groups that stay have to hold top_k experts
+  if ((long long)r->topk_group * (E / G) < r->top_k) return MOE_ERR_INVALID_ARG;
+  if (G > kMaxGroups) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+SelectArgs select_args(const moe_routing& r, const float* logits, int M, int E,
+                       int32_t* topk_ids, float* topk_weights) {
+  return SelectArgs{logits, r.select_bias, M, E, r.top_k, r.score == MOE_SCORE_SIGMOID ? 1 : 0,
+                    r.renormalize, r.n_group, r.topk_group, r.group_top, r.scale, topk_ids,
+                    topk_weights};
+}
+
+// The softmax rule of the calls that take top_k and renormalize (null: a
+// moe_routing rule is given instead).
+struct Rule {
+  int top_k, renormalize;
+  const moe_routing* scored;   // null: softmax, top_k, renormalize
+};
+
+int check_rule(const Rule& u, int E) {
+  if (u.scored != nullptr) return check_routing(u.scored, E);
+  return u.renormalize == 0 || u.renormalize == 1 ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
+// Small batches under the softmax rule run the top-k and the index lists in
+// one launch; a scored rule always selects in a launch of its own.
+bool rule_fused(const Rule& u, int M) { return u.scored == nullptr && fused_route(M, u.top_k); }
+
+// Launches from the router logits to the index lists.
+int rule_launches(const Rule& u, int M) {
+  return rule_fused(u, M) ? 2 : 2 + (align_segments(M * u.top_k) > 1 ? 2 : 1);
+}
+
+// Ids and weights from ra.logits, and the MXFP8 copy of x where ra asks for
+// one (the softmax top-k writes it in its own launch).
+hipError_t launch_rule_topk(const Rule& u, const RouteArgs& ra, hipStream_t s) {
+  if (u.scored == nullptr) return launch_route_topk(ra, s);
+  if (ra.qx_codes != nullptr) {
+    const hipError_t e = launch_mx_quantize(ra.x, ra.M, ra.H, ra.qx_codes, ra.qx_scales, s);
+    if (e != hipSuccess) return e;
+  }
+  return launch_select(select_args(*u.scored, ra.logits, ra.M, ra.E, ra.topk_ids, ra.topk_weights),
+                       s);
+}
 
 GemmArgs gemm_args(int M, int top_k, int E, int H, int I, int B) {
   GemmArgs g{};
@@ -339,15 +397,21 @@ int moe_grouped_gemm_w2_combine(const uint16_t* act, const uint16_t* w2,
   return run_gemm2(g, s);
 }
 
-int moe_forward(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
-                const uint16_t* w13, const uint16_t* w2, int M, int E, int top_k, int H, int I,
-                int renormalize, uint16_t* out, int32_t* topk_ids_out, float* topk_weights_out,
-                void* workspace, size_t ws_bytes, moe_dispatch_info* info, void* stream) {
+}  // extern "C"
+
+namespace {
+
+int forward_rule(const uint16_t* x, const uint16_t* w_router, const float* logit_bias, const
+                 uint16_t* w13, const uint16_t* w2, int M, int E, const Rule& rule, int H, int I,
+                 uint16_t* out, int32_t* topk_ids_out, float* topk_weights_out, void* workspace,
+                 size_t ws_bytes, moe_dispatch_info* info, void* stream) {
+  const int top_k = rule.top_k;
   int st = check_sizes(M, E, top_k, H, I);
   if (st != MOE_OK) return st;
-  if (renormalize != 0 && renormalize != 1) return MOE_ERR_INVALID_ARG;
+  st = check_rule(rule, E);
+  if (st != MOE_OK) return st;
   const int B = moe_pick_block_m(M, E, top_k);
-  const int route_launches = fused_route(M, top_k) ? 2 : 2 + (align_segments(M * top_k) > 1 ? 2 : 1);
+  const int route_launches = rule_launches(rule, M);
   const bool per_pair = B == 1;
   if (per_pair)
     fill_info(info, B, H, I, kPairGemvForwardLaunches, 0);
@@ -369,7 +433,7 @@ int moe_forward(const uint16_t* x, const uint16_t* w_router, const float* logit_
   uint16_t* act = reinterpret_cast<uint16_t*>(ws + L.act);
 
   // the router-logits kernel clears the arrival counter
-  RouteArgs ra{x, w_router, logit_bias, M, H, E, top_k, renormalize,
+  RouteArgs ra{x, w_router, logit_bias, M, H, E, top_k, rule.renormalize,
                reinterpret_cast<float*>(ws + L.logits), ids, wts,
                reinterpret_cast<float*>(ws + L.arrive), 1};
   AlignArgs aa{ids, M * top_k, E, B, sorted, eids, boff,
@@ -378,15 +442,15 @@ int moe_forward(const uint16_t* x, const uint16_t* w_router, const float* logit_
   MOE_TRY_HIP(launch_route_logits(ra, s));
   if (per_pair) {
     PairGemvArgs pg{x, w13, w2, ids, wts, M, top_k, H, I, act, out, nullptr, nullptr, nullptr};
-    MOE_TRY_HIP(launch_route_topk(ra, s));
+    MOE_TRY_HIP(launch_rule_topk(rule, ra, s));
     MOE_TRY_HIP(launch_pair_gemv1(pg, s));
     MOE_TRY_HIP(launch_pair_gemv2(pg, s));
     return MOE_OK;
   }
-  if (fused_route(M, top_k)) {
+  if (rule_fused(rule, M)) {
     MOE_TRY_HIP(launch_route_topk_align(ra, aa, reinterpret_cast<int32_t*>(ws + L.arrive), s));
   } else {
-    MOE_TRY_HIP(launch_route_topk(ra, s));
+    MOE_TRY_HIP(launch_rule_topk(rule, ra, s));
     MOE_TRY_HIP(launch_align(aa, s));
   }
   GemmArgs g = gemm_args(M, top_k, E, H, I, B);
@@ -406,14 +470,16 @@ int moe_forward(const uint16_t* x, const uint16_t* w_router, const float* logit_
   return run_gemm2(g, s);
 }
 
-int moe_forward_quantized(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
-                          const moe_quantized_weights* qw, int M, int E, int top_k, int H, int I,
-                          int renormalize, uint16_t* out, int32_t* topk_ids_out,
-                          float* topk_weights_out, void* workspace, size_t ws_bytes,
-                          moe_dispatch_info* info, void* stream) {
+int forward_quantized_rule(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
+                           const moe_quantized_weights* qw, int M, int E, const Rule& rule, int H,
+                           int I, uint16_t* out, int32_t* topk_ids_out, float* topk_weights_out,
+                           void* workspace, size_t ws_bytes, moe_dispatch_info* info, void* stream)
+                           {
+  const int top_k = rule.top_k;
   int st = check_sizes(M, E, top_k, H, I);
   if (st != MOE_OK) return st;
-  if (renormalize != 0 && renormalize != 1) return MOE_ERR_INVALID_ARG;
+  st = check_rule(rule, E);
+  if (st != MOE_OK) return st;
   if (qw == nullptr) return MOE_ERR_INVALID_ARG;
   if ((qw->bits != 4 && qw->bits != 8) || qw->group_size != 64) return MOE_ERR_UNSUPPORTED;
   if (H % 64 != 0 || I % 64 != 0) return MOE_ERR_UNSUPPORTED;
@@ -432,7 +498,7 @@ int moe_forward_quantized(const uint16_t* x, const uint16_t* w_router, const flo
     else if (qgemm_stream_shapes_ok(H, I)) B = 16;
   }
   const bool per_pair = B == 1;
-  const int route_launches = fused_route(M, top_k) ? 2 : 2 + (align_segments(M * top_k) > 1 ? 2 : 1);
+  const int route_launches = rule_launches(rule, M);
   if (per_pair) {
     fill_info(info, 1, H, I, M == 0 ? 0 : kPairGemvForwardLaunches, 0);
     if (info != nullptr) info->variant = MOE_VARIANT_PAIR_GEMV_QUANT;
@@ -459,14 +525,14 @@ int moe_forward_quantized(const uint16_t* x, const uint16_t* w_router, const flo
   int32_t* ids = topk_ids_out ? topk_ids_out : reinterpret_cast<int32_t*>(ws + L.ids);
   float* wts = topk_weights_out ? topk_weights_out : reinterpret_cast<float*>(ws + L.wts);
   uint16_t* act = reinterpret_cast<uint16_t*>(ws + L.act);
-  RouteArgs ra{x, w_router, logit_bias, M, H, E, top_k, renormalize,
+  RouteArgs ra{x, w_router, logit_bias, M, H, E, top_k, rule.renormalize,
                reinterpret_cast<float*>(ws + L.logits), ids, wts,
                per_pair ? nullptr : reinterpret_cast<float*>(ws + L.arrive), per_pair ? 0u : 1u};
   MOE_TRY_HIP(launch_route_logits(ra, s));
   if (per_pair) {
     QPairGemvArgs q{x, qw->w13_q, qw->w13_scales, qw->w13_biases, qw->w2_q, qw->w2_scales,
                     qw->w2_biases, ids, wts, M, top_k, H, I, qw->bits, act, out};
-    MOE_TRY_HIP(launch_route_topk(ra, s));
+    MOE_TRY_HIP(launch_rule_topk(rule, ra, s));
     MOE_TRY_HIP(launch_qpair_gemv1(q, s));
     MOE_TRY_HIP(launch_qpair_gemv2(q, s));
     return MOE_OK;
@@ -477,10 +543,10 @@ int moe_forward_quantized(const uint16_t* x, const uint16_t* w_router, const flo
   AlignArgs aa{ids, M * top_k, E, B, sorted, eids, boff,
                reinterpret_cast<int32_t*>(ws + L.counts),
                reinterpret_cast<int32_t*>(ws + L.align_scratch)};
-  if (fused_route(M, top_k)) {
+  if (rule_fused(rule, M)) {
     MOE_TRY_HIP(launch_route_topk_align(ra, aa, reinterpret_cast<int32_t*>(ws + L.arrive), s));
   } else {
-    MOE_TRY_HIP(launch_route_topk(ra, s));
+    MOE_TRY_HIP(launch_rule_topk(rule, ra, s));
     MOE_TRY_HIP(launch_align(aa, s));
   }
   QGemmArgs g{x, qw->w13_q, qw->w13_scales, qw->w13_biases, qw->w2_q, qw->w2_scales,
@@ -494,6 +560,128 @@ int moe_forward_quantized(const uint16_t* x, const uint16_t* w_router, const flo
     MOE_TRY_HIP(launch_qgemm1_tiled(g, s));
     MOE_TRY_HIP(launch_qgemm2_tiled(g, s));
   }
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_forward(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
+                const uint16_t* w13, const uint16_t* w2, int M, int E, int top_k, int H, int I,
+                int renormalize, uint16_t* out, int32_t* topk_ids_out, float* topk_weights_out,
+                void* workspace, size_t ws_bytes, moe_dispatch_info* info, void* stream) {
+  return forward_rule(x, w_router, logit_bias, w13, w2, M, E, Rule{top_k, renormalize, nullptr}, H,
+                      I, out, topk_ids_out, topk_weights_out, workspace, ws_bytes, info, stream);
+}
+
+int moe_forward_scored(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
+                       const moe_routing* routing, const uint16_t* w13, const uint16_t* w2, int M,
+                       int E, int H, int I, uint16_t* out, int32_t* topk_ids_out,
+                       float* topk_weights_out, void* workspace, size_t ws_bytes,
+                       moe_dispatch_info* info, void* stream) {
+  if (routing == nullptr) return MOE_ERR_INVALID_ARG;
+  return forward_rule(x, w_router, logit_bias, w13, w2, M, E, Rule{routing->top_k, 0, routing}, H,
+                      I, out, topk_ids_out, topk_weights_out, workspace, ws_bytes, info, stream);
+}
+
+int moe_forward_quantized(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
+                          const moe_quantized_weights* qw, int M, int E, int top_k, int H, int I,
+                          int renormalize, uint16_t* out, int32_t* topk_ids_out,
+                          float* topk_weights_out, void* workspace, size_t ws_bytes,
+                          moe_dispatch_info* info, void* stream) {
+  return forward_quantized_rule(x, w_router, logit_bias, qw, M, E,
+                                Rule{top_k, renormalize, nullptr}, H, I, out, topk_ids_out,
+                                topk_weights_out, workspace, ws_bytes, info, stream);
+}
+
+int moe_forward_quantized_scored(const uint16_t* x, const uint16_t* w_router,
+                                 const float* logit_bias, const moe_routing* routing,
+                                 const moe_quantized_weights* qw, int M, int E, int H, int I,
+                                 uint16_t* out, int32_t* topk_ids_out, float* topk_weights_out,
+                                 void* workspace, size_t ws_bytes, moe_dispatch_info* info,
+                                 void* stream) {
+  if (routing == nullptr) return MOE_ERR_INVALID_ARG;
+  return forward_quantized_rule(x, w_router, logit_bias, qw, M, E,
+                                Rule{routing->top_k, 0, routing}, H, I, out, topk_ids_out,
+                                topk_weights_out, workspace, ws_bytes, info, stream);
+}
+
+int moe_select(const float* logits, const moe_routing* routing, int M, int E, int32_t* topk_ids,
+               float* topk_weights, void* stream) {
+  if (routing == nullptr) return MOE_ERR_INVALID_ARG;
+  int st = check_sizes(M, E, routing->top_k, 8, 8);
+  if (st != MOE_OK) return st;
+  st = check_routing(routing, E);
+  if (st != MOE_OK) return st;
+  if (M == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_weights) return MOE_ERR_INVALID_ARG;
+  if (!a16(logits)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY_HIP(launch_select(select_args(*routing, logits, M, E, topk_ids, topk_weights),
+                            static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+int moe_select_backward(const float* logits, const int32_t* topk_ids, const float* grad_weights,
+                        const moe_routing* routing, int M, int E, float* grad_logits,
+                        void* stream) {
+  if (routing == nullptr) return MOE_ERR_INVALID_ARG;
+  int st = check_sizes(M, E, routing->top_k, 8, 8);
+  if (st != MOE_OK) return st;
+  st = check_routing(routing, E);
+  if (st != MOE_OK) return st;
+  if (M == 0) return MOE_OK;
+  if (!logits || !topk_ids || !grad_weights || !grad_logits) return MOE_ERR_INVALID_ARG;
+  if (grad_logits == logits) return MOE_ERR_INVALID_ARG;
+  if (!a16(logits) || !a16(grad_logits)) return MOE_ERR_INVALID_ARG;
+  SelectArgs a = select_args(*routing, logits, M, E, const_cast<int32_t*>(topk_ids), nullptr);
+  MOE_TRY_HIP(launch_select_backward(a, grad_weights, grad_logits,
+                                     static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+int moe_route_scored(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
+                     const moe_routing* routing, int M, int H, int E, int32_t* topk_ids,
+                     float* topk_weights, float* logits_out, void* workspace, size_t ws_bytes,
+                     void* stream) {
+  if (routing == nullptr) return MOE_ERR_INVALID_ARG;
+  int st = check_sizes(M, E, routing->top_k, H, 8);
+  if (st != MOE_OK) return st;
+  st = check_routing(routing, E);
+  if (st != MOE_OK) return st;
+  if (M == 0) return MOE_OK;
+  if (!x || !w_router || !topk_ids || !topk_weights) return MOE_ERR_INVALID_ARG;
+  if (!a16(x) || !a16(w_router) || !a16(logits_out) || !a16(workspace))
+    return MOE_ERR_INVALID_ARG;
+  float* logits = logits_out;
+  if (logits == nullptr) {
+    if (workspace == nullptr || ws_bytes < (size_t)M * E * 4) return MOE_ERR_WORKSPACE;
+    logits = static_cast<float*>(workspace);
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  RouteArgs a{x, w_router, logit_bias, M, H, E, routing->top_k, 0, logits, topk_ids,
+              topk_weights, nullptr, 0};
+  MOE_TRY_HIP(launch_route_logits(a, s));
+  MOE_TRY_HIP(launch_select(select_args(*routing, logits, M, E, topk_ids, topk_weights), s));
+  return MOE_OK;
+}
+
+int moe_linear_quantized(const uint16_t* x, const moe_quantized_matrix* w, int M, int N, int K,
+                         int gated, const float* row_scale, const uint16_t* addend, uint16_t* out,
+                         void* stream) {
+  if (w == nullptr || M < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (gated != 0 && gated != 1) return MOE_ERR_INVALID_ARG;
+  if (gated && N % 2 != 0) return MOE_ERR_INVALID_ARG;
+  const int g = w->group_size;
+  if (w->bits != 4 || (g != 32 && g != 64 && g != 128)) return MOE_ERR_UNSUPPORTED;
+  if (K % g != 0) return MOE_ERR_UNSUPPORTED;
+  if (M >= kMaxPairs || N >= kMaxPairs || K >= kMaxPairs) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!x || !w->q || !w->scales || !w->biases || !out) return MOE_ERR_INVALID_ARG;
+  if (!a16(x) || !a16(w->q) || !a16(w->scales) || !a16(w->biases) || !a16(out) || !a16(addend))
+    return MOE_ERR_INVALID_ARG;
+  QLinearArgs a{x, w->q, w->scales, w->biases, M, N, K, g, gated, row_scale, addend, out};
+  MOE_TRY_HIP(launch_qlinear(a, static_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
 
@@ -552,27 +740,35 @@ size_t moe_mx_workspace_size(int M_max, int E, int top_k, int H, int I) {
   return std::max<size_t>(best, kAlign);
 }
 
-int moe_forward_mxfp8(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
-                      const moe_mx_weights* w, int M, int E, int top_k, int H, int I,
-                      int renormalize, uint16_t* out, int32_t* topk_ids_out,
-                      float* topk_weights_out, void* workspace, size_t ws_bytes,
-                      moe_dispatch_info* info, void* stream) {
+}  // extern "C"
+
+namespace {
+
+int forward_mxfp8_rule(const uint16_t* x, const uint16_t* w_router, const float* logit_bias, const
+                       moe_mx_weights* w, int M, int E, const Rule& rule, int H, int I, uint16_t*
+                       out, int32_t* topk_ids_out, float* topk_weights_out, void* workspace, size_t
+                       ws_bytes, moe_dispatch_info* info, void* stream) {
+  const int top_k = rule.top_k;
   int st = check_sizes(M, E, top_k, H, I);
   if (st != MOE_OK) return st;
-  if (renormalize != 0 && renormalize != 1) return MOE_ERR_INVALID_ARG;
+  st = check_rule(rule, E);
+  if (st != MOE_OK) return st;
   if (w == nullptr) return MOE_ERR_INVALID_ARG;
   if (!mx_sizes_ok(H, I)) return MOE_ERR_UNSUPPORTED;
   const int B = mx_block_m(M, E, top_k);
   const bool per_pair = B == 1;
-  const int route_launches = fused_route(M, top_k) ? 2 : 2 + (align_segments(M * top_k) > 1 ? 2 : 1);
+  // a scored rule's selection leaves the copy of x to a launch of its own
+  const int quantize_launches = rule.scored != nullptr ? 1 : 0;
+  const int route_launches = rule_launches(rule, M);
   if (per_pair) {
     // router logits, top-k (+ x quantized), GEMV 1, GEMV 2 with the sum
-    fill_info(info, B, H, I, M == 0 ? 0 : kPairGemvForwardLaunches, 0);
+    fill_info(info, B, H, I, M == 0 ? 0 : kPairGemvForwardLaunches + quantize_launches, 0);
     if (info != nullptr) info->variant = MOE_VARIANT_PAIR_GEMV_MXFP8;
   } else {
     // GEMM 1, quantize act (in GEMM 1's epilogue at block_m 16), then GEMM 2
     // and its per-token sum (x is quantized by the top-k launch)
-    fill_info(info, B, H, I, M == 0 ? 0 : route_launches + (B == 16 ? 1 : 2) + kGemm2Launches);
+    fill_info(info, B, H, I, M == 0 ? 0 : route_launches + quantize_launches + (B == 16 ? 1 : 2) +
+                                                    kGemm2Launches);
     if (info != nullptr)
       info->variant = B == 16 ? MOE_VARIANT_STREAM_MXFP8 : MOE_VARIANT_TILED_MXFP8;
   }
@@ -599,7 +795,7 @@ int moe_forward_mxfp8(const uint16_t* x, const uint16_t* w_router, const float* 
   uint8_t* qact = reinterpret_cast<uint8_t*>(ws + X.qact);
   uint8_t* sact = reinterpret_cast<uint8_t*>(ws + X.sact);
 
-  RouteArgs ra{x, w_router, logit_bias, M, H, E, top_k, renormalize,
+  RouteArgs ra{x, w_router, logit_bias, M, H, E, top_k, rule.renormalize,
                reinterpret_cast<float*>(ws + L.logits), ids, wts,
                reinterpret_cast<float*>(ws + L.arrive), 1};
   AlignArgs aa{ids, M * top_k, E, B, sorted, eids, boff,
@@ -611,7 +807,7 @@ int moe_forward_mxfp8(const uint16_t* x, const uint16_t* w_router, const float* 
     // each pair runs as its own GEMV against its expert's MXFP8 rows.
     ra.qx_codes = qx;
     ra.qx_scales = sx;
-    MOE_TRY_HIP(launch_route_topk(ra, s));
+    MOE_TRY_HIP(launch_rule_topk(rule, ra, s));
     MxPairGemvArgs pg{qx, sx, w->w13_codes, w->w13_scales, w->w2_codes, w->w2_scales, ids, wts,
                       M, top_k, H, I, act, out};
     MOE_TRY_HIP(launch_mx_pair_gemv1(pg, s));
@@ -621,10 +817,10 @@ int moe_forward_mxfp8(const uint16_t* x, const uint16_t* w_router, const float* 
   // the top-k launch also quantizes x
   ra.qx_codes = qx;
   ra.qx_scales = sx;
-  if (fused_route(M, top_k)) {
+  if (rule_fused(rule, M)) {
     MOE_TRY_HIP(launch_route_topk_align(ra, aa, reinterpret_cast<int32_t*>(ws + L.arrive), s));
   } else {
-    MOE_TRY_HIP(launch_route_topk(ra, s));
+    MOE_TRY_HIP(launch_rule_topk(rule, ra, s));
     MOE_TRY_HIP(launch_align(aa, s));
   }
   GemmArgs g = gemm_args(M, top_k, E, H, I, B);
@@ -653,6 +849,32 @@ int moe_forward_mxfp8(const uint16_t* x, const uint16_t* w_router, const float* 
   g.partial = reinterpret_cast<float*>(ws + L.partial);
   MOE_TRY_HIP(B == 16 ? launch_gemm2_stream(g, s) : launch_gemm2_tiled(g, s));
   return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_forward_mxfp8(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
+                          const moe_mx_weights* w, int M, int E, int top_k, int H, int I,
+                          int renormalize, uint16_t* out, int32_t* topk_ids_out,
+                          float* topk_weights_out, void* workspace, size_t ws_bytes,
+                          moe_dispatch_info* info, void* stream) {
+  return forward_mxfp8_rule(x, w_router, logit_bias, w, M, E,
+                                Rule{top_k, renormalize, nullptr}, H, I, out, topk_ids_out,
+                                topk_weights_out, workspace, ws_bytes, info, stream);
+}
+
+int moe_forward_mxfp8_scored(const uint16_t* x, const uint16_t* w_router,
+                                 const float* logit_bias, const moe_routing* routing,
+                                 const moe_mx_weights* w, int M, int E, int H, int I,
+                                 uint16_t* out, int32_t* topk_ids_out, float* topk_weights_out,
+                                 void* workspace, size_t ws_bytes, moe_dispatch_info* info,
+                                 void* stream) {
+  if (routing == nullptr) return MOE_ERR_INVALID_ARG;
+  return forward_mxfp8_rule(x, w_router, logit_bias, w, M, E,
+                                Rule{routing->top_k, 0, routing}, H, I, out, topk_ids_out,
+                                topk_weights_out, workspace, ws_bytes, info, stream);
 }
 
 }  // extern "C"

@@ -569,6 +569,35 @@ struct RouteArgs {
 hipError_t launch_route_logits(const RouteArgs& a, hipStream_t s);
 hipError_t launch_route_topk(const RouteArgs& a, hipStream_t s);
 
+// Scored routing (moe_select and its gradient): the fields of a moe_routing
+// rule, checked by the C ABI.
+struct SelectArgs {
+  const float* logits;       // [M, E]
+  const float* select_bias;  // [E] or null
+  int M, E, top_k, sigmoid, renormalize, n_group, topk_group, group_top;
+  float scale;
+  int32_t* topk_ids;         // [M, top_k] (read by the gradient)
+  float* topk_weights;       // [M, top_k]
+};
+hipError_t launch_select(const SelectArgs& a, hipStream_t s);
+hipError_t launch_select_backward(const SelectArgs& a, const float* grad_weights,
+                                  float* grad_logits, hipStream_t s);
+
+// Dense product with 4-bit affine weights: out = addend + row_scale * f(x W^T),
+// f = identity, or SiLU(first half of the rows) * second half.
+struct QLinearArgs {
+  const uint16_t* x;         // [M, K]
+  const uint32_t* q;         // [N, K / 8]
+  const uint16_t* scales;    // [N, K / group]
+  const uint16_t* biases;    // [N, K / group]
+  int M, N, K, group;        // group 32, 64 or 128; K % group == 0
+  int gated;                 // N even; out has N / 2 columns
+  const float* row_scale;    // [M] or null
+  const uint16_t* addend;    // [M, n_out] or null; may be out
+  uint16_t* out;             // [M, n_out]
+};
+hipError_t launch_qlinear(const QLinearArgs& a, hipStream_t s);
+
 struct AlignArgs {
   const int32_t* topk_ids;
   int P, E, block_m;

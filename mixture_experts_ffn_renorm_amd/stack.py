@@ -18,20 +18,23 @@ l + 1).  A step can be recorded once into a HIP graph
 (``torch.cuda.CUDAGraph``) and replayed, which removes the host's per-launch
 cost.
 
-Orchestration only: every layer is one ``moe_forward`` call of the C ABI.
+Orchestration only: every layer is one ``moe_forward`` call of the C ABI, or
+one ``moe_forward_scored`` call where the layer brings a routing rule.
 """
 
 from __future__ import annotations
 
 from typing import Sequence
 
-from . import moe_forward, workspace
+from . import moe_forward, moe_forward_scored, workspace
 
 
 class MoEStack:
     """``layers``: sequence of dicts with device tensors ``w_router`` [E, H],
     ``w13`` [E, 2I, H], ``w2`` [E, H, I] (bf16) and ``logit_bias`` ([E] fp32
-    or None), all of one shape.  ``M_max``: the largest batch a step takes."""
+    or None), all of one shape, and optionally ``routing`` (a ``Routing`` rule
+    with this ``top_k``, in the place of ``top_k`` and ``renormalize``).
+    ``M_max``: the largest batch a step takes."""
 
     def __init__(self, layers: Sequence[dict], top_k: int, M_max: int,
                  renormalize: bool = True, residual: bool = True, device=None):
@@ -45,6 +48,8 @@ class MoEStack:
                     tuple(lay["w2"].shape) != (E, H, two_i // 2) or \
                     tuple(lay["w_router"].shape) != (E, H):
                 raise ValueError("every layer of a stack must have the same shape")
+            if lay.get("routing") is not None and lay["routing"].top_k != top_k:
+                raise ValueError("every layer's routing rule must have the stack's top_k")
         self.layers = list(layers)
         self.top_k, self.M_max, self.renormalize = top_k, M_max, renormalize
         self.residual = residual
@@ -85,11 +90,15 @@ class MoEStack:
             src = x
         for l, lay in enumerate(self.layers):
             dst = y if self.residual else self.bufs[l % 2][:M]
-            _, info = moe_forward(src, lay["w_router"], lay["w13"], lay["w2"], self.top_k,
-                                  self.renormalize, logit_bias=lay.get("logit_bias"), out=dst,
-                                  topk_ids_out=self.topk_ids[l][:M],
-                                  topk_weights_out=self.topk_weights[l][:M], ws=self.ws,
-                                  stream=stream)
+            buffers = dict(logit_bias=lay.get("logit_bias"), out=dst,
+                           topk_ids_out=self.topk_ids[l][:M],
+                           topk_weights_out=self.topk_weights[l][:M], ws=self.ws, stream=stream)
+            if lay.get("routing") is not None:
+                _, info = moe_forward_scored(src, lay["w_router"], lay["w13"], lay["w2"],
+                                             lay["routing"], **buffers)
+            else:
+                _, info = moe_forward(src, lay["w_router"], lay["w13"], lay["w2"], self.top_k,
+                                      self.renormalize, **buffers)
             launches += info["launches"]
             infos.append(info)
             if self.residual:

@@ -492,3 +492,114 @@ def mx_layer_forward(layer: dict, topk_ids: np.ndarray, topk_weights: np.ndarray
         slots[pos[ts], js] = mx_dequantize(aq, asc) @ W2.T
     y = np.einsum("tk,tkh->th", np.asarray(topk_weights, dtype=np.float64)[tokens], slots)
     return y, xq, xs
+
+
+# ---------------------------------------------------------------------------
+# scored routing (softmax or sigmoid scores, a choice bias, expert groups)
+# and its gradient; dense products with affine group weights
+# ---------------------------------------------------------------------------
+
+def log_scores(logits: np.ndarray, score: str) -> np.ndarray:
+    """Logarithms of the scores, float64; a softmax row of -inf alone scores
+    zero everywhere."""
+    l = np.asarray(logits, dtype=np.float64)
+    if score == "sigmoid":
+        return -np.logaddexp(0.0, -l)
+    m = l.max(axis=1, keepdims=True)
+    shifted = l - np.where(np.isneginf(m), 0.0, m)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        out = shifted - np.log(np.exp(shifted).sum(axis=1, keepdims=True))
+    return np.where(np.isneginf(m), -np.inf, out)
+
+
+def _descending(values) -> list:
+    """Positions by descending value, NaN last, equal values in order."""
+    key = [(-np.inf, 1) if np.isnan(v) else (v, 0) for v in values]
+    return sorted(range(len(key)), key=lambda i: (key[i][1], -key[i][0], i))
+
+
+def select_ids(logits: np.ndarray, top_k: int, score: str, select_bias=None, n_group: int = 1,
+               topk_group: int = 1, group_top: int = 1) -> np.ndarray:
+    """The choice, one token at a time: int32 [M, top_k]."""
+    l = np.asarray(logits, dtype=np.float32).astype(np.float64)
+    M, E = l.shape
+    s = np.exp(log_scores(l, score))
+    c = s if select_bias is None else s + np.asarray(select_bias, dtype=np.float32).astype(
+        np.float64)
+    order_by = l if select_bias is None else c
+    size = E // n_group
+    ids = np.empty((M, top_k), dtype=np.int32)
+    for t in range(M):
+        members = range(E)
+        if n_group > 1:
+            group = []
+            for g in range(n_group):
+                part = c[t, g * size:(g + 1) * size]
+                best = [part[i] for i in _descending(part)[:group_top]]
+                group.append(best[0] if group_top == 1 else best[0] + best[1])
+            kept = set(_descending(group)[:topk_group])
+            members = [e for e in range(E) if e // size in kept]
+        members = list(members)
+        ids[t] = [members[i] for i in _descending([order_by[t, e] for e in members])[:top_k]]
+    return ids
+
+
+def select_weights(logits: np.ndarray, ids: np.ndarray, score: str, renormalize: bool,
+                   scale: float = 1.0) -> np.ndarray:
+    """Weights of given experts, float64, through logarithms: right where
+    every chosen score underflows; 0 where every chosen score is 0."""
+    ls = log_scores(np.asarray(logits, dtype=np.float32), score)
+    lk = np.take_along_axis(ls, np.asarray(ids, dtype=np.int64), axis=1)
+    if renormalize:
+        m = lk.max(axis=1, keepdims=True)
+        m = np.where(np.isneginf(m), 0.0, m)
+        with np.errstate(divide="ignore", invalid="ignore"):
+            lk = lk - m - np.log(np.exp(lk - m).sum(axis=1, keepdims=True))
+        lk = np.where(np.isnan(lk), -np.inf, lk)
+        lk = np.where(np.isposinf(lk), -np.inf, lk)
+    return scale * np.exp(lk)
+
+
+def select_backward(logits: np.ndarray, ids: np.ndarray, grad_weights: np.ndarray, score: str,
+                    renormalize: bool, scale: float = 1.0) -> np.ndarray:
+    """dL/dlogits [M, E] float64: each weight's Jacobian row, slot by slot."""
+    l = np.asarray(logits, dtype=np.float32).astype(np.float64)
+    M, E = l.shape
+    p = np.exp(log_scores(l, score))
+    w = select_weights(logits, ids, score, renormalize)
+    out = np.zeros((M, E))
+    for t in range(M):
+        k = ids.shape[1]
+        for j in range(k):
+            g = scale * float(grad_weights[t, j])
+            if renormalize:
+                # d w_j / d l_i = w_j (delta_ij - w_i) (1 - s_i  for a sigmoid)
+                for i in range(k):
+                    d = w[t, j] * ((1.0 if i == j else 0.0) - w[t, i])
+                    if score == "sigmoid":
+                        d *= 1.0 - p[t, ids[t, i]]
+                    out[t, ids[t, i]] += g * d
+            elif score == "sigmoid":
+                s = p[t, ids[t, j]]
+                out[t, ids[t, j]] += g * s * (1.0 - s)
+            else:
+                s = p[t, ids[t, j]]
+                out[t] -= g * s * p[t]
+                out[t, ids[t, j]] += g * s
+    return out
+
+
+def linear_quantized(x: np.ndarray, words: np.ndarray, scales: np.ndarray, biases: np.ndarray,
+                     group: int, gated: bool = False, row_scale=None, addend=None) -> np.ndarray:
+    """Dense product with 4-bit affine weights and its epilogue, float64:
+    x [M, K], addend [M, n_out], scales and biases as bf16 bits."""
+    X = widen_bf16(x)
+    y = X @ dequantize_affine(words, scales, biases, 4, X.shape[1], group).T
+    if gated:
+        half = y.shape[1] // 2
+        y = y[:, :half] / (1.0 + np.exp(-y[:, :half])) * y[:, half:]
+    if row_scale is not None:
+        y = y * np.asarray(row_scale, dtype=np.float32).astype(np.float64)[:, None]
+    if addend is not None:
+        y = y + widen_bf16(addend)
+    return y

@@ -3,8 +3,13 @@
 //   out = bf16(addend + row_scale[m] * y), or with `gated` SiLU(y[m, f]) *
 //   y[m, N / 2 + f] in y's place (rows 0 .. N/2 - 1 the gate).
 // Codes as in the group-quantized experts (least significant first in 32-bit
-// words), groups of 32, 64 or 128 elements; the codes are never rounded:
-// sum_k x w = s * sum q x + b * sum x inside a group, accumulated in fp32.
+// words), groups of 32, 64 or 128 elements.
+//
+// The codes are never rounded: a code q becomes the bf16 value 128 + q
+// exactly (q in the low mantissa bits of 128), the matrix cores form
+// acc = sum (128 + q) x and sx = sum x over one group in fp32, and
+//   s * sum q x + b * sum x = s * acc + (b - 128 s) * sx
+// is added to the output's fp32 sum, two FMAs per group and output.
 #include "moe_common.h"
 #include "qunit.h"
 
@@ -12,63 +17,300 @@ using namespace moe;
 
 namespace {
 
-constexpr int kLinWaves = 4;
-constexpr int kLinTokens = 4;
+// A 16-byte unit holds 32 codes of one weight row; a "block" is 128 codes of
+// each of 16 rows: lane (r = lane % 16, g = lane / 16) loads unit g of row r
+// (64 contiguous bytes per row).  An MFMA sums over the four lanes of a row,
+// so the codes it takes have to belong to one group: for groups of 64 and 32
+// the words are exchanged between the lanes of a row so that each word
+// register holds one group (two or four lane-swap instructions per block).
+constexpr int kBlockK = 128;
 
-// The epilogue of one output value.
-__device__ __forceinline__ void store_out(float y, const float* row_scale, const uint16_t* addend,
-                                          uint16_t* out, size_t m, size_t at) {
-  if (row_scale != nullptr) y *= row_scale[m];
-  if (addend != nullptr) y += bf16_load(addend + at);
-  out[at] = (uint16_t)f32_to_bf16(y);
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
 }
 
-// One output column (a row of W, or a gate row and its up row) per wave, up
-// to kLinTokens tokens; lane l takes units l, l + 64, ...
-template <bool kGated>
-__global__ __launch_bounds__(64 * kLinWaves) void qlinear_gemv_kernel(moe_host::QLinearArgs a) {
-  const int lane = threadIdx.x & 63;
+// Words of a block so that words [j * G/32, (j + 1) * G/32) are group j's.
+template <int G>
+__device__ __forceinline__ void group_words(u32x4& w) {
+  uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
+  if (G <= 64) {
+    swap32(a, c);
+    swap32(b, d);
+  }
+  if (G == 32) {
+    swap16(a, b);
+    swap16(c, d);
+  }
+  w = u32x4{a, b, c, d};
+}
+
+// The k offset inside a block of the 8 codes that lane group g holds in word
+// st after group_words.
+template <int G>
+__device__ __forceinline__ int word_k(int st, int g) {
+  if (G == 128) return 32 * g + 8 * st;
+  if (G == 64) return (g < 2 ? 32 * g : 32 * (g - 2) + 16) + 64 * (st >> 1) + 8 * (st & 1);
+  return 32 * st + 8 * g;
+}
+
+// Each group's (scale, bias) pair in every lane of its row, from the pair of
+// the lane's own unit.
+template <int G>
+__device__ __forceinline__ void group_pairs(uint32_t own, uint32_t (&p)[128 / G]) {
+  p[0] = own;
+  if constexpr (G <= 64) {
+    uint32_t other = own;
+    swap32(p[0], other);
+    if constexpr (G == 64) {
+      p[1] = other;
+    } else {
+      p[2] = other;
+      p[1] = p[0];
+      p[3] = p[2];
+      swap16(p[0], p[1]);
+      swap16(p[2], p[3]);
+    }
+  }
+}
+
+// 8 codes as bf16 values 128 + q, pairs (i, i + 4).  The constants are kept
+// in a scalar and a vector register, so that each pair is one and-or (two
+// literals would not fit one instruction).
+struct WidenConst {
+  uint32_t mask, magic;
+  __device__ __forceinline__ WidenConst() : mask(0x000f000fu), magic(0x43004300u) {
+    asm("" : "+s"(mask));
+    asm("" : "+v"(magic));
+  }
+};
+__device__ __forceinline__ u32x4 widen8(uint32_t w, const WidenConst& k) {
+  return u32x4{(w & k.mask) | k.magic, ((w >> 4) & k.mask) | k.magic,
+               ((w >> 8) & k.mask) | k.magic, ((w >> 12) & k.mask) | k.magic};
+}
+
+// 8 consecutive bf16 elements in the same pairs (i, i + 4).
+__device__ __forceinline__ u32x4 pair8(u32x4 X) {
+  const bf16x8 v = __builtin_bit_cast(bf16x8, X);
+  return __builtin_bit_cast(u32x4, __builtin_shufflevector(v, v, 0, 4, 1, 5, 2, 6, 3, 7));
+}
+
+// The epilogue of one output value.
+__device__ __forceinline__ void store_out(const moe_host::QLinearArgs& a, float y, int m, int n,
+                                          int n_out) {
+  const size_t at = (size_t)m * n_out + n;
+  if (a.row_scale != nullptr) y *= a.row_scale[m];
+  if (a.addend != nullptr) y += bf16_load(a.addend + at);
+  a.out[at] = (uint16_t)f32_to_bf16(y);
+}
+
+// ---- streaming kernel: few tokens ----
+//
+// A wave owns 32 weight rows (gated: 16 gate rows and their 16 up rows) and
+// 16 TM tokens; `kw` waves of a workgroup split K in interleaved blocks and
+// add their sums through LDS.  Weights go from memory to registers once, a
+// few blocks ahead, and every token of the tile reads x from the caches.
+template <int G, int TM, bool kGated, int D>
+__global__ __launch_bounds__(512) void qlinear_stream_kernel(moe_host::QLinearArgs a, int kw,
+                                                             int ntile) {
+  constexpr int NG = 128 / G;      // groups per block
+  constexpr int NS = G / 32;       // MFMA steps per group
+  extern __shared__ __attribute__((aligned(16))) float red[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
   const int n_out = kGated ? a.N / 2 : a.N;
-  const int ncol = ceil_div(n_out, kLinWaves);
-  const int bx = blockIdx.x % ncol;
-  const int m0 = blockIdx.x / ncol * kLinTokens;
-  const int f = bx * kLinWaves + (threadIdx.x >> 6);
-  if (f >= n_out) return;   // whole wave; no barrier follows
-  constexpr int R = kGated ? 2 : 1;
-  const int nunit = a.K / 32, ng = a.K / a.group, upg = a.group / 32;
-  float acc[R][kLinTokens];
+  const int per_wg = (blockDim.x >> 6) / kw;                 // row tiles per workgroup
+  const int wg_n = ceil_div(ntile, per_wg);
+  const int bn = blockIdx.x % wg_n, bm = blockIdx.x / wg_n;
+  const int tile = bn * per_wg + wave / kw, part = wave % kw;
+  if (kw == 1 && tile >= ntile) return;   // whole wave; no barrier follows
+  const int m0 = bm * 16 * TM;
+  const int n0 = tile * (kGated ? 16 : 32);   // past the end: nothing is stored
+  const int nblk = ceil_div(a.K, kBlockK);
+  const int upr = a.K / 32, gpr = a.K / G;                   // units and groups per row
+
+  // rows past the ends are read as the last one and never stored
+  const u32x4* wrow[2];
+  const uint16_t *srow[2], *brow[2];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int f = 0; f < 2; ++f) {
+    const int n = min(n0 + r + (kGated ? 0 : 16 * f), n_out - 1) + (kGated && f ? n_out : 0);
+    wrow[f] = reinterpret_cast<const u32x4*>(a.q) + (size_t)n * upr;
+    srow[f] = a.scales + (size_t)n * gpr;
+    brow[f] = a.biases + (size_t)n * gpr;
+  }
+  const uint16_t* xrow[TM];
 #pragma unroll
-    for (int u = 0; u < kLinTokens; ++u) acc[r][u] = 0.f;
-  for (int u = lane; u < nunit; u += 64) {
-    XPairs4 xp[kLinTokens];
+  for (int t = 0; t < TM; ++t) xrow[t] = a.x + (size_t)min(m0 + 16 * t + r, a.M - 1) * a.K;
+
+  const WidenConst wc;
+  f32x4 tot[2][TM];
 #pragma unroll
-    for (int v = 0; v < kLinTokens; ++v) {
-      const int m = m0 + v < a.M ? m0 + v : 0;
-      const u32x4* xr = reinterpret_cast<const u32x4*>(a.x + (size_t)m * a.K) + (size_t)u * 4;
-      u32x4 xv[4];
+  for (int f = 0; f < 2; ++f)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xv[i] = xr[i];
-      xp[v] = regroup_x4(xv);
+    for (int t = 0; t < TM; ++t) tot[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  u32x4 wb[D][2], xb[D][TM][4];
+  uint32_t sb[D][2];
+  auto load = [&](int blk, u32x4 (&w)[2], uint32_t (&p)[2], u32x4 (&xv)[TM][4]) {
+    // a unit past the row's end is read as unit 0; its x is cleared below
+    const int u = 4 * blk + g < upr ? 4 * blk + g : 0;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      w[f] = __builtin_nontemporal_load(wrow[f] + u);
+      const int gi = u * 32 / G;
+      p[f] = (uint32_t)srow[f][gi] | ((uint32_t)brow[f][gi] << 16);
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const size_t row = (size_t)f + (size_t)r * n_out;
-      const u32x4 c = reinterpret_cast<const u32x4*>(a.q)[row * nunit + u];
-      const float s = bf16_load(a.scales + row * ng + u / upg);
-      const float b = bf16_load(a.biases + row * ng + u / upg);
+    for (int t = 0; t < TM; ++t)
 #pragma unroll
-      for (int v = 0; v < kLinTokens; ++v) acc[r][v] += s * dot_unit4(c, xp[v]) + b * xp[v].sx;
+      for (int st = 0; st < 4; ++st) {
+        const int k = blk * kBlockK + word_k<G>(st, g);
+        xv[t][st] = load16(xrow[t] + (k < a.K ? k : 0));
+      }
+  };
+  auto compute = [&](int blk, u32x4 (&w)[2], uint32_t (&p)[2], u32x4 (&xv)[TM][4]) {
+    if ((blk + 1) * kBlockK > a.K) {
+#pragma unroll
+      for (int st = 0; st < 4; ++st)
+        if (blk * kBlockK + word_k<G>(st, g) >= a.K)
+#pragma unroll
+          for (int t = 0; t < TM; ++t) xv[t][st] = u32x4{0u, 0u, 0u, 0u};
+      if (4 * blk + g >= upr) p[0] = p[1] = 0u;
+    }
+    uint32_t pair[2][NG];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      group_words<G>(w[f]);
+      group_pairs<G>(p[f], pair[f]);
+    }
+    const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      f32x4 acc[2][TM], sx[TM];
+#pragma unroll
+      for (int t = 0; t < TM; ++t) {
+        sx[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        acc[0][t] = acc[1][t] = sx[t];
+      }
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int st = j * NS + i;
+        const u32x4 w0 = widen8(w[0][st], wc), w1 = widen8(w[1][st], wc);
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+          const u32x4 xp = pair8(xv[t][st]);
+          sx[t] = mfma_16x16x32(xp, ones, sx[t]);
+          acc[0][t] = mfma_16x16x32(xp, w0, acc[0][t]);
+          acc[1][t] = mfma_16x16x32(xp, w1, acc[1][t]);
+        }
+      }
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const float s = bf16_lo(pair[f][j]);
+        const float c = __builtin_fmaf(-128.f, s, bf16_hi(pair[f][j]));
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            tot[f][t][q] = __builtin_fmaf(
+                s, acc[f][t][q], __builtin_fmaf(c, sx[t][q], tot[f][t][q]));
+      }
+    }
+  };
+
+  // blocks part, part + kw, ...; loads past the last one repeat it, so that
+  // no load sits behind a branch
+  const int n = (nblk - part + kw - 1) / kw;
+  auto at = [&](int i) { return min(part + i * kw, nblk - 1); };
+#pragma unroll
+  for (int i = 0; i < D; ++i) load(at(i), wb[i], sb[i], xb[i]);
+  int it = 0;
+  for (; it + D <= n; it += D) {
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      compute(at(it + i), wb[i], sb[i], xb[i]);
+      load(at(it + i + D), wb[i], sb[i], xb[i]);
     }
   }
 #pragma unroll
-  for (int v = 0; v < kLinTokens; ++v) {
-    float y = wave_sum(acc[0][v]);
-    if (kGated) y = silu_mul(y, wave_sum(acc[R - 1][v]));
-    if (lane == 0 && m0 + v < a.M)
-      store_out(y, a.row_scale, a.addend, a.out, m0 + v, (size_t)(m0 + v) * n_out + f);
+  for (int i = 0; i < D - 1; ++i)
+    if (it + i < n) compute(at(it + i), wb[i], sb[i], xb[i]);
+  if (kw > 1) {
+    constexpr int kVals = 2 * TM * 4;
+    float* mine = red + (size_t)wave * kVals * 64 + lane;
+    if (part != 0) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mine[((f * TM + t) * 4 + q) * 64] = tot[f][t][q];
+    }
+    __syncthreads();
+    if (part != 0) return;
+    for (int o = 1; o < kw; ++o)
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            tot[f][t][q] += mine[(o * kVals + (f * TM + t) * 4 + q) * 64];
   }
+  // lane: weight row r of each fragment, tokens 4 g .. 4 g + 3 of each tile
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int m = m0 + 16 * t + 4 * g + q;
+      if (m >= a.M) continue;
+      if (kGated) {
+        if (n0 + r < n_out) store_out(a, silu_mul(tot[0][t][q], tot[1][t][q]), m, n0 + r, n_out);
+      } else {
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          if (n0 + 16 * f + r < n_out) store_out(a, tot[f][t][q], m, n0 + 16 * f + r, n_out);
+      }
+    }
+}
+
+template <int G, int TM, bool kGated, int D>
+hipError_t launch_stream(const moe_host::QLinearArgs& a, hipStream_t s) {
+  using moe_host::ceil_div_host;
+  const int n_out = kGated ? a.N / 2 : a.N;
+  const int ntile = ceil_div_host(n_out, kGated ? 16 : 32);
+  const int mtile = ceil_div_host(a.M, 16 * TM);
+  const int nblk = ceil_div_host(a.K, kBlockK);
+  // enough waves to keep two on every SIMD, as far as K has blocks to split
+  const long long want = 8LL * moe_host::device_cu_count();
+  int kw = 1;
+  while (kw < 8 && kw < nblk && (long long)ntile * mtile * kw < want) kw *= 2;
+  const int waves = kw < 4 ? 4 : kw;
+  const size_t lds = kw > 1 ? (size_t)waves * 2 * TM * 4 * 64 * sizeof(float) : 0;
+  const dim3 grid((unsigned)ceil_div_host(ntile, waves / kw) * mtile);
+  if (lds > 64 * 1024) return hipErrorInvalidValue;   // 8 waves x 8 KB at most
+  hipLaunchKernelGGL((qlinear_stream_kernel<G, TM, kGated, D>), grid, dim3(64 * waves), lds, s, a,
+                     kw, ntile);
+  return hipGetLastError();
+}
+
+template <int G, bool kGated>
+hipError_t launch_tokens(const moe_host::QLinearArgs& a, hipStream_t s) {
+  if (a.M <= 16) return launch_stream<G, 1, kGated, 2>(a, s);
+  if (a.M <= 32) return launch_stream<G, 2, kGated, 1>(a, s);
+  return launch_stream<G, 4, kGated, 1>(a, s);
+}
+
+template <int G>
+hipError_t launch_group(const moe_host::QLinearArgs& a, hipStream_t s) {
+  return a.gated ? launch_tokens<G, true>(a, s) : launch_tokens<G, false>(a, s);
 }
 
 }  // namespace
@@ -76,13 +318,11 @@ __global__ __launch_bounds__(64 * kLinWaves) void qlinear_gemv_kernel(moe_host::
 namespace moe_host {
 
 hipError_t launch_qlinear(const QLinearArgs& a, hipStream_t s) {
-  const int n_out = a.gated ? a.N / 2 : a.N;
-  const dim3 grid((unsigned)ceil_div_host(n_out, kLinWaves) * ceil_div_host(a.M, kLinTokens));
-  if (a.gated)
-    hipLaunchKernelGGL(qlinear_gemv_kernel<true>, grid, dim3(64 * kLinWaves), 0, s, a);
-  else
-    hipLaunchKernelGGL(qlinear_gemv_kernel<false>, grid, dim3(64 * kLinWaves), 0, s, a);
-  return hipGetLastError();
+  switch (a.group) {
+    case 32: return launch_group<32>(a, s);
+    case 64: return launch_group<64>(a, s);
+    default: return launch_group<128>(a, s);
+  }
 }
 
 }  // namespace moe_host

@@ -110,6 +110,144 @@ __device__ __forceinline__ void store_out(const moe_host::QLinearArgs& a, float 
   a.out[at] = (uint16_t)f32_to_bf16(y);
 }
 
+// ---- GEMV: one to four tokens ----
+//
+// A lane keeps one unit (32 elements) of each token's x in registers, as the
+// pairs that the codes widen to, and walks over weight rows: four rows at a
+// time, the next four in flight, 1 KB of codes per row and wave.  Rows longer
+// than 64 units are cut into `ns` slices of at most 64 units, one per wave
+// (more than kGemvWaves slices: in turns, x read again).  The four rows' sums
+// over the lanes share their first two steps (lane swaps), and the sums wait
+// in LDS until the workgroup's rows are done.
+constexpr int kGemvWaves = 8;
+constexpr int kGemvMaxRows = 64;   // weight rows per wave group
+
+template <int T, bool kGated>
+__global__ __launch_bounds__(64 * kGemvWaves) void qlinear_gemv_kernel(moe_host::QLinearArgs a,
+                                                                       int ns, int nw,
+                                                                       int chunks) {
+  __shared__ float red[kGemvWaves][kGemvMaxRows * T];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int groups = (blockDim.x >> 6) / nw;               // wave groups per workgroup
+  const int grp = wave / nw, w = wave % nw;
+  const int n_out = kGated ? a.N / 2 : a.N;
+  constexpr int kOut = kGated ? 2 : 4;                     // outputs per chunk of four rows
+  const int o0 = (blockIdx.x * groups + grp) * chunks * kOut;
+  const int upr = a.K / 32, gpr = a.K / a.group, sh = a.group == 32 ? 0 : a.group == 64 ? 1 : 2;
+  const int ulen = ceil_div(upr, ns);
+  const u32x4* q = reinterpret_cast<const u32x4*>(a.q);
+
+  // row i of chunk c; rows past the end read the last one
+  auto row_of = [&](int c, int i) {
+    const int o = min(o0 + c * kOut + (kGated ? i & 1 : i), n_out - 1);
+    return kGated && i >= 2 ? o + n_out : o;
+  };
+  for (int sl = w; sl < ns; sl += nw) {
+    const int u = sl * ulen + lane;
+    const bool ok = lane < ulen && u < upr;
+    const int uc = ok ? u : 0;
+    u32x4 cw[4];
+    uint32_t cs[4], cb[4];
+    auto load = [&](int c) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const size_t n = (size_t)row_of(c, i);
+        cw[i] = __builtin_nontemporal_load(q + n * upr + uc);
+        cs[i] = a.scales[n * gpr + (uc >> sh)];
+        cb[i] = a.biases[n * gpr + (uc >> sh)];
+      }
+    };
+    load(0);
+    XPairs4 xp[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const u32x4* xr =
+          reinterpret_cast<const u32x4*>(a.x + (size_t)min(t, a.M - 1) * a.K) + (size_t)uc * 4;
+      u32x4 xv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        xv[i] = xr[i];
+        if (!ok) xv[i] = u32x4{0u, 0u, 0u, 0u};
+      }
+      xp[t] = regroup_x4(xv);
+    }
+    const WidenConst wc;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      float y[T][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float s = __uint_as_float(cs[i] << 16);
+        const float k = __builtin_fmaf(-128.f, s, __uint_as_float(cb[i] << 16));
+        float d[T];
+#pragma unroll
+        for (int t = 0; t < T; ++t) d[t] = 0.f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const u32x4 p = widen8(cw[i][v], wc);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int t = 0; t < T; ++t) d[t] = dot2_bf16(p[j], xp[t].y[4 * v + j], d[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t) y[t][i] = __builtin_fmaf(s, d[t], k * xp[t].sx);
+      }
+      load(min(c + 1, chunks - 1));
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        // four sums over 64 lanes -> one register: row of 16 lanes i holds sum i
+        uint32_t b0 = __float_as_uint(y[t][0]), b1 = __float_as_uint(y[t][1]);
+        uint32_t b2 = __float_as_uint(y[t][2]), b3 = __float_as_uint(y[t][3]);
+        swap32(b0, b2);
+        swap32(b1, b3);
+        uint32_t e = __float_as_uint(__uint_as_float(b0) + __uint_as_float(b2));
+        uint32_t o = __float_as_uint(__uint_as_float(b1) + __uint_as_float(b3));
+        swap16(e, o);
+        const float v = group_sum_last<16>(__uint_as_float(e) + __uint_as_float(o));
+        if ((lane & 15) == 15) {
+          float* r = &red[wave][t * kGemvMaxRows + 4 * c + (lane >> 4)];
+          *r = sl == w ? v : *r + v;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  // outputs of this wave group, over its own threads
+  const int no = chunks * kOut;
+  for (int i = w * 64 + lane; i < no * T; i += 64 * nw) {
+    const int t = i / no, o = i - t * no;
+    if (t >= a.M || o0 + o >= n_out) continue;
+    const int at = t * kGemvMaxRows + (kGated ? 4 * (o >> 1) + (o & 1) : o);
+    float y = 0.f, up = 0.f;
+    for (int p = 0; p < nw; ++p) {
+      y += red[grp * nw + p][at];
+      if (kGated) up += red[grp * nw + p][at + 2];
+    }
+    if (kGated) y = silu_mul(y, up);
+    store_out(a, y, t, o0 + o, n_out);
+  }
+}
+
+template <int T, bool kGated>
+hipError_t launch_gemv(const moe_host::QLinearArgs& a, hipStream_t s) {
+  using moe_host::ceil_div_host;
+  const int n_out = kGated ? a.N / 2 : a.N;
+  constexpr int kOut = kGated ? 2 : 4;
+  const int ns = ceil_div_host(a.K / 32, 64);
+  const int nw = ns < kGemvWaves ? ns : kGemvWaves;
+  const int groups = nw >= 4 ? 1 : 4 / nw;
+  // chunks per wave group: about six waves for every SIMD
+  const long long total = ceil_div_host(n_out, kOut);
+  const long long want = 24LL * moe_host::device_cu_count() / nw;
+  long long chunks = (total + want - 1) / want;
+  if (chunks > kGemvMaxRows / 4) chunks = kGemvMaxRows / 4;
+  const dim3 grid((unsigned)ceil_div_host((int)((total + chunks - 1) / chunks), groups));
+  hipLaunchKernelGGL((qlinear_gemv_kernel<T, kGated>), grid, dim3(64 * nw * groups), 0, s, a, ns,
+                     nw, (int)chunks);
+  return hipGetLastError();
+}
+
 // ---- streaming kernel: few tokens ----
 //
 // A wave owns 32 weight rows (gated: 16 gate rows and their 16 up rows) and
@@ -301,6 +439,13 @@ hipError_t launch_stream(const moe_host::QLinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <bool kGated>
+hipError_t launch_few(const moe_host::QLinearArgs& a, hipStream_t s) {
+  if (a.M == 1) return launch_gemv<1, kGated>(a, s);
+  if (a.M == 2) return launch_gemv<2, kGated>(a, s);
+  return launch_gemv<4, kGated>(a, s);
+}
+
 template <int G, bool kGated>
 hipError_t launch_tokens(const moe_host::QLinearArgs& a, hipStream_t s) {
   if (a.M <= 16) return launch_stream<G, 1, kGated, 2>(a, s);
@@ -318,6 +463,7 @@ hipError_t launch_group(const moe_host::QLinearArgs& a, hipStream_t s) {
 namespace moe_host {
 
 hipError_t launch_qlinear(const QLinearArgs& a, hipStream_t s) {
+  if (a.M <= 4) return a.gated ? launch_few<true>(a, s) : launch_few<false>(a, s);
   switch (a.group) {
     case 32: return launch_group<32>(a, s);
     case 64: return launch_group<64>(a, s);

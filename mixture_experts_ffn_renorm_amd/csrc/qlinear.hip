@@ -248,6 +248,165 @@ hipError_t launch_gemv(const moe_host::QLinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ---- row-tile kernel: up to 32 tokens ----
+//
+// A wave keeps the x of 16 TM tokens and NB blocks (its slice of K) in
+// registers as MFMA operands and walks over tiles of 16 weight rows, one
+// tile's codes in flight while another is multiplied; the `nw` waves of a
+// workgroup hold the slices of one K (in turns where there are more slices
+// than waves).  A tile's sums wait in LDS until the workgroup's tiles are
+// done and are then added over the waves.
+constexpr int kRowsWaves = 8;
+constexpr int kRowsLds = 64 * 1024;
+
+template <int G, int TM, int NB>
+__global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host::QLinearArgs a,
+                                                                       int ns, int tiles) {
+  constexpr int NG = 128 / G;      // groups per block
+  constexpr int NS = G / 32;       // MFMA steps per group
+  extern __shared__ __attribute__((aligned(16))) f32x4 sums[];   // [nw][tiles][TM][64]
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nw = blockDim.x >> 6;
+  const int r = lane & 15, g = lane >> 4;
+  const int n_out = a.gated ? a.N / 2 : a.N;
+  const int upr = a.K / 32, gpr = a.K / G;
+  // gated: tiles 2 j and 2 j + 1 are the gate and up rows of the same outputs
+  const int t0 = blockIdx.x * tiles;
+  auto row_of = [&](int tile) {
+    const int o = (a.gated ? tile >> 1 : tile) * 16 + r;
+    return min(o, n_out - 1) + (a.gated && (tile & 1) ? n_out : 0);
+  };
+  const WidenConst wc;
+  const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+#pragma unroll 1
+  for (int sl = w; sl < ns; sl += nw) {
+    const int u0 = sl * NB * 4 + g;   // this lane's unit of the slice's first block
+    u32x4 cw[NB];
+    uint32_t cs[NB], cb[NB];
+    auto load = [&](int tile) {
+      const size_t n = (size_t)row_of(t0 + tile);
+      const u32x4* q = reinterpret_cast<const u32x4*>(a.q) + n * upr;
+      const uint16_t *sp = a.scales + n * gpr, *bp = a.biases + n * gpr;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        // a unit past the row's end is read as unit 0; its x is 0
+        const int u = u0 + 4 * b < upr ? u0 + 4 * b : 0;
+        cw[b] = __builtin_nontemporal_load(q + u);
+        cs[b] = sp[u * 32 / G];
+        cb[b] = bp[u * 32 / G];
+      }
+    };
+    load(0);
+    u32x4 xp[TM][NB][4];
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      const uint16_t* xr = a.x + (size_t)min(16 * t + r, a.M - 1) * a.K;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+          const int k = (sl * NB + b) * kBlockK + word_k<G>(st, g);
+          u32x4 v = load16(xr + (k < a.K ? k : 0));
+          if (k >= a.K) v = u32x4{0u, 0u, 0u, 0u};
+          xp[t][b][st] = pair8(v);
+        }
+    }
+#pragma unroll 1
+    for (int tile = 0; tile < tiles; ++tile) {
+      f32x4 tot[TM];
+#pragma unroll
+      for (int t = 0; t < TM; ++t) tot[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        asm volatile("" : "+v"(cs[b]), "+v"(cb[b]));   // joined here, not where they are loaded
+        uint32_t pair[NG];
+        group_words<G>(cw[b]);
+        group_pairs<G>(u0 + 4 * b < upr ? cs[b] | (cb[b] << 16) : 0u, pair);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+          f32x4 acc[TM], sx[TM];
+#pragma unroll
+          for (int t = 0; t < TM; ++t) acc[t] = sx[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            const u32x4 wv = widen8(cw[b][j * NS + i], wc);
+#pragma unroll
+            for (int t = 0; t < TM; ++t) {
+              sx[t] = mfma_16x16x32(xp[t][b][j * NS + i], ones, sx[t]);
+              acc[t] = mfma_16x16x32(xp[t][b][j * NS + i], wv, acc[t]);
+            }
+          }
+          const float s = bf16_lo(pair[j]);
+          const float c = __builtin_fmaf(-128.f, s, bf16_hi(pair[j]));
+#pragma unroll
+          for (int t = 0; t < TM; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              tot[t][q] = __builtin_fmaf(s, acc[t][q], __builtin_fmaf(c, sx[t][q], tot[t][q]));
+        }
+      }
+      load(min(tile + 1, tiles - 1));
+#pragma unroll
+      for (int t = 0; t < TM; ++t) {
+        f32x4* p = sums + ((size_t)(w * tiles + tile) * TM + t) * 64 + lane;
+        *p = sl == w ? tot[t] : *p + tot[t];
+      }
+    }
+  }
+  __syncthreads();
+  // lane: weight row r of a tile, tokens 4 g .. 4 g + 3 of a token tile
+  const int per = a.gated ? 2 : 1;
+  for (int i = threadIdx.x; i < tiles / per * TM * 64; i += blockDim.x) {
+    const int ln = i & 63, t = (i >> 6) % TM, tile = (i >> 6) / TM * per;
+    f32x4 y = {0.f, 0.f, 0.f, 0.f}, up = y;
+    for (int p = 0; p < nw; ++p) {
+      y += sums[((p * tiles + tile) * TM + t) * 64 + ln];
+      if (a.gated) up += sums[((p * tiles + tile + 1) * TM + t) * 64 + ln];
+    }
+    const int o = (t0 + tile) / per * 16 + (ln & 15);
+    if (o >= n_out) continue;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int m = 16 * t + 4 * (ln >> 4) + q;
+      if (m < a.M) store_out(a, a.gated ? silu_mul(y[q], up[q]) : y[q], m, o, n_out);
+    }
+  }
+}
+
+template <int G, int TM, int NB>
+hipError_t launch_rows_nb(const moe_host::QLinearArgs& a, hipStream_t s) {
+  using moe_host::ceil_div_host;
+  const int per = a.gated ? 2 : 1;
+  const int total = ceil_div_host(a.gated ? a.N / 2 : a.N, 16) * per;
+  const int ns = ceil_div_host(ceil_div_host(a.K, kBlockK), NB);
+  const int nw = ns < kRowsWaves ? ns : kRowsWaves;
+  // tiles per workgroup: about two waves for every SIMD, as far as LDS holds
+  // the sums (gated: whole pairs of tiles)
+  const long long want = 8LL * moe_host::device_cu_count() / nw;
+  int tiles = (int)((total + want - 1) / want);
+  const int most = kRowsLds / (nw * TM * 1024);
+  tiles = tiles > most ? most : tiles;
+  tiles = (tiles + per - 1) / per * per;
+  const size_t lds = (size_t)nw * tiles * TM * 1024;
+  hipLaunchKernelGGL((qlinear_rows_kernel<G, TM, NB>), dim3(ceil_div_host(total, tiles)),
+                     dim3(64 * nw), lds, s, a, ns, tiles);
+  return hipGetLastError();
+}
+
+// Blocks per wave: the fewest turns of at most four blocks over eight waves,
+// evenly filled.
+template <int G, int TM>
+hipError_t launch_rows(const moe_host::QLinearArgs& a, hipStream_t s) {
+  const int nblk = moe_host::ceil_div_host(a.K, kBlockK);
+  const int turns = moe_host::ceil_div_host(nblk, 4 * kRowsWaves);
+  switch (moe_host::ceil_div_host(nblk, turns * kRowsWaves)) {
+    case 1: return launch_rows_nb<G, TM, 1>(a, s);
+    case 2: return launch_rows_nb<G, TM, 2>(a, s);
+    case 3: return launch_rows_nb<G, TM, 3>(a, s);
+    default: return launch_rows_nb<G, TM, 4>(a, s);
+  }
+}
+
 // ---- streaming kernel: few tokens ----
 //
 // A wave owns 32 weight rows (gated: 16 gate rows and their 16 up rows) and
@@ -295,15 +454,16 @@ __global__ __launch_bounds__(512) void qlinear_stream_kernel(moe_host::QLinearAr
     for (int t = 0; t < TM; ++t) tot[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   u32x4 wb[D][2], xb[D][TM][4];
-  uint32_t sb[D][2];
-  auto load = [&](int blk, u32x4 (&w)[2], uint32_t (&p)[2], u32x4 (&xv)[TM][4]) {
+  uint16_t sb[D][2][2];   // scale, bias: joined only when used, so that no load is waited for here
+  auto load = [&](int blk, u32x4 (&w)[2], uint16_t (&p)[2][2], u32x4 (&xv)[TM][4]) {
     // a unit past the row's end is read as unit 0; its x is cleared below
     const int u = 4 * blk + g < upr ? 4 * blk + g : 0;
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
       w[f] = __builtin_nontemporal_load(wrow[f] + u);
       const int gi = u * 32 / G;
-      p[f] = (uint32_t)srow[f][gi] | ((uint32_t)brow[f][gi] << 16);
+      p[f][0] = srow[f][gi];
+      p[f][1] = brow[f][gi];
     }
 #pragma unroll
     for (int t = 0; t < TM; ++t)
@@ -313,20 +473,20 @@ __global__ __launch_bounds__(512) void qlinear_stream_kernel(moe_host::QLinearAr
         xv[t][st] = load16(xrow[t] + (k < a.K ? k : 0));
       }
   };
-  auto compute = [&](int blk, u32x4 (&w)[2], uint32_t (&p)[2], u32x4 (&xv)[TM][4]) {
+  auto compute = [&](int blk, u32x4 (&w)[2], uint16_t (&p)[2][2], u32x4 (&xv)[TM][4]) {
     if ((blk + 1) * kBlockK > a.K) {
 #pragma unroll
       for (int st = 0; st < 4; ++st)
         if (blk * kBlockK + word_k<G>(st, g) >= a.K)
 #pragma unroll
           for (int t = 0; t < TM; ++t) xv[t][st] = u32x4{0u, 0u, 0u, 0u};
-      if (4 * blk + g >= upr) p[0] = p[1] = 0u;
     }
+    const bool in = 4 * blk + g < upr;
     uint32_t pair[2][NG];
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
       group_words<G>(w[f]);
-      group_pairs<G>(p[f], pair[f]);
+      group_pairs<G>(in ? (uint32_t)p[f][0] | ((uint32_t)p[f][1] << 16) : 0u, pair[f]);
     }
     const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 #pragma unroll
@@ -448,8 +608,8 @@ hipError_t launch_few(const moe_host::QLinearArgs& a, hipStream_t s) {
 
 template <int G, bool kGated>
 hipError_t launch_tokens(const moe_host::QLinearArgs& a, hipStream_t s) {
-  if (a.M <= 16) return launch_stream<G, 1, kGated, 2>(a, s);
-  if (a.M <= 32) return launch_stream<G, 2, kGated, 1>(a, s);
+  if (a.M <= 16) return launch_rows<G, 1>(a, s);
+  if (a.M <= 32) return launch_rows<G, 2>(a, s);
   return launch_stream<G, 4, kGated, 1>(a, s);
 }
 

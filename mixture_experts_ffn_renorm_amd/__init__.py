@@ -573,7 +573,7 @@ class Routing:
     scored by their best expert (``group_top`` 1) or the sum of their best two
     (2); ``scale``: a factor of every weight."""
 
-    __slots__ = ("_c", "select_bias")
+    __slots__ = ("_c", "_address", "top_k", "select_bias")
 
     def __init__(self, top_k: int, score: str = "softmax", renormalize: bool = True,
                  select_bias=None, n_group: int = 1, topk_group: Optional[int] = None,
@@ -582,14 +582,17 @@ class Routing:
             raise ValueError(f"score must be one of {tuple(_SCORES)}, got {score!r}")
         if select_bias is not None:
             _check(select_bias, "select_bias", (_torch().float32,))
-        self.select_bias = select_bias
-        self._c = RoutingRule(_SCORES[score], int(top_k), int(bool(renormalize)), int(n_group),
-                              int(n_group if topk_group is None else topk_group),
-                              int(group_top), float(scale), None)
+        set_ = object.__setattr__
+        set_(self, "select_bias", select_bias)
+        set_(self, "top_k", int(top_k))
+        set_(self, "_c", RoutingRule(
+            _SCORES[score], int(top_k), int(bool(renormalize)), int(n_group),
+            int(n_group if topk_group is None else topk_group), int(group_top), float(scale),
+            None if select_bias is None else select_bias.data_ptr()))
+        set_(self, "_address", ctypes.addressof(self._c))
 
-    @property
-    def top_k(self) -> int:
-        return self._c.top_k
+    def __setattr__(self, name, value):
+        raise AttributeError("a Routing does not change; build another one")
 
     @property
     def score(self) -> str:
@@ -619,81 +622,81 @@ class Routing:
         """Address of the C struct for a layer of E experts on a device."""
         b = self.select_bias
         if b is not None:
-            _need(b, "select_bias", _torch().float32, (E,), device)
-            self._c.select_bias = b.data_ptr()
-        return ctypes.addressof(self._c)
+            _need(b, "select_bias", b.dtype, (E,), device)
+            if b.data_ptr() != self._c.select_bias:   # its storage was replaced
+                _check(b, "select_bias", (_torch().float32,))
+                self._c.select_bias = b.data_ptr()
+        return self._address
 
 
 def _need(t, name, dtype, shape, device: int):
     """Raise unless t is a dense aligned tensor of that kind on that device."""
     if not (t.dtype is dtype and t.shape == shape and t.get_device() == device and
             t.is_contiguous() and t.data_ptr() % 16 == 0):
-        torch = _torch()
-        _check(t, name, _bf16_types() if dtype is torch.bfloat16 else (dtype,), shape)
-        if t.get_device() != device:
-            raise ValueError(f"{name} is on device {t.get_device()}, expected {device}")
+        _refuse(t, name, dtype, shape, device)
 
 
-def _device_of(t, name) -> int:
-    if t is None or not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    return t.get_device()
+def _refuse(t, name, dtype, shape, device: int):
+    torch = _torch()
+    _check(t, name, _bf16_types() if dtype is torch.bfloat16 else (dtype,), shape)
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on device {t.get_device()}, expected {device}")
 
 
-class _On:
-    """The device of a call's tensors made current, and the stream that the
-    call goes to: ``stream``, or that device's current one."""
+def _current(device: int) -> bool:
+    """Whether the call's device is the current one (False too for a host
+    tensor's -1, which the argument checks then refuse)."""
+    return device >= 0 and _torch()._C._cuda_getDevice() == device
 
-    __slots__ = ("device", "stream", "guard", "given")
 
-    def __init__(self, device: int, stream):
-        self.device, self.given = device, stream
+def _elsewhere(device: int, call, *args):
+    """The call with its tensors' device made current."""
+    torch = _torch()
+    if device < 0:
+        raise ValueError(f"{call.__name__} needs device tensors")
+    with torch.cuda.device(device):
+        return call(*args)
 
-    def __enter__(self):
-        torch = _torch()
-        self.guard = None
-        if self.given is not None and self.given.device_index != self.device:
-            raise ValueError(f"the stream is on device {self.given.device_index}, the tensors "
-                             f"on {self.device}")
-        if torch.cuda.current_device() != self.device:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        self.stream = (torch.cuda.current_stream() if self.given is None
-                       else self.given).cuda_stream
-        return self
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _raw_stream(device: int, stream) -> int:
+    """The hipStream_t of a call: ``stream``, or the device's current one."""
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is on device {stream.device_index}, the tensors on {device}")
+    return stream.cuda_stream
 
-    def empty(self, shape, dtype):
-        """A new tensor that the given stream may use."""
-        t = _torch().empty(shape, dtype=dtype, device=self.device)
-        if self.given is not None:
-            t.record_stream(self.given)
-        return t
+
+def _empty(shape, dtype, device: int, stream):
+    """A new tensor that the call's stream may use."""
+    t = _torch().empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
 
 
 def moe_select(logits, routing: Routing, topk_ids=None, topk_weights=None, stream=None):
     """Expert ids [M, top_k] int32 and weights [M, top_k] fp32 of logits
     [M, E] fp32 under a routing rule."""
     torch = _torch()
+    dev = logits.get_device()
+    if not _current(dev):
+        return _elsewhere(dev, moe_select, logits, routing, topk_ids, topk_weights, stream)
     M, E = logits.shape
-    k = routing.top_k
-    dev = _device_of(logits, "logits")
+    out = (M, routing.top_k)
     _need(logits, "logits", torch.float32, (M, E), dev)
-    rule = routing._arg(E, dev)
-    with _On(dev, stream) as on:
-        if topk_ids is None:
-            topk_ids = on.empty((M, k), torch.int32)
-        if topk_weights is None:
-            topk_weights = on.empty((M, k), torch.float32)
-        _need(topk_ids, "topk_ids", torch.int32, (M, k), dev)
-        _need(topk_weights, "topk_weights", torch.float32, (M, k), dev)
-        st = library().moe_select(logits.data_ptr(), rule, M, E, topk_ids.data_ptr(),
-                                  topk_weights.data_ptr(), on.stream)
-    _raise("moe_select", st)
+    if topk_ids is None:
+        topk_ids = _empty(out, torch.int32, dev, stream)
+    else:
+        _need(topk_ids, "topk_ids", torch.int32, out, dev)
+    if topk_weights is None:
+        topk_weights = _empty(out, torch.float32, dev, stream)
+    else:
+        _need(topk_weights, "topk_weights", torch.float32, out, dev)
+    st = library().moe_select(logits.data_ptr(), routing._arg(E, dev), M, E, topk_ids.data_ptr(),
+                              topk_weights.data_ptr(), _raw_stream(dev, stream))
+    if st:
+        _raise("moe_select", st)
     return topk_ids, topk_weights
 
 
@@ -702,21 +705,24 @@ def moe_select_backward(logits, topk_ids, grad_weights, routing: Routing, grad_l
     """Gradient [M, E] fp32 of moe_select's weights with respect to its
     logits, for the ids it gave and the weights' gradient [M, top_k] fp32."""
     torch = _torch()
+    dev = logits.get_device()
+    if not _current(dev):
+        return _elsewhere(dev, moe_select_backward, logits, topk_ids, grad_weights, routing,
+                          grad_logits, stream)
     M, E = logits.shape
-    k = routing.top_k
-    dev = _device_of(logits, "logits")
+    pairs = (M, routing.top_k)
     _need(logits, "logits", torch.float32, (M, E), dev)
-    _need(topk_ids, "topk_ids", torch.int32, (M, k), dev)
-    _need(grad_weights, "grad_weights", torch.float32, (M, k), dev)
-    rule = routing._arg(E, dev)
-    with _On(dev, stream) as on:
-        if grad_logits is None:
-            grad_logits = on.empty((M, E), torch.float32)
+    _need(topk_ids, "topk_ids", torch.int32, pairs, dev)
+    _need(grad_weights, "grad_weights", torch.float32, pairs, dev)
+    if grad_logits is None:
+        grad_logits = _empty((M, E), torch.float32, dev, stream)
+    else:
         _need(grad_logits, "grad_logits", torch.float32, (M, E), dev)
-        st = library().moe_select_backward(logits.data_ptr(), topk_ids.data_ptr(),
-                                           grad_weights.data_ptr(), rule, M, E,
-                                           grad_logits.data_ptr(), on.stream)
-    _raise("moe_select_backward", st)
+    st = library().moe_select_backward(logits.data_ptr(), topk_ids.data_ptr(),
+                                       grad_weights.data_ptr(), routing._arg(E, dev), M, E,
+                                       grad_logits.data_ptr(), _raw_stream(dev, stream))
+    if st:
+        _raise("moe_select_backward", st)
     return grad_logits
 
 
@@ -724,80 +730,87 @@ def moe_route_scored(x, w_router, routing: Routing, logit_bias=None, topk_ids=No
                      topk_weights=None, logits_out=None, ws=None, stream=None):
     """moe_route with a routing rule: (topk_ids, topk_weights)."""
     torch = _torch()
+    dev = x.get_device()
+    if not _current(dev):
+        return _elsewhere(dev, moe_route_scored, x, w_router, routing, logit_bias, topk_ids,
+                          topk_weights, logits_out, ws, stream)
     M, H = x.shape
     E = w_router.shape[0]
-    k = routing.top_k
-    dev = _device_of(x, "x")
+    out = (M, routing.top_k)
     _need(x, "x", torch.bfloat16, (M, H), dev)
     _need(w_router, "w_router", torch.bfloat16, (E, H), dev)
     if logit_bias is not None:
         _need(logit_bias, "logit_bias", torch.float32, (E,), dev)
-    rule = routing._arg(E, dev)
-    with _On(dev, stream) as on:
-        if topk_ids is None:
-            topk_ids = on.empty((M, k), torch.int32)
-        if topk_weights is None:
-            topk_weights = on.empty((M, k), torch.float32)
-        _need(topk_ids, "topk_ids", torch.int32, (M, k), dev)
-        _need(topk_weights, "topk_weights", torch.float32, (M, k), dev)
-        if logits_out is not None:
-            _need(logits_out, "logits_out", torch.float32, (M, E), dev)
-        elif ws is None:
-            ws = on.empty((max(M * E * 4, 16),), torch.uint8)
-        if ws is not None:
-            _need(ws, "ws", torch.uint8, (ws.numel(),), dev)
-        st = library().moe_route_scored(
-            x.data_ptr(), w_router.data_ptr(), _ptr(logit_bias), rule, M, H, E,
-            topk_ids.data_ptr(), topk_weights.data_ptr(), _ptr(logits_out), _ptr(ws),
-            0 if ws is None else ws.numel(), on.stream)
-    _raise("moe_route_scored", st)
+    if topk_ids is None:
+        topk_ids = _empty(out, torch.int32, dev, stream)
+    else:
+        _need(topk_ids, "topk_ids", torch.int32, out, dev)
+    if topk_weights is None:
+        topk_weights = _empty(out, torch.float32, dev, stream)
+    else:
+        _need(topk_weights, "topk_weights", torch.float32, out, dev)
+    if logits_out is not None:
+        _need(logits_out, "logits_out", torch.float32, (M, E), dev)
+    elif ws is None:
+        ws = _empty((max(M * E * 4, 16),), torch.uint8, dev, stream)
+    if ws is not None:
+        _need(ws, "ws", torch.uint8, (ws.numel(),), dev)
+    st = library().moe_route_scored(
+        x.data_ptr(), w_router.data_ptr(), _ptr(logit_bias), routing._arg(E, dev), M, H, E,
+        topk_ids.data_ptr(), topk_weights.data_ptr(), _ptr(logits_out), _ptr(ws),
+        0 if ws is None else ws.numel(), _raw_stream(dev, stream))
+    if st:
+        _raise("moe_route_scored", st)
     return topk_ids, topk_weights
 
 
 def _layer_scored(call: str, x, w_router, routing: Routing, weights, weight_args, I: int, ws_size,
                   logit_bias, out, topk_ids_out, topk_weights_out, ws, stream):
-    """A layer call with a routing rule: ``weights`` are (name, tensor, dtype
-    or None for int32/uint32 words, shape) to check, ``weight_args`` what the C call
-    takes for them."""
+    """A layer call with a routing rule: ``weights`` are (name, tensor, dtype,
+    shape) to check, ``weight_args`` what the C call takes for them."""
     torch = _torch()
+    dev = x.get_device()
+    if not _current(dev):
+        return _elsewhere(dev, _layer_scored, call, x, w_router, routing, weights, weight_args, I,
+                          ws_size, logit_bias, out, topk_ids_out, topk_weights_out, ws, stream)
     M, H = x.shape
     E = w_router.shape[0]
     k = routing.top_k
-    dev = _device_of(x, "x")
     _need(x, "x", torch.bfloat16, (M, H), dev)
     _need(w_router, "w_router", torch.bfloat16, (E, H), dev)
     for name, t, dtype, shape in weights:
-        _need(t, name, t.dtype if dtype is None and t.dtype in _words() else dtype or torch.int32,
-              shape, dev)
+        _need(t, name, dtype, shape, dev)
     if logit_bias is not None:
         _need(logit_bias, "logit_bias", torch.float32, (E,), dev)
-    rule = routing._arg(E, dev)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = on.empty((M, H), torch.bfloat16)
+    if out is None:
+        out = _empty((M, H), torch.bfloat16, dev, stream)
+    else:
         _need(out, "out", torch.bfloat16, (M, H), dev)
-        if topk_ids_out is not None:
-            _need(topk_ids_out, "topk_ids_out", torch.int32, (M, k), dev)
-        if topk_weights_out is not None:
-            _need(topk_weights_out, "topk_weights_out", torch.float32, (M, k), dev)
-        if ws is None:
-            n = ws_size(M, E, k, H, I)
-            if n == 0:
-                raise MoeError(call, -2)
-            ws = on.empty((n,), torch.uint8)
+    if topk_ids_out is not None:
+        _need(topk_ids_out, "topk_ids_out", torch.int32, (M, k), dev)
+    if topk_weights_out is not None:
+        _need(topk_weights_out, "topk_weights_out", torch.float32, (M, k), dev)
+    if ws is None:
+        n = ws_size(M, E, k, H, I)
+        if n == 0:
+            raise MoeError(call, -2)
+        ws = _empty((n,), torch.uint8, dev, stream)
+    else:
         _need(ws, "ws", torch.uint8, (ws.numel(),), dev)
-        info = DispatchInfo()
-        st = getattr(library(), call)(
-            x.data_ptr(), w_router.data_ptr(), _ptr(logit_bias), rule, *weight_args, M, E, H, I,
-            out.data_ptr(), _ptr(topk_ids_out), _ptr(topk_weights_out), ws.data_ptr(), ws.numel(),
-            ctypes.byref(info), on.stream)
+    info = DispatchInfo()
+    st = getattr(library(), call)(
+        x.data_ptr(), w_router.data_ptr(), _ptr(logit_bias), routing._arg(E, dev), *weight_args, M,
+        E, H, I, out.data_ptr(), _ptr(topk_ids_out), _ptr(topk_weights_out), ws.data_ptr(),
+        ws.numel(), ctypes.byref(info), _raw_stream(dev, stream))
     _raise(call, st)
     return out, info.as_dict()
 
 
-def _words():
+def _word_type(t):
+    """The type that a tensor of packed code words has to have: int32, or
+    uint32 where it has that."""
     torch = _torch()
-    return (torch.int32, getattr(torch, "uint32", torch.int32))
+    return t.dtype if t.dtype is getattr(torch, "uint32", None) else torch.int32
 
 
 def moe_forward_scored(x, w_router, w13, w2, routing: Routing, logit_bias=None, out=None,
@@ -831,7 +844,7 @@ def moe_forward_quantized_scored(x, w_router, qweights: dict, routing: Routing, 
                           *(qweights[n].data_ptr() for n in names))
     return _layer_scored(
         "moe_forward_quantized_scored", x, w_router, routing,
-        tuple((n, qweights[n], None if n.endswith("_q") else bf16, s)
+        tuple((n, qweights[n], _word_type(qweights[n]) if n.endswith("_q") else bf16, s)
               for n, s in zip(names, shapes)),
         (ctypes.byref(qw),), I, moe_workspace_size, logit_bias, out, topk_ids_out,
         topk_weights_out, ws, stream)
@@ -863,6 +876,10 @@ def moe_linear_quantized(x, weight: dict, gated: bool = False, row_scale=None, a
     ``row_scale`` [M] fp32 and ``addend`` [M, n_out] bf16 (``out`` itself, to
     add in place) are optional."""
     torch = _torch()
+    dev = x.get_device()
+    if not _current(dev):
+        return _elsewhere(dev, moe_linear_quantized, x, weight, gated, row_scale, addend, out,
+                          stream)
     bf16 = torch.bfloat16
     M, K = x.shape
     q, scales, biases = weight["q"], weight["scales"], weight["biases"]
@@ -870,23 +887,23 @@ def moe_linear_quantized(x, weight: dict, gated: bool = False, row_scale=None, a
     if bits != 4 or group not in (32, 64, 128) or K % group != 0:
         raise MoeError("moe_linear_quantized", -2)
     N = q.shape[0]
-    n_out = N // 2 if gated else N
-    dev = _device_of(x, "x")
+    shape = (M, N // 2 if gated else N)
     _need(x, "x", bf16, (M, K), dev)
-    _need(q, "q", q.dtype if q.dtype in _words() else torch.int32, (N, K // 8), dev)
+    _need(q, "q", _word_type(q), (N, K // 8), dev)
     _need(scales, "scales", bf16, (N, K // group), dev)
     _need(biases, "biases", bf16, (N, K // group), dev)
     if row_scale is not None:
         _need(row_scale, "row_scale", torch.float32, (M,), dev)
     if addend is not None:
-        _need(addend, "addend", bf16, (M, n_out), dev)
+        _need(addend, "addend", bf16, shape, dev)
+    if out is None:
+        out = _empty(shape, bf16, dev, stream)
+    else:
+        _need(out, "out", bf16, shape, dev)
     w = QuantizedMatrix(bits, group, q.data_ptr(), scales.data_ptr(), biases.data_ptr())
-    with _On(dev, stream) as on:
-        if out is None:
-            out = on.empty((M, n_out), bf16)
-        _need(out, "out", bf16, (M, n_out), dev)
-        st = library().moe_linear_quantized(x.data_ptr(), ctypes.addressof(w), M, N, K,
-                                            int(bool(gated)), _ptr(row_scale), _ptr(addend),
-                                            out.data_ptr(), on.stream)
-    _raise("moe_linear_quantized", st)
+    st = library().moe_linear_quantized(x.data_ptr(), ctypes.addressof(w), M, N, K,
+                                        1 if gated else 0, _ptr(row_scale), _ptr(addend),
+                                        out.data_ptr(), _raw_stream(dev, stream))
+    if st:
+        _raise("moe_linear_quantized", st)
     return out

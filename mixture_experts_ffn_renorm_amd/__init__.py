@@ -876,16 +876,16 @@ def moe_linear_quantized(x, weight: dict, gated: bool = False, row_scale=None, a
     ``row_scale`` [M] fp32 and ``addend`` [M, n_out] bf16 (``out`` itself, to
     add in place) are optional."""
     torch = _torch()
+    M, K = x.shape
+    bits, group = int(weight["bits"]), int(weight.get("group_size", 64))
+    if bits != 4 or group not in (32, 64, 128) or K % group != 0:
+        raise MoeError("moe_linear_quantized", -2)
     dev = x.get_device()
     if not _current(dev):
         return _elsewhere(dev, moe_linear_quantized, x, weight, gated, row_scale, addend, out,
                           stream)
     bf16 = torch.bfloat16
-    M, K = x.shape
     q, scales, biases = weight["q"], weight["scales"], weight["biases"]
-    bits, group = int(weight["bits"]), int(weight.get("group_size", 64))
-    if bits != 4 or group not in (32, 64, 128) or K % group != 0:
-        raise MoeError("moe_linear_quantized", -2)
     N = q.shape[0]
     shape = (M, N // 2 if gated else N)
     _need(x, "x", bf16, (M, K), dev)

@@ -444,7 +444,7 @@ typedef struct moe_routing {
                                  at least top_k experts                          */
   int group_top;              /* 1 or 2 (at most E/n_group where n_group > 1)    */
   float scale;                /* finite factor of every weight                   */
-  const float* select_bias;   /* [E] fp32 or NULL                                */
+  const float* select_bias;   /* [E] fp32, 16-byte aligned, or NULL              */
 } moe_routing;
 
 /*

@@ -132,6 +132,7 @@ int check_routing(const moe_routing* r, int E) {
   // the groups that stay have to hold top_k experts
   if ((long long)r->topk_group * (E / G) < r->top_k) return MOE_ERR_INVALID_ARG;
   if (G > kMaxGroups) return MOE_ERR_UNSUPPORTED;
+  if (!a16(r->select_bias)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 

@@ -220,6 +220,18 @@ __device__ __forceinline__ float row16_max(float v) {
   v = dpp_max_with<0x140>(v);   // row_mirror
   return v;
 }
+// Lane swaps (gfx950): the upper half of a's lanes with the lower half of
+// b's; in each half, a's odd row of 16 lanes with b's even row.
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
 __device__ __forceinline__ float wave_sum(float v) {
   v = group_sum_last<64>(v);
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));

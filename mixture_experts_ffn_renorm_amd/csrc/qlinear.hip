@@ -25,17 +25,6 @@ namespace {
 // register holds one group (two or four lane-swap instructions per block).
 constexpr int kBlockK = 128;
 
-__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
-  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
-  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-
 // Words of a block so that words [j * G/32, (j + 1) * G/32) are group j's.
 template <int G>
 __device__ __forceinline__ void group_words(u32x4& w) {

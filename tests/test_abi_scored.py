@@ -168,3 +168,9 @@ def test_binding_refuses_host_tensors_and_bad_rules():
         moe.moe_linear_quantized(torch.zeros(3, 64, dtype=torch.bfloat16), w)
     with pytest.raises(moe.MoeError):
         moe.moe_linear_quantized(torch.zeros(3, 64, dtype=torch.bfloat16), dict(w, bits=8))
+
+
+def test_misaligned_bias():
+    lib = _moe().library()
+    c = rule(bias=ODD)
+    assert lib.moe_select(FAKE, ctypes.addressof(c), 4, 256, FAKE, FAKE, NULL) == -1

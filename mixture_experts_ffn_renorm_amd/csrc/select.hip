@@ -20,7 +20,6 @@ namespace {
 
 constexpr int kSelMaxE = 512;
 constexpr int kSelWaves = 4;
-constexpr int kCands = 64;          // candidates a token may have
 
 // Order-preserving 64-bit key: larger value, larger key; -0 and +0 equal;
 // -inf above NaN above 0, the key of an expert that cannot be chosen.
@@ -28,6 +27,56 @@ __device__ __forceinline__ uint64_t choice_key(double v) {
   if (v != v) return 1ull;
   const uint64_t u = (uint64_t)__builtin_bit_cast(long long, v + 0.0);
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+
+__device__ __forceinline__ double key_value(uint64_t k) {
+  if (k <= 1ull) return __builtin_nan("");
+  return __builtin_bit_cast(double, (long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
+}
+
+// Unsigned maximum over the wave, in every lane.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_umax_with(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xf, 0xf, false));
+}
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  v = dpp_umax_with<0xb1>(v);    // quad_perm [1, 0, 3, 2]
+  v = dpp_umax_with<0x4e>(v);    // quad_perm [2, 3, 0, 1]
+  v = dpp_umax_with<0x141>(v);   // row_half_mirror
+  v = dpp_umax_with<0x140>(v);   // row_mirror
+  uint32_t a = v, b = v;
+  swap16(a, b);
+  a = b = max(a, b);
+  swap32(a, b);
+  return max(a, b);
+}
+
+// e^x: x = n ln 2 + r with |r| <= ln 2 / 2 (ln 2 in two parts), the Taylor
+// series of e^r to r^13 / 13! (the next term is below 2^-57), times 2^n.
+// The constants are made opaque scalars where they are used: the compiler
+// would hold two dozen of them in vector registers through the kernel.
+__device__ __forceinline__ double exp_f64(double x) {
+  const double c = fmin(fmax(x, -800.0), 800.0);
+  double log2e = 0x1.71547652b82fep+0, ln2_hi = -0x1.62e42fefa39efp-1;
+  double ln2_lo = -0x1.abc9e3b39803fp-56;
+  asm volatile("" : "+s"(log2e), "+s"(ln2_hi), "+s"(ln2_lo));
+  const double n = __builtin_rint(c * log2e);
+  const double r = __builtin_fma(n, ln2_lo, __builtin_fma(n, ln2_hi, c));
+  double p = 1.0 / 6227020800.0;
+  asm volatile("" : "+s"(p));
+  double y = p;
+  constexpr double kInv[] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0,
+                             1.0 / 40320.0,     1.0 / 5040.0,     1.0 / 720.0,     1.0 / 120.0,
+                             1.0 / 24.0,        1.0 / 6.0};
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    double q = kInv[i];
+    asm volatile("" : "+s"(q));
+    y = __builtin_fma(y, r, q);
+  }
+  y = __builtin_fma(__builtin_fma(__builtin_fma(y, r, 0.5), r, 1.0), r, 1.0);
+  y = __builtin_ldexp(y, (int)n);
+  return x != x ? x : y;
 }
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
@@ -114,21 +163,25 @@ struct SelectParams {
 // E doubles of this wave.  Kept small (no unrolled element loops): it runs
 // seldom.
 __device__ __forceinline__ void select_exactly(const SelectParams& a, int t, double* c) {
-  const int lane = threadIdx.x & 63;
-  const int E = a.E, k = a.top_k;
+  int lane = threadIdx.x & 63, E = a.E, G = a.n_group;
+  const int k = a.top_k;
+  // opaque here, so that nothing computed from them is held in registers
+  // through the fp32 pass
+  asm volatile("" : "+v"(lane));
+  asm volatile("" : "+s"(E), "+s"(G));
   const float* row = a.logits + (size_t)t * E;
   float mx = -INFINITY;
 #pragma unroll 1
   for (int e = lane; e < E; e += 64) mx = fmaxf(mx, row[e]);
   mx = wave_max(mx);
-  const bool scored = a.bias != nullptr || (a.n_group > 1 && a.group_top == 2);
+  const bool scored = a.bias != nullptr || (G > 1 && a.group_top == 2);
   if (scored) {
     // sigmoid: e^-l, softmax: e^(l - mx), summed
     const double sign = a.sigmoid ? -1.0 : 1.0, shift = a.sigmoid ? 0.0 : (double)mx;
     double z = 0.0;
 #pragma unroll 1
     for (int e = lane; e < E; e += 64) {
-      const double v = exp(sign * ((double)row[e] - shift));
+      const double v = exp_f64(sign * ((double)row[e] - shift));
       c[e] = v;
       z += v;
     }
@@ -147,66 +200,72 @@ __device__ __forceinline__ void select_exactly(const SelectParams& a, int t, dou
   }
   __builtin_amdgcn_wave_barrier();
   unsigned long long kept = ~0ull;
-  const int gs = E / a.n_group;
-  if (a.n_group > 1) {
-    // lane g scores group g (at most 64)
-    uint64_t gkey = 0ull;
-    if (lane < a.n_group) {
-      uint64_t k1 = 0ull, k2 = 0ull;
-      double v1 = 0.0, v2 = 0.0;
+  const int gs = E / G;
+  if (G > 1) {
+    // 64 / n_group lanes scan a group (n_group <= 64) and join their two best
+    const int lpg = 64 / G;
+    const int g = min(lane / lpg, G - 1), sub = lane - g * lpg;
+    uint64_t k1 = 0ull, k2 = 0ull;   // keys order as the values do
 #pragma unroll 1
-      for (int j = 0; j < gs; ++j) {
-        const double v = c[lane * gs + j];
-        const uint64_t q = choice_key(v);
-        if (q > k1) {
-          k2 = k1; v2 = v1;
-          k1 = q; v1 = v;
-        } else if (q > k2) {
-          k2 = q; v2 = v;
-        }
-      }
-      gkey = choice_key(a.group_top == 2 ? v1 + v2 : v1);
+    for (int j = sub; j < gs && sub < lpg; j += lpg) {
+      const uint64_t q = choice_key(c[g * gs + j]);
+      k2 = max(k2, min(k1, q));
+      k1 = max(k1, q);
     }
+    const uint64_t o1 = k1, o2 = k2;
+#pragma unroll 1
+    for (int o = 1; o < lpg; ++o) {
+      const int src = sub < lpg ? g * lpg + (sub + o) % lpg : lane;
+      const uint64_t p1 = __shfl(o1, src, kWave), p2 = __shfl(o2, src, kWave);
+      k2 = max(max(k2, p2), min(k1, p1));
+      k1 = max(k1, p1);
+    }
+    if (a.group_top == 2) k1 = choice_key(key_value(k1) + key_value(k2));
     int rank = 0;
-#pragma unroll 1
-    for (int g = 0; g < a.n_group; ++g) {
-      const uint64_t o = __shfl(gkey, g, kWave);
-      rank += (o > gkey) | ((o == gkey) & (g < lane));
+#pragma unroll 2
+    for (int o = 0; o < G; ++o) {
+      const uint64_t other = __shfl(k1, o * lpg, kWave);
+      rank += (other > k1) | ((other == k1) & (o < g));
     }
-    kept = __ballot(lane < a.n_group && rank < a.topk_group);
-  }
-  __builtin_amdgcn_wave_barrier();
-  // without a bias the order is the logits'
-  unsigned open = 0u;   // bit i: expert lane + 64 i can still be chosen
+    // bit g: group g stays
+    const unsigned long long m = __ballot(rank < a.topk_group && sub == 0);
+    kept = 0ull;
 #pragma unroll 1
-  for (int i = 0, e = lane; e < E; ++i, e += 64) {
-    if (a.bias == nullptr) c[e] = (double)row[e];
-    if (a.n_group == 1 || ((kept >> (e / gs)) & 1ull)) open |= 1u << i;
+    for (int o = 0; o < G; ++o) kept |= ((m >> (o * lpg)) & 1ull) << o;
   }
-  // top_k times the largest key, the lowest expert id among equals
+  // without a bias the order is the logits'
+  constexpr int kPer = kSelMaxE / 64;
+  uint32_t hi[kPer], lo[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane + 64 * i;
+    uint64_t q = 0ull;
+    if (e < E && (G == 1 || ((kept >> (e / gs)) & 1ull)))
+      q = choice_key(a.bias != nullptr ? c[e] : (double)row[e]);
+    hi[i] = (uint32_t)(q >> 32);
+    lo[i] = (uint32_t)q;
+  }
+  // top_k times the largest key, the lowest expert id among equals: the
+  // largest upper half, then the largest lower half of those, then the id
   int my_id = 0;
 #pragma unroll 1
   for (int j = 0; j < k; ++j) {
-    uint64_t best = 0ull;
-    int at = kSelMaxE;
-#pragma unroll 1
-    for (int i = 0, e = lane; e < E; ++i, e += 64) {
-      const uint64_t q = (open >> i) & 1u ? choice_key(c[e]) : 0ull;
-      if (q > best) {
-        best = q;
-        at = e;
-      }
-    }
-#pragma unroll 1
-    for (int d = 32; d >= 1; d >>= 1) {
-      const uint64_t ob = __shfl_xor(best, d, kWave);
-      const int oa = __shfl_xor(at, d, kWave);
-      if (ob > best || (ob == best && oa < at)) {
-        best = ob;
-        at = oa;
-      }
-    }
-    if ((at & 63) == lane) open &= ~(1u << (at >> 6));
+    uint32_t h = hi[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) h = max(h, hi[i]);
+    h = wave_umax(h);
+    uint32_t v = 0u;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v = max(v, hi[i] == h ? lo[i] : 0u);
+    v = wave_umax(v);
+    uint32_t first = 0u;   // kSelMaxE - id, the largest for the lowest id
+#pragma unroll
+    for (int i = kPer - 1; i >= 0; --i)
+      if (hi[i] == h && lo[i] == v) first = kSelMaxE - (lane + 64 * i);
+    const int at = kSelMaxE - (int)wave_umax(first);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (at == lane + 64 * i) hi[i] = lo[i] = 0u;
     if (lane == j) my_id = at;
   }
   const float l = lane < k ? row[my_id] : -INFINITY;
@@ -252,15 +311,17 @@ __device__ __forceinline__ void select_exactly(const SelectParams& a, int t, dou
 // hardware transcendentals, two roundings), softmax 2^-19 (the common sum of
 // C / 4 + 6 terms in a row, each rounding once), and 2^-24 |c| for the bias.
 template <int L, int C, int V>
-__global__ __launch_bounds__(64 * kSelWaves, C <= 8 ? 5 : C == 16 ? 4 : 3) void select_kernel(SelectParams a, int lpg) {
+__global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, int lpg) {
   constexpr int T = 64 / L;                    // tokens per wave
   constexpr int kList = 64;                    // rows to do over, per wave
+  // candidates a token may have: with eight lanes of sixteen experts open and
+  // top_k 8, 64 are too few for one token in 8000, 128 always enough
+  constexpr int kCands = L == 16 ? 128 : 64;
   struct TokenLds {
-    double c[kCands];                          // candidates: choice score, id, logit
-    int id[kCands];
-    float l[kCands];
+    double c[kCands];                          // candidates: choice score, id
+    uint16_t id[kCands];
     float lm[L];                               // lane maxima
-    float top_c[34], top_l[34];                // by rank
+    float top_c[34];                           // by rank
     int top_id[34];
   };
   union WaveLds {
@@ -270,13 +331,14 @@ __global__ __launch_bounds__(64 * kSelWaves, C <= 8 ? 5 : C == 16 ? 4 : 3) void 
   __shared__ __attribute__((aligned(16))) WaveLds s_all[kSelWaves];
   __shared__ int s_list[kSelWaves][kList];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int li = lane % L, base = lane - li;   // lane within its token
+  int li = lane % L, base = lane - li;         // lane within its token
   TokenLds& s = s_all[w].tok[lane / L];
   const int E = a.E, k = a.top_k, G = a.n_group;
   const int gs = E / G;
   const int grp = li / lpg, sub = li - grp * lpg;
   const bool scored = a.bias != nullptr || (G > 1 && a.group_top == 2);
   const bool by_logit = a.bias == nullptr;     // the order of experts is exact
+  const bool refine = !by_logit && a.sigmoid;  // candidates evaluated again
   const float eps = a.sigmoid ? 0x1p-21f : 0x1p-18f;   // of a difference of two c
   // first expert of piece i: lane_e0 + i * V * lpg; present while below lane_end
   int lane_e0 = grp * gs + V * sub;
@@ -289,8 +351,9 @@ __global__ __launch_bounds__(64 * kSelWaves, C <= 8 ? 5 : C == 16 ? 4 : 3) void 
     int nlist = 0;
 #pragma unroll 1
     for (; t0 < a.M && nlist <= kList - T; t0 += step) {
-      // keeps each expert's index from being held in a register of its own
-      asm volatile("" : "+v"(lane_e0));
+      // opaque in each turn, so that what is computed from them (the index of
+      // each expert, addresses) is not held in registers of its own
+      asm volatile("" : "+v"(lane_e0), "+v"(li), "+v"(base));
       const int t = t0 + lane / L;
       const bool live = t < a.M;
       const float* row = a.logits + (size_t)(live ? t : a.M - 1) * E;
@@ -425,20 +488,18 @@ __global__ __launch_bounds__(64 * kSelWaves, C <= 8 ? 5 : C == 16 ? 4 : 3) void 
       for (int i = 0; i < C; ++i)
         if (c[i] >= cut) {
           if (pos < kCands) {
-            s.c[pos] = (double)c[i];
-            s.l[pos] = l[i];
-            s.id[pos] = expert(i);
+            s.c[pos] = (double)(refine ? l[i] : c[i]);
+            s.id[pos] = (uint16_t)expert(i);
           }
           ++pos;
         }
       unsure = unsure || total < k || total > kCands;
       const int most = min(kCands, (int)wave_max((float)total));
       __builtin_amdgcn_wave_barrier();
-      if (!by_logit && a.sigmoid) {
+      if (refine) {
 #pragma unroll 1
         for (int q = li; q < most; q += L)
-          if (q < total)
-            s.c[q] = 1.0 / (1.0 + exp(-(double)s.l[q])) + (double)a.bias[s.id[q]];
+          if (q < total) s.c[q] = 1.0 / (1.0 + exp_f64(-s.c[q])) + (double)a.bias[s.id[q]];
         __builtin_amdgcn_wave_barrier();
       }
 #pragma unroll 1
@@ -453,7 +514,6 @@ __global__ __launch_bounds__(64 * kSelWaves, C <= 8 ? 5 : C == 16 ? 4 : 3) void 
         }
         if (q < total && rank <= k) {
           s.top_c[rank] = (float)my;
-          s.top_l[rank] = s.l[q];
           s.top_id[rank] = id;
         }
       }
@@ -462,8 +522,8 @@ __global__ __launch_bounds__(64 * kSelWaves, C <= 8 ? 5 : C == 16 ? 4 : 3) void 
       int id = 0;
       float lj = -INFINITY;
       if (li < k) {
-        id = s.top_id[li];
-        lj = s.top_l[li];
+        id = min(max(s.top_id[li], 0), E - 1);   // unset in a row that is done over
+        lj = by_logit ? s.top_c[li] : row[id];
       }
       if (!by_logit && !a.sigmoid) {
         bool close = false;

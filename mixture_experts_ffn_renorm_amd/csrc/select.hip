@@ -34,6 +34,22 @@ __device__ __forceinline__ double key_value(uint64_t k) {
   return __builtin_bit_cast(double, (long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
 }
 
+// A candidate's key: fp32 value in order, then the lower id first; distinct
+// ids give distinct keys.  (A sigmoid's refined key: a double's upper 55 bits
+// in order, then the id.)
+__device__ __forceinline__ uint64_t cand_key(float v, int id) {
+  uint32_t u = __float_as_uint(v + 0.f);   // -0 as +0
+  u = (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  return ((uint64_t)u << 32) | (uint32_t)(kSelMaxE - 1 - id);
+}
+__device__ __forceinline__ int cand_id(uint64_t key) {
+  return kSelMaxE - 1 - (int)(key & (kSelMaxE - 1));
+}
+__device__ __forceinline__ float cand_value(uint64_t key) {
+  const uint32_t u = (uint32_t)(key >> 32);
+  return __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u);
+}
+
 // Unsigned maximum over the wave, in every lane.
 template <int kCtrl>
 __device__ __forceinline__ uint32_t dpp_umax_with(uint32_t v) {
@@ -126,6 +142,23 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+// Inclusive prefix sums over aligned groups of L lanes (DPP shifts inside a
+// row of 16, then each row's total into the next rows).
+template <int kCtrl, int kRowMask, bool kBound>
+__device__ __forceinline__ int dpp_shifted_addi(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, kCtrl, kRowMask, 0xf, kBound);
+}
+template <int L>
+__device__ __forceinline__ int lanes_scan(int v) {
+  v = dpp_shifted_addi<0x111, 0xf, true>(v);    // row_shr:1
+  v = dpp_shifted_addi<0x112, 0xf, true>(v);    // row_shr:2
+  v = dpp_shifted_addi<0x114, 0xf, true>(v);    // row_shr:4
+  v = dpp_shifted_addi<0x118, 0xf, true>(v);    // row_shr:8
+  if (L >= 32) v = dpp_shifted_addi<0x142, 0xa, false>(v);   // row_bcast:15
+  if (L == 64) v = dpp_shifted_addi<0x143, 0xc, false>(v);   // row_bcast:31
+  return v;
+}
+
 // sum over the first n lanes of a wave in lane order, in every lane
 __device__ __forceinline__ float lane0_sum(float v, int n) {
   float s = 0.f;
@@ -148,6 +181,15 @@ __device__ __forceinline__ float sigmoid_f32(float l) {
 }
 
 constexpr float kLog2e = 1.44269504f;
+
+// The same on the hardware's exponential (one ulp; the rounding of its
+// argument adds |x| 2^-24 relative): shift is m for the softmax, min(m, 0)
+// for a sigmoid, and finite.
+__device__ __forceinline__ float hw_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+__device__ __forceinline__ float fast_score(float l, float shift, bool sigmoid) {
+  const float e = hw_exp(l >= 0.f && sigmoid ? 0.f : l - shift);
+  return sigmoid ? e * __builtin_amdgcn_rcpf(1.f + hw_exp(-fabsf(l))) : e;
+}
 
 struct SelectParams {
   const float* logits;
@@ -318,11 +360,10 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
   // top_k 8, 64 are too few for one token in 8000, 128 always enough
   constexpr int kCands = L == 16 ? 128 : 64;
   struct TokenLds {
-    double c[kCands];                          // candidates: choice score, id
-    uint16_t id[kCands];
+    uint64_t cand[kCands];                     // candidates' keys
+    uint64_t top[34];                          // by rank
     float lm[L];                               // lane maxima
-    float top_c[34];                           // by rank
-    int top_id[34];
+    uint16_t id[kCands];
   };
   union WaveLds {
     TokenLds tok[T];
@@ -372,7 +413,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
       }
       // the softmax over all experts, where it is needed
       const bool full = !a.sigmoid && (scored || !a.renormalize);
-      float mx = -INFINITY, z = 0.f;
+      float mx = -INFINITY, z = 0.f, rz = 0.f;
       if (full) {
 #pragma unroll
         for (int i = 0; i < C; ++i) mx = fmaxf(mx, l[i]);
@@ -391,21 +432,22 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
           for (int i = 0; i < C; ++i)
             c[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * l[i]));
         } else {
-          const float rz = 1.f / z;
+          rz = __builtin_amdgcn_rcpf(z);
 #pragma unroll
           for (int i = 0; i < C; ++i) c[i] *= rz;
         }
+        // experts that are not there: -inf for their bias
 #pragma unroll
         for (int i = 0; i < C; i += V) {
           const int e = expert(i);
+          const float none = e < lane_end ? 0.f : -INFINITY;
           if constexpr (V == 4) {
-            f32x4 b = {0.f, 0.f, 0.f, 0.f};
-            if (a.bias != nullptr) b = *reinterpret_cast<const f32x4*>(a.bias + min(e, E - 4));
+            f32x4 b = {none, none, none, none};
+            if (a.bias != nullptr && e < lane_end) b = *reinterpret_cast<const f32x4*>(a.bias + e);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[i + j] = e < lane_end ? c[i + j] + b[j] : -INFINITY;
+            for (int j = 0; j < 4; ++j) c[i + j] += b[j];
           } else {
-            const float b = a.bias != nullptr ? a.bias[min(e, E - 1)] : 0.f;
-            c[i] = e < lane_end ? c[i] + b : -INFINITY;
+            c[i] += a.bias != nullptr && e < lane_end ? a.bias[e] : none;
           }
         }
       } else {
@@ -446,20 +488,17 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
           // a group of -inf (or NaN) alone among those that stay
           unsure = lanes_max<L>(open && !(score > -INFINITY) ? 1.f : 0.f) > 0.f;
         }
+        if (scored && by_logit) {
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-          if (by_logit) c[i] = l[i];
-          if (!open) c[i] = -INFINITY;
+          for (int i = 0; i < C; ++i) c[i] = l[i];
         }
       }
       // the bound
       float lmax = c[0];
 #pragma unroll
       for (int i = 1; i < C; ++i) lmax = fmaxf(lmax, c[i]);
-      if (lmax != lmax) lmax = -INFINITY;
+      if (lmax != lmax || !open) lmax = -INFINITY;
       s.lm[li] = lmax;
-#pragma unroll
-      for (int i = 0; i < kCands / L; ++i) s.c[i * L + li] = -INFINITY;
       __builtin_amdgcn_wave_barrier();
       int gt = 0;
 #pragma unroll
@@ -471,78 +510,85 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
       const float bound = -lanes_max<L>(gt < k ? -lmax : -INFINITY);
       const float tol = by_logit ? 0.f : 2.f * eps + 0x1p-22f * fabsf(bound);
       // fewer than top_k lanes hold anything: every finite expert
-      const float cut = bound > -INFINITY ? bound - tol : -3.4028235e38f;
-      // candidates into LDS
-      int n = 0;
+      const float cut = !open ? INFINITY : bound > -INFINITY ? bound - tol : -3.4028235e38f;
+      // this lane's candidates, expert i at bit C - 1 - i
+      uint32_t mask = 0u;
 #pragma unroll
-      for (int i = 0; i < C; ++i) n += c[i] >= cut;
-      int pos = n;
-#pragma unroll
-      for (int d = 1; d < L; d <<= 1) {
-        const int o = __shfl_up(pos, d, L);
-        if (li >= d) pos += o;
-      }
-      const int total = __shfl(pos, base + L - 1, kWave);
-      pos -= n;
-#pragma unroll
-      for (int i = 0; i < C; ++i)
-        if (c[i] >= cut) {
-          if (pos < kCands) {
-            s.c[pos] = (double)(refine ? l[i] : c[i]);
-            s.id[pos] = (uint16_t)expert(i);
-          }
+      for (int i = 0; i < C; ++i) mask = 2u * mask + (c[i] >= cut ? 1u : 0u);
+      if (!open) mask = 0u;   // +inf is no candidate either
+      const int n = __popc(mask);
+      const int upto = lanes_scan<L>(n);
+      const int total = (int)lanes_max<L>((float)upto);
+      unsure = unsure || total < k || total > kCands;
+      const int most = min(kCands, (int)lanes_max<64>((float)total));
+      int pos = upto - n;
+      while (__any(mask != 0u)) {
+        if (mask != 0u) {
+          const int i = C - 32 + __clz(mask);
+          if (pos < kCands) s.id[pos] = (uint16_t)expert(i);
+          mask &= ~(0x80000000u >> __clz(mask));
           ++pos;
         }
-      unsure = unsure || total < k || total > kCands;
-      const int most = min(kCands, (int)wave_max((float)total));
-      __builtin_amdgcn_wave_barrier();
-      if (refine) {
-#pragma unroll 1
-        for (int q = li; q < most; q += L)
-          if (q < total) s.c[q] = 1.0 / (1.0 + exp_f64(-s.c[q])) + (double)a.bias[s.id[q]];
-        __builtin_amdgcn_wave_barrier();
       }
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
       for (int q = li; q < most; q += L) {
-        const double my = s.c[q];
-        const int id = s.id[q];
+        uint64_t key = 0ull;
+        if (q < total) {
+          const int id = s.id[q];
+          const float v = row[id];
+          if (refine) {
+            const double u = 1.0 + exp_f64(-(double)v);
+            key = (choice_key(1.0 / u + (double)a.bias[id]) & ~(uint64_t)(kSelMaxE - 1)) |
+                  (uint64_t)(kSelMaxE - 1 - id);
+          } else {
+            key = cand_key(by_logit ? v : hw_exp(v - mx) * rz + a.bias[id], id);
+          }
+        }
+        s.cand[q] = key;
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+      for (int q = li; q < most; q += L) {
+        const uint64_t my = s.cand[q];
         int rank = 0;
 #pragma unroll 4
-        for (int o = 0; o < most; ++o) {
-          const double ot = s.c[o];
-          rank += (ot > my) | ((ot == my) & (s.id[o] < id));
-        }
-        if (q < total && rank <= k) {
-          s.top_c[rank] = (float)my;
-          s.top_id[rank] = id;
-        }
+        for (int o = 0; o < most; ++o) rank += s.cand[o] > my;
+        if (q < total && rank <= k) s.top[rank] = my;
       }
       __builtin_amdgcn_wave_barrier();
       // lane j: slot j
       int id = 0;
       float lj = -INFINITY;
       if (li < k) {
-        id = min(max(s.top_id[li], 0), E - 1);   // unset in a row that is done over
-        lj = by_logit ? s.top_c[li] : row[id];
-      }
-      if (!by_logit && !a.sigmoid) {
-        bool close = false;
-        if (li < k && li + 1 < total) {
-          const float my = s.top_c[li], nx = s.top_c[li + 1];
-          close = !(my - nx > eps + 0x1p-22f * fmaxf(fabsf(my), fabsf(nx)));
+        const uint64_t my = s.top[li];
+        id = min(cand_id(my), E - 1);   // unset in a row that is done over
+        lj = by_logit ? cand_value(my) : row[id];
+        if (!by_logit && li + 1 < total) {
+          const uint64_t nx = s.top[li + 1];
+          bool close;
+          if (refine) {
+            // the keys dropped the last nine bits, and the doubles are an
+            // ulp or two off
+            close = my - nx < 2ull * kSelMaxE;
+          } else {
+            const float x = cand_value(my), y = cand_value(nx);
+            close = !(x - y > eps + 0x1p-22f * fmaxf(fabsf(x), fabsf(y)));
+          }
+          unsure = unsure || close;
         }
-        unsure = unsure || lanes_max<L>(close ? 1.f : 0.f) > 0.f;
       }
+      if (!by_logit) unsure = lanes_max<L>(unsure ? 1.f : 0.f) > 0.f;
       float wt;
       if (a.renormalize) {
         const float m = lanes_max<L>(lj);
-        const float sh = li < k ? shifted_score(lj, m, a.sigmoid != 0) : 0.f;
+        const float sh = li < k ? fast_score(lj, a.sigmoid ? fminf(m, 0.f) : m, a.sigmoid) : 0.f;
         const float sum = lanes_sum<L>(sh);
-        wt = sum == 0.f ? 0.f : a.scale * (sh / sum);
+        wt = sum == 0.f ? 0.f : a.scale * (sh * __builtin_amdgcn_rcpf(sum));
       } else if (a.sigmoid) {
-        wt = a.scale * sigmoid_f32(lj);
+        wt = a.scale * fast_score(lj, fminf(lj, 0.f), true) * (lj < 0.f ? hw_exp(lj) : 1.f);
       } else {
-        wt = a.scale * (expf(lj - mx) / z);
+        wt = a.scale * (hw_exp(lj - mx) * __builtin_amdgcn_rcpf(z));
       }
       if (live && !unsure && li < k) {
         a.ids[(size_t)t * k + li] = id;

@@ -159,13 +159,6 @@ __device__ __forceinline__ int lanes_scan(int v) {
   return v;
 }
 
-// sum over the first n lanes of a wave in lane order, in every lane
-__device__ __forceinline__ float lane0_sum(float v, int n) {
-  float s = 0.f;
-  for (int j = 0; j < n; ++j) s += __shfl(v, j, kWave);
-  return s;
-}
-
 // A chosen expert's score up to a factor common to the row, so that
 // renormalized weights stay right where every score underflows: softmax
 // e^(l - m), sigmoid e^(l - min(m, 0)) / (1 + e^l) (or its mirror for l >= 0),
@@ -186,6 +179,10 @@ constexpr float kLog2e = 1.44269504f;
 // argument adds |x| 2^-24 relative): shift is m for the softmax, min(m, 0)
 // for a sigmoid, and finite.
 __device__ __forceinline__ float hw_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+__device__ __forceinline__ float hw_sigmoid(float l) {
+  const float t = hw_exp(-fabsf(l));
+  return (l >= 0.f ? 1.f : t) * __builtin_amdgcn_rcpf(1.f + t);
+}
 __device__ __forceinline__ float fast_score(float l, float shift, bool sigmoid) {
   const float e = hw_exp(l >= 0.f && sigmoid ? 0.f : l - shift);
   return sigmoid ? e * __builtin_amdgcn_rcpf(1.f + hw_exp(-fabsf(l))) : e;
@@ -350,8 +347,9 @@ __device__ __forceinline__ void select_exactly(const SelectParams& a, int t, dou
 //    kCands candidates (rows of ties).
 //
 // Error of c: sigmoid 2^-22 (its slope times the exponent's rounding, two
-// hardware transcendentals, two roundings), softmax 2^-19 (the common sum of
-// C / 4 + 6 terms in a row, each rounding once), and 2^-24 |c| for the bias.
+// hardware transcendentals, two roundings), softmax 2^-19 of the largest
+// probability (the common sum of C / 4 + 6 terms in a row, each rounding
+// once), and 2^-24 |c| for the bias.
 template <int L, int C, int V>
 __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, int lpg) {
   constexpr int T = 64 / L;                    // tokens per wave
@@ -380,7 +378,6 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
   const bool scored = a.bias != nullptr || (G > 1 && a.group_top == 2);
   const bool by_logit = a.bias == nullptr;     // the order of experts is exact
   const bool refine = !by_logit && a.sigmoid;  // candidates evaluated again
-  const float eps = a.sigmoid ? 0x1p-21f : 0x1p-18f;   // of a difference of two c
   // first expert of piece i: lane_e0 + i * V * lpg; present while below lane_end
   int lane_e0 = grp * gs + V * sub;
   const int lane_end = grp < G ? (grp + 1) * gs : 0;
@@ -426,6 +423,9 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
         }
         z = lanes_sum<L>((zp[0] + zp[1]) + (zp[2] + zp[3]));
       }
+      // error of a difference of two c (the softmax's is relative to its
+      // largest probability, 1 / z)
+      const float eps = a.sigmoid ? 0x1p-21f : 0x1p-18f * __builtin_amdgcn_rcpf(z);
       if (scored) {
         if (a.sigmoid) {
 #pragma unroll
@@ -586,7 +586,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
         const float sum = lanes_sum<L>(sh);
         wt = sum == 0.f ? 0.f : a.scale * (sh * __builtin_amdgcn_rcpf(sum));
       } else if (a.sigmoid) {
-        wt = a.scale * fast_score(lj, fminf(lj, 0.f), true) * (lj < 0.f ? hw_exp(lj) : 1.f);
+        wt = a.scale * hw_sigmoid(lj);
       } else {
         wt = a.scale * (hw_exp(lj - mx) * __builtin_amdgcn_rcpf(z));
       }
@@ -605,8 +605,8 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
   }
 }
 
-// Gradient of the weights to the logits; one wave per token.  With s^ the
-// renormalized scores and d_j = scale * g_j:
+// Gradient of the weights to the logits, L lanes per token, slot j on lane j.
+// With s^ the renormalized scores and d_j = scale * g_j:
 //   renormalize   s_j (dL/ds_j) = s^_j (d_j - sum_i d_i s^_i)
 //   else          s_j (dL/ds_j) = s_j d_j
 //   sigmoid       dL/dl_j = (1 - s_j) * that, 0 for the other experts
@@ -614,66 +614,105 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
 //                 the others; else dL/dl_e = that - p_e sum_j p_j d_j
 // An id outside [0, E) takes no part; an id that a row holds twice gets both
 // slots' gradients, added in slot order.
-__global__ __launch_bounds__(256) void select_backward_wave_kernel(
-    const float* __restrict__ logits, const int32_t* __restrict__ topk_ids,
-    const float* __restrict__ grad_weights, int M, int E, int top_k, int sigmoid, int renormalize,
-    float scale, float* __restrict__ grad_logits) {
-  __shared__ float s_row[4][kSelMaxE];
+//
+// The slots' values go through a row of LDS that is zero elsewhere: it is
+// read in pieces of V experts, stored, and cleared again at the slots alone.
+// Bound by the stores of [M, E].
+template <int L, int V>
+__global__ __launch_bounds__(64 * kSelWaves) void select_backward_kernel(
+    SelectParams a, const float* __restrict__ grad_weights, float* __restrict__ grad_logits) {
+  constexpr int T = 64 / L;
+  __shared__ __attribute__((aligned(16))) float s_row[kSelWaves][T][kSelMaxE];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const long long t = (long long)blockIdx.x * 4 + w;
-  if (t >= M) return;   // whole wave; no workgroup barrier below
-  const float* row = logits + (size_t)t * E;
-  float* out = s_row[w];
-  int id = -1;
-  float l = -INFINITY, d = 0.f;
-  if (lane < top_k) {
-    id = topk_ids[(size_t)t * top_k + lane];
-    if (id < 0 || id >= E) id = -1;
-    if (id >= 0) {
-      l = row[id];
-      d = scale * grad_weights[(size_t)t * top_k + lane];
+  const int li = lane % L, base = lane - li;
+  const int E = a.E, k = a.top_k;
+  const bool sigmoid = a.sigmoid != 0, dense = !sigmoid && !a.renormalize;
+  float* r = s_row[w][lane / L];
+  for (int e = li; e < E; e += L) r[e] = 0.f;
+  __builtin_amdgcn_wave_barrier();
+  const int step = (int)gridDim.x * kSelWaves * T;
+#pragma unroll 1
+  for (int t0 = ((int)blockIdx.x * kSelWaves + w) * T; t0 < a.M; t0 += step) {
+    const bool live = t0 + lane / L < a.M;
+    const int t = live ? t0 + lane / L : a.M - 1;
+    const float* row = a.logits + (size_t)t * E;
+    int id = -1;
+    float d = 0.f;
+    if (li < k) {
+      id = a.ids[(size_t)t * k + li];
+      d = a.scale * grad_weights[(size_t)t * k + li];
     }
+    const bool used = id >= 0 && id < E;
+    const float l = used ? row[id] : -INFINITY;
+    if (!used) d = 0.f;
+    float mx = -INFINITY, rz = 0.f;
+    if (dense) {
+      // maximum and sum of exponentials of the row, one pass
+      float z = 0.f;
+      for (int e = li; e < E; e += L) {
+        const float v = row[e], m = fmaxf(mx, v);
+        if (m > -INFINITY) z = z * hw_exp(mx - m) + hw_exp(v - m);
+        mx = m;
+      }
+      const float all = lanes_max<L>(mx);
+      z = lanes_sum<L>(mx > -INFINITY ? z * hw_exp(mx - all) : z);
+      mx = all;
+      rz = mx == -INFINITY ? 0.f : __builtin_amdgcn_rcpf(z);
+      if (mx == -INFINITY) mx = 0.f;
+    }
+    float g;
+    if (a.renormalize) {
+      const float m = lanes_max<L>(l);
+      const float sh = used && m > -INFINITY
+                           ? fast_score(l, sigmoid ? fminf(m, 0.f) : m, sigmoid) : 0.f;
+      const float total = lanes_sum<L>(sh);
+      const float hat = total == 0.f ? 0.f : sh * __builtin_amdgcn_rcpf(total);
+      g = hat * (d - lanes_sum<L>(hat * d));
+    } else if (sigmoid) {
+      g = hw_sigmoid(l) * d;
+    } else {
+      g = hw_exp(l - mx) * rz * d;
+    }
+    if (sigmoid) g *= hw_sigmoid(-l);
+    if (!used) g = 0.f;
+    const float all = dense ? lanes_sum<L>(g) : 0.f;
+    // a slot that finds another's mark shares its id
+    if (used) r[id] = __int_as_float(li);
+    __builtin_amdgcn_wave_barrier();
+    const bool shared = used && __float_as_int(r[id]) != li;
+    if (__any(shared)) {
+      float sum = 0.f;
+      for (int j = 0; j < k; ++j) {
+        const int oj = __shfl(id, base + j, kWave);
+        const float gj = __shfl(g, base + j, kWave);
+        if (oj == id) sum += gj;
+      }
+      g = sum;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (used) r[id] = g;
+    __builtin_amdgcn_wave_barrier();
+    float* out = grad_logits + (size_t)t * E;
+    if (live) {
+#pragma unroll 4
+      for (int e = V * li; e < E; e += V * L) {
+        if constexpr (V == 4) {
+          f32x4 v = *reinterpret_cast<const f32x4*>(r + e);
+          if (dense) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(row + e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] -= hw_exp(x[j] - mx) * rz * all;
+          }
+          *reinterpret_cast<f32x4*>(out + e) = v;
+        } else {
+          out[e] = dense ? r[e] - hw_exp(row[e] - mx) * rz * all : r[e];
+        }
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (used) r[id] = 0.f;
+    __builtin_amdgcn_wave_barrier();
   }
-  const bool dense = !sigmoid && !renormalize;
-  float mx = -INFINITY, z = 1.f;
-  if (dense) {
-    for (int e = lane; e < E; e += 64) mx = fmaxf(mx, row[e]);
-    mx = wave_max(mx);
-    z = 0.f;
-    for (int e = lane; e < E; e += 64) z += shifted_score(row[e], mx, false);
-    z = wave_sum(z);
-  }
-  float g;
-  if (renormalize) {
-    float m = -INFINITY;
-    for (int j = 0; j < top_k; ++j) m = fmaxf(m, __shfl(l, j, kWave));
-    const float sh = id >= 0 ? shifted_score(l, m, sigmoid != 0) : 0.f;
-    const float total = lane0_sum(sh, top_k);
-    const float hat = total == 0.f ? 0.f : sh / total;
-    g = hat * (d - lane0_sum(hat * d, top_k));
-  } else if (sigmoid) {
-    g = sigmoid_f32(l) * d;
-  } else {
-    g = z == 0.f || id < 0 ? 0.f : shifted_score(l, mx, false) / z * d;
-  }
-  if (sigmoid) g *= sigmoid_f32(-l);
-  const float all = dense ? lane0_sum(g, top_k) : 0.f;
-  for (int e = lane; e < E; e += 64)
-    out[e] = dense && z != 0.f ? -(shifted_score(row[e], mx, false) / z) * all : 0.f;
-  __builtin_amdgcn_wave_barrier();
-  // every slot of an id adds the same sum: which one stores it does not matter
-  float sum = 0.f;
-  for (int j = 0; j < top_k; ++j) {
-    const int oj = __shfl(id, j, kWave);
-    const float gj = __shfl(g, j, kWave);
-    if (oj == id) sum += gj;
-  }
-  float base = 0.f;
-  if (id >= 0) base = out[id];
-  __builtin_amdgcn_wave_barrier();
-  if (id >= 0) out[id] = base + sum;
-  __builtin_amdgcn_wave_barrier();
-  for (int e = lane; e < E; e += 64) grad_logits[(size_t)t * E + e] = out[e];
 }
 
 }  // namespace
@@ -735,12 +774,34 @@ hipError_t launch_select(const SelectArgs& a, hipStream_t s) {
   return a.E / a.n_group % 4 == 0 ? launch_select_v<4>(a, s) : launch_select_v<1>(a, s);
 }
 
+namespace {
+
+template <int L, int V>
+hipError_t go_backward(const SelectArgs& a, const float* grad_weights, float* grad_logits,
+                       hipStream_t s) {
+  const SelectParams p{a.logits, nullptr, a.M, a.E, a.top_k, a.sigmoid, a.renormalize, a.n_group,
+                       a.topk_group, a.group_top, a.scale, a.topk_ids, nullptr};
+  const int wgs = ceil_div_host(a.M, kSelWaves * 64 / L), most = 8 * device_cu_count();
+  hipLaunchKernelGGL((select_backward_kernel<L, V>), dim3(wgs < most ? wgs : most),
+                     dim3(64 * kSelWaves), 0, s, p, grad_weights, grad_logits);
+  return hipGetLastError();
+}
+
+template <int V>
+hipError_t launch_backward_v(const SelectArgs& a, const float* grad_weights, float* grad_logits,
+                             hipStream_t s) {
+  // as launch_select: a wave per token while the chip has waves for them
+  if (a.M <= 16 * device_cu_count()) return go_backward<64, V>(a, grad_weights, grad_logits, s);
+  if (a.top_k <= 16) return go_backward<16, V>(a, grad_weights, grad_logits, s);
+  return go_backward<32, V>(a, grad_weights, grad_logits, s);
+}
+
+}  // namespace
+
 hipError_t launch_select_backward(const SelectArgs& a, const float* grad_weights,
                                   float* grad_logits, hipStream_t s) {
-  hipLaunchKernelGGL(select_backward_wave_kernel, dim3(ceil_div_host(a.M, 4)), dim3(256), 0, s,
-                     a.logits, a.topk_ids, grad_weights, a.M, a.E, a.top_k, a.sigmoid,
-                     a.renormalize, a.scale, grad_logits);
-  return hipGetLastError();
+  return a.E % 4 == 0 ? launch_backward_v<4>(a, grad_weights, grad_logits, s)
+                      : launch_backward_v<1>(a, grad_weights, grad_logits, s);
 }
 
 }  // namespace moe_host

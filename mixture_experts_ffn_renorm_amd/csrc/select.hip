@@ -617,7 +617,9 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
 //
 // The slots' values go through a row of LDS that is zero elsewhere: it is
 // read in pieces of V experts, stored, and cleared again at the slots alone.
-// Bound by the stores of [M, E].
+// Bound by the stores of [M, E] (non-temporal: 65536 x 512 in 33 us, 44 with
+// plain stores, which push the logits' lines out) and by the lines that the
+// top_k gathered logits bring in.
 template <int L, int V>
 __global__ __launch_bounds__(64 * kSelWaves) void select_backward_kernel(
     SelectParams a, const float* __restrict__ grad_weights, float* __restrict__ grad_logits) {
@@ -647,16 +649,28 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_backward_kernel(
     if (!used) d = 0.f;
     float mx = -INFINITY, rz = 0.f;
     if (dense) {
-      // maximum and sum of exponentials of the row, one pass
+      // maximum, then sum of exponentials of the row (from the cache)
       float z = 0.f;
-      for (int e = li; e < E; e += L) {
-        const float v = row[e], m = fmaxf(mx, v);
-        if (m > -INFINITY) z = z * hw_exp(mx - m) + hw_exp(v - m);
-        mx = m;
+#pragma unroll 4
+      for (int e = V * li; e < E; e += V * L) {
+        if constexpr (V == 4) {
+          const f32x4 x = *reinterpret_cast<const f32x4*>(row + e);
+          mx = fmaxf(mx, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+        } else {
+          mx = fmaxf(mx, row[e]);
+        }
       }
-      const float all = lanes_max<L>(mx);
-      z = lanes_sum<L>(mx > -INFINITY ? z * hw_exp(mx - all) : z);
-      mx = all;
+      mx = lanes_max<L>(mx);
+#pragma unroll 4
+      for (int e = V * li; e < E; e += V * L) {
+        if constexpr (V == 4) {
+          const f32x4 x = *reinterpret_cast<const f32x4*>(row + e);
+          z += (hw_exp(x[0] - mx) + hw_exp(x[1] - mx)) + (hw_exp(x[2] - mx) + hw_exp(x[3] - mx));
+        } else {
+          z += hw_exp(row[e] - mx);
+        }
+      }
+      z = lanes_sum<L>(z);
       rz = mx == -INFINITY ? 0.f : __builtin_amdgcn_rcpf(z);
       if (mx == -INFINITY) mx = 0.f;
     }
@@ -703,7 +717,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_backward_kernel(
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] -= hw_exp(x[j] - mx) * rz * all;
           }
-          *reinterpret_cast<f32x4*>(out + e) = v;
+          __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(out + e));
         } else {
           out[e] = dense ? r[e] - hw_exp(row[e] - mx) * rz * all : r[e];
         }

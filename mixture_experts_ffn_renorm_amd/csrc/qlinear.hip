@@ -90,6 +90,12 @@ __device__ __forceinline__ u32x4 pair8(u32x4 X) {
   return __builtin_bit_cast(u32x4, __builtin_shufflevector(v, v, 0, 4, 1, 5, 2, 6, 3, 7));
 }
 
+template <int kCtrl>
+__device__ __forceinline__ float dpp_add_lanes(float v) {
+  const int s = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xf, 0xf, false);
+  return v + __builtin_bit_cast(float, s);
+}
+
 // The epilogue of one output value.
 __device__ __forceinline__ void store_out(const moe_host::QLinearArgs& a, float y, int m, int n,
                                           int n_out) {
@@ -588,6 +594,256 @@ hipError_t launch_stream(const moe_host::QLinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ---- tile kernel: many tokens ----
+//
+// A workgroup owns 64 tokens and 32 weight rows per wave (gated: 16 gate rows
+// and their 16 up rows); K goes by in stages of 256.  x passes through LDS
+// once per workgroup: each 16-byte piece is put into the codes' pair order on
+// the way (piece c of token m at slot c ^ (m & 15) of its half row: the 16
+// tokens of an operand read fall on distinct banks) and summed over its group.
+// A wave's codes go from memory to registers one stage ahead.
+//
+// The group sums' term, sum_j b_j sx_j - 128 s_j sx_j, is a product over the
+// groups of its own: sx in three bf16 parts (24 bits), against the bf16 b and
+// s themselves, eight k slots per group [b b b s s s 0 0] x
+// [h m l -128h -128m -128l 0 0], so one more MFMA step per four groups adds it
+// to the fp32 sums, where FMAs would cost as much vector time as the scaling.
+constexpr int kTileM = 64;
+constexpr int kTileK = 256;
+constexpr int kTileX = kTileM * kTileK * 2;      // bytes of x per stage
+
+template <int G, int W>
+__global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearArgs a, int ntile) {
+  constexpr int NG = kTileK / G;                  // groups per stage
+  constexpr int NX = (NG + 3) / 4;                // steps of the sums' product
+  constexpr int NS = G / 32;                      // MFMA steps per group
+  constexpr int kSums = NX * 4 * kTileM * 16;     // bytes of sums per stage
+  constexpr int kStage = kTileX + kSums;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int n_out = a.gated ? a.N / 2 : a.N;
+  const int wg_n = ceil_div(ntile, W);
+  const int id = xcd_contiguous_tile(blockIdx.x, wg_n * ceil_div(a.M, kTileM));
+  if (id < 0) return;                             // whole workgroup
+  const int m0 = id / wg_n * kTileM;
+  const int n0 = (id % wg_n * W + wave) * (a.gated ? 16 : 32);   // past the end: not stored
+  const int upr = a.K / 32, gpr = a.K / G;
+  const int nstage = ceil_div(a.K, kTileK);
+
+  const u32x4* wrow[2];
+  const uint16_t *srow[2], *brow[2];
+#pragma unroll
+  for (int f = 0; f < 2; ++f) {
+    const int n = min(n0 + r + (a.gated ? 0 : 16 * f), n_out - 1) + (a.gated && f ? n_out : 0);
+    wrow[f] = reinterpret_cast<const u32x4*>(a.q) + (size_t)n * upr;
+    srow[f] = a.scales + (size_t)n * gpr;
+    brow[f] = a.biases + (size_t)n * gpr;
+  }
+  // x: 32 pieces of 8 elements per token and stage; a row of 16 lanes takes
+  // half a token's, so a piece's group lies inside its row of lanes
+  constexpr int kPer = kTileM * kTileK / 8 / (64 * W);   // pieces per thread
+  u32x4 xr[kPer];
+  u32x4 wn[2][2];
+  uint32_t sn[2][NX], bn[2][NX];
+  auto load_x = [&](int st) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int p = i * 64 * W + tid, m = p >> 5, k = st * kTileK + (p & 31) * 8;
+      xr[i] = load16_or_zero(a.x + (size_t)min(m0 + m, a.M - 1) * a.K + k, k < a.K);
+    }
+  };
+  auto load_w = [&](int st) {
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int u = st * (kTileK / 32) + 4 * b + g;
+        wn[f][b] = load16(wrow[f] + (u < upr ? u : 0));   // past K: its x is 0
+      }
+#pragma unroll
+      for (int j = 0; j < NX; ++j) {
+        const int gi = st * NG + 4 * j + g;
+        const bool in = 4 * j + g < NG && gi < gpr;
+        sn[f][j] = srow[f][in ? gi : 0];
+        bn[f][j] = brow[f][in ? gi : 0];
+      }
+    }
+  };
+  auto store_x = [&](int st) {
+    uint8_t* buf = lds + (st & 1) * kStage;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int p = i * 64 * W + tid, m = p >> 5, c = p & 31;
+      *reinterpret_cast<u32x4*>(buf + m * 512 + (c >> 4) * 256 + (((c & 15) ^ (m & 15)) << 4)) =
+          pair8(xr[i]);
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s = dot2_bf16(xr[i][j], 0x3f803f80u, s);
+      s = dpp_add_lanes<0xb1>(s);                 // quad_perm [1, 0, 3, 2]
+      s = dpp_add_lanes<0x4e>(s);                 // quad_perm [2, 3, 0, 1]
+      if (G >= 64) s = dpp_add_lanes<0x141>(s);   // row_half_mirror
+      if (G == 128) s = dpp_add_lanes<0x140>(s);  // row_mirror
+      if (c % (G / 8) == 0) {
+        const float h = bf16_lo(f32_to_bf16(s));
+        const float mid = bf16_lo(f32_to_bf16(s - h));
+        const float lo = s - h - mid;
+        *reinterpret_cast<u32x4*>(buf + kTileX + ((c / (G / 8)) * kTileM + m) * 16) =
+            u32x4{pack_bf16x2(h, mid), pack_bf16x2(lo, -128.f * h),
+                  pack_bf16x2(-128.f * mid, -128.f * lo), 0u};
+      }
+    }
+  };
+
+  const WidenConst wc;
+  f32x4 tot[2][4];
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) tot[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // group slots that no group fills (G = 128): zero in both buffers
+  if (NX * 4 > NG)
+    for (int i = tid; i < 2 * (NX * 4 - NG) * kTileM; i += blockDim.x)
+      *reinterpret_cast<u32x4*>(lds + (i & 1) * kStage + kTileX + (NG * kTileM + (i >> 1)) * 16) =
+          u32x4{0u, 0u, 0u, 0u};
+
+  load_x(0);
+  load_w(0);
+  store_x(0);
+  __syncthreads();
+#pragma unroll 1
+  for (int st = 0; st < nstage; ++st) {
+    const uint8_t* buf = lds + (st & 1) * kStage;
+    u32x4 w[2][2];
+    uint32_t pr[2][NX];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        w[f][b] = wn[f][b];
+        group_words<G>(w[f][b]);
+      }
+#pragma unroll
+      for (int j = 0; j < NX; ++j) pr[f][j] = sn[f][j] | (bn[f][j] << 16);
+    }
+    const int next = min(st + 1, nstage - 1);
+    load_x(next);
+    load_w(next);
+    uint32_t pair[2][NX * 4];
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int j = 0; j < NX; ++j) {
+        uint32_t p[4];
+        group_pairs<32>(pr[f][j], p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pair[f][4 * j + i] = p[i];
+      }
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {
+      if (NX == 2 || b == 0) {
+        // the sums' product for four groups
+        u32x4 bx[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const uint32_t p = pr[f][0];
+          bx[f] = u32x4{__builtin_amdgcn_perm(p, p, 0x07060706u),    // b b
+                        __builtin_amdgcn_perm(p, p, 0x05040706u),    // b s
+                        __builtin_amdgcn_perm(p, p, 0x05040504u),    // s s
+                        0u};
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const u32x4 ax = *reinterpret_cast<const u32x4*>(
+              buf + kTileX + ((4 * b + g) * kTileM + 16 * t + r) * 16);
+#pragma unroll
+          for (int f = 0; f < 2; ++f) tot[f][t] = mfma_16x16x32(ax, bx[f], tot[f][t]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NG / 2; ++j) {          // groups of this block
+        f32x4 acc[2][4];
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) acc[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const int word = j * NS + i;
+          const int c = word_k<G>(word, g) >> 3;  // piece of the half row
+          const u32x4 w0 = widen8(w[0][0][word], wc), w1 = widen8(w[1][0][word], wc);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const u32x4 ax = *reinterpret_cast<const u32x4*>(
+                buf + (16 * t + r) * 512 + b * 256 + ((c ^ r) << 4));
+            acc[0][t] = mfma_16x16x32(ax, w0, acc[0][t]);
+            acc[1][t] = mfma_16x16x32(ax, w1, acc[1][t]);
+          }
+        }
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const float s = bf16_lo(pair[f][j]);
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tot[f][t][q] = __builtin_fmaf(s, acc[f][t][q], tot[f][t][q]);
+        }
+      }
+      // the second block in the first one's registers
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        w[f][0] = w[f][1];
+        pr[f][0] = pr[f][NX - 1];
+#pragma unroll
+        for (int j = 0; j < NG / 2; ++j) pair[f][j] = pair[f][NG / 2 + j];
+      }
+    }
+    if (st + 1 < nstage) store_x(st + 1);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int m = m0 + 16 * t + 4 * g + q;
+      if (m >= a.M) continue;
+      if (a.gated) {
+        if (n0 + r < n_out) store_out(a, silu_mul(tot[0][t][q], tot[1][t][q]), m, n0 + r, n_out);
+      } else {
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          if (n0 + 16 * f + r < n_out) store_out(a, tot[f][t][q], m, n0 + 16 * f + r, n_out);
+      }
+    }
+}
+
+template <int G, int W>
+hipError_t launch_tile_waves(const moe_host::QLinearArgs& a, int ntile, int mtile, hipStream_t s) {
+  using moe_host::ceil_div_host;
+  constexpr int NX = (kTileK / G + 3) / 4;
+  constexpr int kLds = 2 * (kTileX + NX * 4 * kTileM * 16);
+  static bool set[moe_host::kMaxDevices] = {};
+  const hipError_t e = moe_host::ensure_dynamic_lds(
+      reinterpret_cast<const void*>(&qlinear_tile_kernel<G, W>), kLds, set);
+  if (e != hipSuccess) return e;
+  const int tiles = ceil_div_host(ntile, W) * mtile;
+  hipLaunchKernelGGL((qlinear_tile_kernel<G, W>), dim3((unsigned)ceil_div_host(tiles, 8) * 8),
+                     dim3(64 * W), kLds, s, a, ntile);
+  return hipGetLastError();
+}
+
+template <int G>
+hipError_t launch_tile(const moe_host::QLinearArgs& a, hipStream_t s) {
+  using moe_host::ceil_div_host;
+  const int ntile = ceil_div_host(a.gated ? a.N / 2 : a.N, a.gated ? 16 : 32);
+  const int mtile = ceil_div_host(a.M, kTileM);
+  // eight waves share a stage of x; four where that leaves CUs without work
+  if (ceil_div_host(ntile, 8) * mtile >= moe_host::device_cu_count())
+    return launch_tile_waves<G, 8>(a, ntile, mtile, s);
+  return launch_tile_waves<G, 4>(a, ntile, mtile, s);
+}
+
 template <bool kGated>
 hipError_t launch_few(const moe_host::QLinearArgs& a, hipStream_t s) {
   if (a.M == 1) return launch_gemv<1, kGated>(a, s);
@@ -599,6 +855,7 @@ template <int G, bool kGated>
 hipError_t launch_tokens(const moe_host::QLinearArgs& a, hipStream_t s) {
   if (a.M <= 16) return launch_rows<G, 1>(a, s);
   if (a.M <= 32) return launch_rows<G, 2>(a, s);
+  if (a.M > 64) return launch_tile<G>(a, s);
   return launch_stream<G, 4, kGated, 1>(a, s);
 }
 

@@ -632,20 +632,29 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
   const int upr = a.K / 32, gpr = a.K / G;
   const int nstage = ceil_div(a.K, kTileK);
 
-  const u32x4* wrow[2];
-  const uint16_t *srow[2], *brow[2];
+  // weight row i (0..31) of this wave: fragment i / 16
+  auto row_of = [&](int i) {
+    return min(n0 + (a.gated ? i & 15 : i), n_out - 1) + (a.gated && i >= 16 ? n_out : 0);
+  };
+  // A stage holds 128 bytes of codes per row: eight lanes load a row's, the
+  // four loads cover 32 rows, whole cache lines each, and the operands are
+  // read back from the wave's own LDS (piece c of row i at c ^ ((i >> 1) & 7):
+  // 16 rows of an operand fall on distinct banks).  Scales and biases: four
+  // lanes load a row's four groups.
+  const int lrow = lane >> 3, lpc = lane & 7;
+  const u32x4* wsrc[4];
 #pragma unroll
-  for (int f = 0; f < 2; ++f) {
-    const int n = min(n0 + r + (a.gated ? 0 : 16 * f), n_out - 1) + (a.gated && f ? n_out : 0);
-    wrow[f] = reinterpret_cast<const u32x4*>(a.q) + (size_t)n * upr;
-    srow[f] = a.scales + (size_t)n * gpr;
-    brow[f] = a.biases + (size_t)n * gpr;
-  }
+  for (int i = 0; i < 4; ++i)
+    wsrc[i] = reinterpret_cast<const u32x4*>(a.q) + (size_t)row_of(8 * i + lrow) * upr;
+  size_t srow[2];
+#pragma unroll
+  for (int f = 0; f < 2; ++f) srow[f] = (size_t)row_of(16 * f + (lane >> 2)) * gpr;
+  uint8_t* wl = lds + 2 * kStage + wave * 4096;
   // x: 32 pieces of 8 elements per token and stage; a row of 16 lanes takes
   // half a token's, so a piece's group lies inside its row of lanes
   constexpr int kPer = kTileM * kTileK / 8 / (64 * W);   // pieces per thread
   u32x4 xr[kPer];
-  u32x4 wn[2][2];
+  u32x4 wn[4];
   uint32_t sn[2][NX], bn[2][NX];
   auto load_x = [&](int st) {
 #pragma unroll
@@ -655,20 +664,24 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
     }
   };
   auto load_w = [&](int st) {
+    const int u = st * (kTileK / 32) + lpc;
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
+    for (int i = 0; i < 4; ++i) wn[i] = load16(wsrc[i] + (u < upr ? u : 0));   // past K: its x is 0
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int u = st * (kTileK / 32) + 4 * b + g;
-        wn[f][b] = load16(wrow[f] + (u < upr ? u : 0));   // past K: its x is 0
-      }
+    for (int f = 0; f < 2; ++f)
 #pragma unroll
       for (int j = 0; j < NX; ++j) {
-        const int gi = st * NG + 4 * j + g;
-        const bool in = 4 * j + g < NG && gi < gpr;
-        sn[f][j] = srow[f][in ? gi : 0];
-        bn[f][j] = brow[f][in ? gi : 0];
+        const int gl = 4 * j + (lane & 3), gi = st * NG + gl;
+        const size_t at = srow[f] + (gl < NG && gi < gpr ? gi : 0);
+        sn[f][j] = a.scales[at];
+        bn[f][j] = a.biases[at];
       }
+  };
+  auto store_w = [&]() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 8 * i + lrow;
+      *reinterpret_cast<u32x4*>(wl + row * 128 + ((lpc ^ ((row >> 1) & 7)) << 4)) = wn[i];
     }
   };
   auto store_x = [&](int st) {
@@ -711,6 +724,7 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
   load_x(0);
   load_w(0);
   store_x(0);
+  store_w();
   __syncthreads();
 #pragma unroll 1
   for (int st = 0; st < nstage; ++st) {
@@ -721,11 +735,14 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
     for (int f = 0; f < 2; ++f) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        w[f][b] = wn[f][b];
+        w[f][b] = *reinterpret_cast<const u32x4*>(
+            wl + (16 * f + r) * 128 + (((4 * b + g) ^ ((r >> 1) & 7)) << 4));
         group_words<G>(w[f][b]);
       }
+      // from lane 4 r + g to lane r + 16 g
 #pragma unroll
-      for (int j = 0; j < NX; ++j) pr[f][j] = sn[f][j] | (bn[f][j] << 16);
+      for (int j = 0; j < NX; ++j)
+        pr[f][j] = (uint32_t)__shfl((int)(sn[f][j] | (bn[f][j] << 16)), 4 * r + g, kWave);
     }
     const int next = min(st + 1, nstage - 1);
     load_x(next);
@@ -799,7 +816,10 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
         for (int j = 0; j < NG / 2; ++j) pair[f][j] = pair[f][NG / 2 + j];
       }
     }
-    if (st + 1 < nstage) store_x(st + 1);
+    if (st + 1 < nstage) {
+      store_x(st + 1);
+      store_w();
+    }
     __syncthreads();
   }
 #pragma unroll
@@ -822,7 +842,7 @@ template <int G, int W>
 hipError_t launch_tile_waves(const moe_host::QLinearArgs& a, int ntile, int mtile, hipStream_t s) {
   using moe_host::ceil_div_host;
   constexpr int NX = (kTileK / G + 3) / 4;
-  constexpr int kLds = 2 * (kTileX + NX * 4 * kTileM * 16);
+  constexpr int kLds = 2 * (kTileX + NX * 4 * kTileM * 16) + W * 4096;
   static bool set[moe_host::kMaxDevices] = {};
   const hipError_t e = moe_host::ensure_dynamic_lds(
       reinterpret_cast<const void*>(&qlinear_tile_kernel<G, W>), kLds, set);

@@ -686,6 +686,11 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
   };
   auto store_x = [&](int st) {
     uint8_t* buf = lds + (st & 1) * kStage;
+    // a piece's group sum is in every lane of the group; lane i of a group
+    // keeps the i-th piece's, so that the parts are formed once
+    constexpr int kLanes = G / 8;                 // lanes of a group: 4, 8 or 16
+    const int mine = lane & (kLanes - 1);
+    float sum[(kPer + kLanes - 1) / kLanes];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int p = i * 64 * W + tid, m = p >> 5, c = p & 31;
@@ -698,15 +703,20 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
       s = dpp_add_lanes<0x4e>(s);                 // quad_perm [2, 3, 0, 1]
       if (G >= 64) s = dpp_add_lanes<0x141>(s);   // row_half_mirror
       if (G == 128) s = dpp_add_lanes<0x140>(s);  // row_mirror
-      if (c % (G / 8) == 0) {
+      sum[i / kLanes] = i % kLanes == 0 || mine == i % kLanes ? s : sum[i / kLanes];
+    }
+#pragma unroll
+    for (int v = 0; v < kPer; v += kLanes)
+      if (v + mine < kPer) {
+        const int p = (v + mine) * 64 * W + tid, m = p >> 5, c = p & 31;
+        const float s = sum[v / kLanes];
         const float h = bf16_lo(f32_to_bf16(s));
         const float mid = bf16_lo(f32_to_bf16(s - h));
         const float lo = s - h - mid;
-        *reinterpret_cast<u32x4*>(buf + kTileX + ((c / (G / 8)) * kTileM + m) * 16) =
+        *reinterpret_cast<u32x4*>(buf + kTileX + ((c / kLanes) * kTileM + m) * 16) =
             u32x4{pack_bf16x2(h, mid), pack_bf16x2(lo, -128.f * h),
                   pack_bf16x2(-128.f * mid, -128.f * lo), 0u};
       }
-    }
   };
 
   const WidenConst wc;
@@ -822,20 +832,47 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
     }
     __syncthreads();
   }
+  // lane: weight row r of each fragment, tokens 4 g .. 4 g + 3 of each tile;
+  // all loads of the epilogue leave before the first store
+  float rs[4][4];
 #pragma unroll
   for (int t = 0; t < 4; ++t)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int m = m0 + 16 * t + 4 * g + q;
-      if (m >= a.M) continue;
-      if (a.gated) {
-        if (n0 + r < n_out) store_out(a, silu_mul(tot[0][t][q], tot[1][t][q]), m, n0 + r, n_out);
-      } else {
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-          if (n0 + 16 * f + r < n_out) store_out(a, tot[f][t][q], m, n0 + 16 * f + r, n_out);
-      }
+      const int m = min(m0 + 16 * t + 4 * g + q, a.M - 1);
+      rs[t][q] = a.row_scale != nullptr ? a.row_scale[m] : 1.f;
     }
+#pragma unroll
+  for (int f = 0; f < 2; ++f) {
+    if (a.gated && f == 1) break;
+    const int n = n0 + 16 * f + r, nc = min(n, n_out - 1);
+    float y[4][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        y[t][q] = (a.gated ? silu_mul(tot[0][t][q], tot[1][t][q]) : tot[f][t][q]) * rs[t][q];
+    if (a.addend != nullptr) {
+      float ad[4][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          ad[t][q] = bf16_load(a.addend + (size_t)min(m0 + 16 * t + 4 * g + q, a.M - 1) * n_out + nc);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[t][q] += ad[t][q];
+    }
+    if (n >= n_out) continue;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int m = m0 + 16 * t + 4 * g + q;
+        if (m < a.M) a.out[(size_t)m * n_out + n] = (uint16_t)f32_to_bf16(y[t][q]);
+      }
+  }
 }
 
 template <int G, int W>

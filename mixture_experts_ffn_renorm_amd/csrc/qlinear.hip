@@ -49,6 +49,15 @@ __device__ __forceinline__ int word_k(int st, int g) {
   return 32 * st + 8 * g;
 }
 
+// 4 word + lane group of the operand that takes piece c (8 elements) of a
+// block: word_k's inverse.
+template <int G>
+__device__ __forceinline__ int word_slot(int c) {
+  if (G == 128) return ((c & 3) << 2) | (c >> 2);
+  if (G == 64) return (c & 8) | ((c & 1) << 2) | (c & 2) | ((c >> 2) & 1);
+  return c;
+}
+
 // Each group's (scale, bias) pair in every lane of its row, from the pair of
 // the lane's own unit.
 template <int G>
@@ -599,8 +608,10 @@ hipError_t launch_stream(const moe_host::QLinearArgs& a, hipStream_t s) {
 // A workgroup owns 64 tokens and 32 weight rows per wave (gated: 16 gate rows
 // and their 16 up rows); K goes by in stages of 256.  x passes through LDS
 // once per workgroup: each 16-byte piece is put into the codes' pair order on
-// the way (piece c of token m at slot c ^ (m & 15) of its half row: the 16
-// tokens of an operand read fall on distinct banks) and summed over its group.
+// the way and summed over its group.  The piece that word w of lane group g
+// multiplies lies at slot (4 w + g) ^ (m & 15) of token m's half row: with g
+// in the low bits, the lanes that one LDS cycle serves fall on distinct banks
+// (with g in the high bits a sixth of the kernel's time went to conflicts).
 // A wave's codes go from memory to registers one stage ahead.
 //
 // The group sums' term, sum_j b_j sx_j - 128 s_j sx_j, is a product over the
@@ -612,7 +623,7 @@ constexpr int kTileM = 64;
 constexpr int kTileK = 256;
 constexpr int kTileX = kTileM * kTileK * 2;      // bytes of x per stage
 
-template <int G, int W>
+template <int G, int W, int F>
 __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearArgs a, int ntile) {
   constexpr int NG = kTileK / G;                  // groups per stage
   constexpr int NX = (NG + 3) / 4;                // steps of the sums' product
@@ -628,34 +639,35 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
   const int id = xcd_contiguous_tile(blockIdx.x, wg_n * ceil_div(a.M, kTileM));
   if (id < 0) return;                             // whole workgroup
   const int m0 = id / wg_n * kTileM;
-  const int n0 = (id % wg_n * W + wave) * (a.gated ? 16 : 32);   // past the end: not stored
+  const int n0 = (id % wg_n * W + wave) * (a.gated ? 8 * F : 16 * F);   // past the end: not stored
   const int upr = a.K / 32, gpr = a.K / G;
   const int nstage = ceil_div(a.K, kTileK);
 
-  // weight row i (0..31) of this wave: fragment i / 16
+  // weight row i of this wave: row i % 16 of fragment i / 16 (gated: the
+  // first half of the fragments gates, the second their up rows)
   auto row_of = [&](int i) {
-    return min(n0 + (a.gated ? i & 15 : i), n_out - 1) + (a.gated && i >= 16 ? n_out : 0);
+    return min(n0 + (a.gated ? i % (8 * F) : i), n_out - 1) + (a.gated && i >= 8 * F ? n_out : 0);
   };
-  // A stage holds 128 bytes of codes per row: eight lanes load a row's, the
-  // four loads cover 32 rows, whole cache lines each, and the operands are
+  // A stage holds 128 bytes of codes per row: eight lanes load a row's
+  // (whole cache lines), and the operands are
   // read back from the wave's own LDS (piece c of row i at c ^ ((i >> 1) & 7):
   // 16 rows of an operand fall on distinct banks).  Scales and biases: four
   // lanes load a row's four groups.
   const int lrow = lane >> 3, lpc = lane & 7;
-  const u32x4* wsrc[4];
+  const u32x4* wsrc[2 * F];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2 * F; ++i)
     wsrc[i] = reinterpret_cast<const u32x4*>(a.q) + (size_t)row_of(8 * i + lrow) * upr;
-  size_t srow[2];
+  size_t srow[F];
 #pragma unroll
-  for (int f = 0; f < 2; ++f) srow[f] = (size_t)row_of(16 * f + (lane >> 2)) * gpr;
-  uint8_t* wl = lds + 2 * kStage + wave * 4096;
+  for (int f = 0; f < F; ++f) srow[f] = (size_t)row_of(16 * f + (lane >> 2)) * gpr;
+  uint8_t* wl = lds + 2 * kStage + wave * (F * 2048);
   // x: 32 pieces of 8 elements per token and stage; a row of 16 lanes takes
   // half a token's, so a piece's group lies inside its row of lanes
   constexpr int kPer = kTileM * kTileK / 8 / (64 * W);   // pieces per thread
   u32x4 xr[kPer];
-  u32x4 wn[4];
-  uint32_t sn[2][NX], bn[2][NX];
+  u32x4 wn[2 * F];
+  uint32_t sn[F][NX], bn[F][NX];
   auto load_x = [&](int st) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -666,9 +678,9 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
   auto load_w = [&](int st) {
     const int u = st * (kTileK / 32) + lpc;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wn[i] = load16(wsrc[i] + (u < upr ? u : 0));   // past K: its x is 0
+    for (int i = 0; i < 2 * F; ++i) wn[i] = load16(wsrc[i] + (u < upr ? u : 0));   // past K: its x is 0
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < F; ++f)
 #pragma unroll
       for (int j = 0; j < NX; ++j) {
         const int gl = 4 * j + (lane & 3), gi = st * NG + gl;
@@ -679,7 +691,7 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
   };
   auto store_w = [&]() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * F; ++i) {
       const int row = 8 * i + lrow;
       *reinterpret_cast<u32x4*>(wl + row * 128 + ((lpc ^ ((row >> 1) & 7)) << 4)) = wn[i];
     }
@@ -694,8 +706,8 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int p = i * 64 * W + tid, m = p >> 5, c = p & 31;
-      *reinterpret_cast<u32x4*>(buf + m * 512 + (c >> 4) * 256 + (((c & 15) ^ (m & 15)) << 4)) =
-          pair8(xr[i]);
+      *reinterpret_cast<u32x4*>(buf + m * 512 + (c >> 4) * 256 +
+                                ((word_slot<G>(c & 15) ^ (m & 15)) << 4)) = pair8(xr[i]);
       float s = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) s = dot2_bf16(xr[i][j], 0x3f803f80u, s);
@@ -720,9 +732,9 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
   };
 
   const WidenConst wc;
-  f32x4 tot[2][4];
+  f32x4 tot[F][4];
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+  for (int f = 0; f < F; ++f)
 #pragma unroll
     for (int t = 0; t < 4; ++t) tot[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   // group slots that no group fills (G = 128): zero in both buffers
@@ -739,10 +751,10 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
 #pragma unroll 1
   for (int st = 0; st < nstage; ++st) {
     const uint8_t* buf = lds + (st & 1) * kStage;
-    u32x4 w[2][2];
-    uint32_t pr[2][NX];
+    u32x4 w[F][2];
+    uint32_t pr[F][NX];
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
+    for (int f = 0; f < F; ++f) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         w[f][b] = *reinterpret_cast<const u32x4*>(
@@ -757,9 +769,9 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
     const int next = min(st + 1, nstage - 1);
     load_x(next);
     load_w(next);
-    uint32_t pair[2][NX * 4];
+    uint32_t pair[F][NX * 4];
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < F; ++f)
 #pragma unroll
       for (int j = 0; j < NX; ++j) {
         uint32_t p[4];
@@ -771,9 +783,9 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
     for (int b = 0; b < 2; ++b) {
       if (NX == 2 || b == 0) {
         // the sums' product for four groups
-        u32x4 bx[2];
+        u32x4 bx[F];
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
+        for (int f = 0; f < F; ++f) {
           const uint32_t p = pr[f][0];
           bx[f] = u32x4{__builtin_amdgcn_perm(p, p, 0x07060706u),    // b b
                         __builtin_amdgcn_perm(p, p, 0x05040706u),    // b s
@@ -785,31 +797,32 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
           const u32x4 ax = *reinterpret_cast<const u32x4*>(
               buf + kTileX + ((4 * b + g) * kTileM + 16 * t + r) * 16);
 #pragma unroll
-          for (int f = 0; f < 2; ++f) tot[f][t] = mfma_16x16x32(ax, bx[f], tot[f][t]);
+          for (int f = 0; f < F; ++f) tot[f][t] = mfma_16x16x32(ax, bx[f], tot[f][t]);
         }
       }
 #pragma unroll
       for (int j = 0; j < NG / 2; ++j) {          // groups of this block
-        f32x4 acc[2][4];
+        f32x4 acc[F][4];
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+        for (int f = 0; f < F; ++f)
 #pragma unroll
           for (int t = 0; t < 4; ++t) acc[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           const int word = j * NS + i;
-          const int c = word_k<G>(word, g) >> 3;  // piece of the half row
-          const u32x4 w0 = widen8(w[0][0][word], wc), w1 = widen8(w[1][0][word], wc);
+          u32x4 wv[F];
+#pragma unroll
+          for (int f = 0; f < F; ++f) wv[f] = widen8(w[f][0][word], wc);
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             const u32x4 ax = *reinterpret_cast<const u32x4*>(
-                buf + (16 * t + r) * 512 + b * 256 + ((c ^ r) << 4));
-            acc[0][t] = mfma_16x16x32(ax, w0, acc[0][t]);
-            acc[1][t] = mfma_16x16x32(ax, w1, acc[1][t]);
+                buf + (16 * t + r) * 512 + b * 256 + (((4 * word + g) ^ r) << 4));
+#pragma unroll
+            for (int f = 0; f < F; ++f) acc[f][t] = mfma_16x16x32(ax, wv[f], acc[f][t]);
           }
         }
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
+        for (int f = 0; f < F; ++f) {
           const float s = bf16_lo(pair[f][j]);
 #pragma unroll
           for (int t = 0; t < 4; ++t)
@@ -819,7 +832,7 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
       }
       // the second block in the first one's registers
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
+      for (int f = 0; f < F; ++f) {
         w[f][0] = w[f][1];
         pr[f][0] = pr[f][NX - 1];
 #pragma unroll
@@ -843,15 +856,15 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
       rs[t][q] = a.row_scale != nullptr ? a.row_scale[m] : 1.f;
     }
 #pragma unroll
-  for (int f = 0; f < 2; ++f) {
-    if (a.gated && f == 1) break;
+  for (int f = 0; f < F; ++f) {
+    if (a.gated && f >= F / 2) break;
     const int n = n0 + 16 * f + r, nc = min(n, n_out - 1);
     float y[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        y[t][q] = (a.gated ? silu_mul(tot[0][t][q], tot[1][t][q]) : tot[f][t][q]) * rs[t][q];
+        y[t][q] = (a.gated ? silu_mul(tot[f][t][q], tot[f | (F / 2)][t][q]) : tot[f][t][q]) * rs[t][q];
     if (a.addend != nullptr) {
       float ad[4][4];
 #pragma unroll
@@ -875,17 +888,18 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
   }
 }
 
-template <int G, int W>
-hipError_t launch_tile_waves(const moe_host::QLinearArgs& a, int ntile, int mtile, hipStream_t s) {
+template <int G, int W, int F>
+hipError_t launch_tile_waves(const moe_host::QLinearArgs& a, hipStream_t s) {
   using moe_host::ceil_div_host;
   constexpr int NX = (kTileK / G + 3) / 4;
-  constexpr int kLds = 2 * (kTileX + NX * 4 * kTileM * 16) + W * 4096;
+  constexpr int kLds = 2 * (kTileX + NX * 4 * kTileM * 16) + W * F * 2048;
   static bool set[moe_host::kMaxDevices] = {};
   const hipError_t e = moe_host::ensure_dynamic_lds(
-      reinterpret_cast<const void*>(&qlinear_tile_kernel<G, W>), kLds, set);
+      reinterpret_cast<const void*>(&qlinear_tile_kernel<G, W, F>), kLds, set);
   if (e != hipSuccess) return e;
-  const int tiles = ceil_div_host(ntile, W) * mtile;
-  hipLaunchKernelGGL((qlinear_tile_kernel<G, W>), dim3((unsigned)ceil_div_host(tiles, 8) * 8),
+  const int ntile = ceil_div_host(a.gated ? a.N / 2 : a.N, a.gated ? 8 * F : 16 * F);
+  const int tiles = ceil_div_host(ntile, W) * ceil_div_host(a.M, kTileM);
+  hipLaunchKernelGGL((qlinear_tile_kernel<G, W, F>), dim3((unsigned)ceil_div_host(tiles, 8) * 8),
                      dim3(64 * W), kLds, s, a, ntile);
   return hipGetLastError();
 }
@@ -893,12 +907,11 @@ hipError_t launch_tile_waves(const moe_host::QLinearArgs& a, int ntile, int mtil
 template <int G>
 hipError_t launch_tile(const moe_host::QLinearArgs& a, hipStream_t s) {
   using moe_host::ceil_div_host;
-  const int ntile = ceil_div_host(a.gated ? a.N / 2 : a.N, a.gated ? 16 : 32);
   const int mtile = ceil_div_host(a.M, kTileM);
   // eight waves share a stage of x; four where that leaves CUs without work
-  if (ceil_div_host(ntile, 8) * mtile >= moe_host::device_cu_count())
-    return launch_tile_waves<G, 8>(a, ntile, mtile, s);
-  return launch_tile_waves<G, 4>(a, ntile, mtile, s);
+  if (ceil_div_host(a.N, 256) * mtile >= moe_host::device_cu_count())
+    return launch_tile_waves<G, 8, 2>(a, s);
+  return launch_tile_waves<G, 4, 2>(a, s);
 }
 
 template <bool kGated>

@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -86,6 +87,10 @@ class QuantizedMatrix(ctypes.Structure):
     """moe_quantized_matrix: bits, group size and three device pointers."""
     _fields_ = [("bits", _c_int), ("group_size", _c_int), ("q", _c_void_p),
                 ("scales", _c_void_p), ("biases", _c_void_p)]
+
+
+# the same struct as bytes, which a call takes in a third of the time
+_pack_matrix = struct.Struct("@iiPPP").pack
 
 
 _SIGNATURES = {
@@ -632,7 +637,7 @@ class Routing:
 def _need(t, name, dtype, shape, device: int):
     """Raise unless t is a dense aligned tensor of that kind on that device."""
     if not (t.dtype is dtype and t.shape == shape and t.get_device() == device and
-            t.is_contiguous() and t.data_ptr() % 16 == 0):
+            t.is_contiguous() and not t.data_ptr() & 15):
         _refuse(t, name, dtype, shape, device)
 
 
@@ -900,10 +905,10 @@ def moe_linear_quantized(x, weight: dict, gated: bool = False, row_scale=None, a
         out = _empty(shape, bf16, dev, stream)
     else:
         _need(out, "out", bf16, shape, dev)
-    w = QuantizedMatrix(bits, group, q.data_ptr(), scales.data_ptr(), biases.data_ptr())
-    st = library().moe_linear_quantized(x.data_ptr(), ctypes.addressof(w), M, N, K,
-                                        1 if gated else 0, _ptr(row_scale), _ptr(addend),
-                                        out.data_ptr(), _raw_stream(dev, stream))
+    w = _pack_matrix(bits, group, q.data_ptr(), scales.data_ptr(), biases.data_ptr())
+    st = library().moe_linear_quantized(x.data_ptr(), w, M, N, K, 1 if gated else 0,
+                                        _ptr(row_scale), _ptr(addend), out.data_ptr(),
+                                        _raw_stream(dev, stream))
     if st:
         _raise("moe_linear_quantized", st)
     return out

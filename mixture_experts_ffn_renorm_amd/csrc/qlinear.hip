@@ -260,72 +260,117 @@ hipError_t launch_gemv(const moe_host::QLinearArgs& a, hipStream_t s) {
 // workgroup hold the slices of one K (in turns where there are more slices
 // than waves).  A tile's sums wait in LDS until the workgroup's tiles are
 // done and are then added over the waves.
+//
+// Memory is read in runs of a row (x 256 NB bytes, codes 64 NB bytes at a
+// time) and turned to operands through the wave's own LDS: loads in operand
+// order touch 16 rows each and took three times as long.
 constexpr int kRowsWaves = 8;
-constexpr int kRowsLds = 64 * 1024;
+constexpr int kRowsSums = 64 * 1024;   // bytes of tile sums at most
 
 template <int G, int TM, int NB>
 __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host::QLinearArgs a,
                                                                        int ns, int tiles) {
-  constexpr int NG = 128 / G;      // groups per block
-  constexpr int NS = G / 32;       // MFMA steps per group
-  extern __shared__ __attribute__((aligned(16))) f32x4 sums[];   // [nw][tiles][TM][64]
+  constexpr int NG = 128 / G;        // groups per block
+  constexpr int NS = G / 32;         // MFMA steps per group
+  constexpr int NGT = NB * NG;       // groups per slice
+  constexpr int kPairs = (16 * NGT + 63) / 64;   // loads of (scale, bias) pairs per tile
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nw = blockDim.x >> 6;
+  uint8_t* own = lds + w * (NB * 4096);          // x, then each tile's codes and pairs
+  f32x4* sums = reinterpret_cast<f32x4*>(lds + nw * (NB * 4096));   // [nw][tiles][TM][64]
   const int r = lane & 15, g = lane >> 4;
   const int n_out = a.gated ? a.N / 2 : a.N;
   const int upr = a.K / 32, gpr = a.K / G;
   // gated: tiles 2 j and 2 j + 1 are the gate and up rows of the same outputs
   const int t0 = blockIdx.x * tiles;
-  auto row_of = [&](int tile) {
-    const int o = (a.gated ? tile >> 1 : tile) * 16 + r;
+  auto row_of = [&](int tile, int i) {
+    const int o = (a.gated ? tile >> 1 : tile) * 16 + i;
     return min(o, n_out - 1) + (a.gated && (tile & 1) ? n_out : 0);
+  };
+  // codes piece u of row i in LDS: distinct banks for the 16 rows of an operand
+  auto code_at = [&](int i, int u) {
+    const int f = NB == 1 ? (0x78 >> ((i >> 2) * 2)) & 3 : (i >> 1) & 7;   // 0 2 3 1
+    return i * (NB * 64) + ((u ^ f) << 4);
   };
   const WidenConst wc;
   const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 #pragma unroll 1
   for (int sl = w; sl < ns; sl += nw) {
-    const int u0 = sl * NB * 4 + g;   // this lane's unit of the slice's first block
     u32x4 cw[NB];
-    uint32_t cs[NB], cb[NB];
+    uint32_t cs[kPairs], cb[kPairs];
     auto load = [&](int tile) {
-      const size_t n = (size_t)row_of(t0 + tile);
-      const u32x4* q = reinterpret_cast<const u32x4*>(a.q) + n * upr;
-      const uint16_t *sp = a.scales + n * gpr, *bp = a.biases + n * gpr;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
+      for (int i = 0; i < NB; ++i) {
+        const int p = 64 * i + lane, u = sl * NB * 4 + p % (NB * 4);
         // a unit past the row's end is read as unit 0; its x is 0
-        const int u = u0 + 4 * b < upr ? u0 + 4 * b : 0;
-        cw[b] = __builtin_nontemporal_load(q + u);
-        cs[b] = sp[u * 32 / G];
-        cb[b] = bp[u * 32 / G];
+        cw[i] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4*>(a.q) +
+            (size_t)row_of(t0 + tile, p / (NB * 4)) * upr + (u < upr ? u : 0));
+      }
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const int e = (64 * i + lane) % (16 * NGT), gi = sl * NGT + e % NGT;
+        const size_t at = (size_t)row_of(t0 + tile, e / NGT) * gpr + (gi < gpr ? gi : 0);
+        cs[i] = a.scales[at];
+        cb[i] = a.biases[at];
       }
     };
+    u32x4 xv[TM][4 * NB];
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+#pragma unroll
+      for (int i = 0; i < 4 * NB; ++i) {
+        const int p = 64 * i + lane, m = p / (16 * NB);
+        const int k = sl * NB * kBlockK + p % (16 * NB) * 8;
+        xv[t][i] = load16_or_zero(a.x + (size_t)min(16 * t + m, a.M - 1) * a.K + k, k < a.K);
+      }
     load(0);
     u32x4 xp[TM][NB][4];
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
-      const uint16_t* xr = a.x + (size_t)min(16 * t + r, a.M - 1) * a.K;
+      // as in the tile kernel: piece of word st, lane group g at (4 st + g) ^ m
+#pragma unroll
+      for (int i = 0; i < 4 * NB; ++i) {
+        const int p = 64 * i + lane, m = p / (16 * NB), c = p % (16 * NB);
+        *reinterpret_cast<u32x4*>(own + m * (NB * 256) + (c >> 4) * 256 +
+                                  ((word_slot<G>(c & 15) ^ m) << 4)) = pair8(xv[t][i]);
+      }
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
-          const int k = (sl * NB + b) * kBlockK + word_k<G>(st, g);
-          u32x4 v = load16(xr + (k < a.K ? k : 0));
-          if (k >= a.K) v = u32x4{0u, 0u, 0u, 0u};
-          xp[t][b][st] = pair8(v);
-        }
+        for (int st = 0; st < 4; ++st)
+          xp[t][b][st] = *reinterpret_cast<const u32x4*>(own + r * (NB * 256) + b * 256 +
+                                                         (((4 * st + g) ^ r) << 4));
+      __builtin_amdgcn_wave_barrier();
     }
 #pragma unroll 1
     for (int tile = 0; tile < tiles; ++tile) {
+      uint32_t* pl = reinterpret_cast<uint32_t*>(own + NB * 1024);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int p = 64 * i + lane;
+        *reinterpret_cast<u32x4*>(own + code_at(p / (NB * 4), p % (NB * 4))) = cw[i];
+      }
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) pl[(64 * i + lane) % (16 * NGT)] = cs[i] | (cb[i] << 16);
+      __builtin_amdgcn_wave_barrier();
+      u32x4 wd[NB];
+      uint32_t pair[NGT];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        wd[b] = *reinterpret_cast<const u32x4*>(own + code_at(r, 4 * b + g));
+#pragma unroll
+      for (int j = 0; j < NGT; ++j) pair[j] = pl[r * NGT + j];
+      __builtin_amdgcn_wave_barrier();
+      load(min(tile + 1, tiles - 1));
       f32x4 tot[TM];
 #pragma unroll
       for (int t = 0; t < TM; ++t) tot[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        asm volatile("" : "+v"(cs[b]), "+v"(cb[b]));   // joined here, not where they are loaded
-        uint32_t pair[NG];
-        group_words<G>(cw[b]);
-        group_pairs<G>(u0 + 4 * b < upr ? cs[b] | (cb[b] << 16) : 0u, pair);
+        group_words<G>(wd[b]);
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
           f32x4 acc[TM], sx[TM];
@@ -333,15 +378,15 @@ __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host:
           for (int t = 0; t < TM; ++t) acc[t] = sx[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
-            const u32x4 wv = widen8(cw[b][j * NS + i], wc);
+            const u32x4 wv = widen8(wd[b][j * NS + i], wc);
 #pragma unroll
             for (int t = 0; t < TM; ++t) {
               sx[t] = mfma_16x16x32(xp[t][b][j * NS + i], ones, sx[t]);
               acc[t] = mfma_16x16x32(xp[t][b][j * NS + i], wv, acc[t]);
             }
           }
-          const float s = bf16_lo(pair[j]);
-          const float c = __builtin_fmaf(-128.f, s, bf16_hi(pair[j]));
+          const float s = bf16_lo(pair[b * NG + j]);
+          const float c = __builtin_fmaf(-128.f, s, bf16_hi(pair[b * NG + j]));
 #pragma unroll
           for (int t = 0; t < TM; ++t)
 #pragma unroll
@@ -349,7 +394,6 @@ __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host:
               tot[t][q] = __builtin_fmaf(s, acc[t][q], __builtin_fmaf(c, sx[t][q], tot[t][q]));
         }
       }
-      load(min(tile + 1, tiles - 1));
 #pragma unroll
       for (int t = 0; t < TM; ++t) {
         f32x4* p = sums + ((size_t)(w * tiles + tile) * TM + t) * 64 + lane;
@@ -388,27 +432,25 @@ hipError_t launch_rows_nb(const moe_host::QLinearArgs& a, hipStream_t s) {
   // the sums (gated: whole pairs of tiles)
   const long long want = 8LL * moe_host::device_cu_count() / nw;
   int tiles = (int)((total + want - 1) / want);
-  const int most = kRowsLds / (nw * TM * 1024);
+  const int most = kRowsSums / (nw * TM * 1024);
   tiles = tiles > most ? most : tiles;
   tiles = (tiles + per - 1) / per * per;
-  const size_t lds = (size_t)nw * tiles * TM * 1024;
+  constexpr int kMost = kRowsWaves * NB * 4096 + kRowsSums;
+  static bool set[moe_host::kMaxDevices] = {};
+  const hipError_t e = moe_host::ensure_dynamic_lds(
+      reinterpret_cast<const void*>(&qlinear_rows_kernel<G, TM, NB>), kMost, set);
+  if (e != hipSuccess) return e;
+  const size_t lds = (size_t)nw * (NB * 4096 + tiles * TM * 1024);
   hipLaunchKernelGGL((qlinear_rows_kernel<G, TM, NB>), dim3(ceil_div_host(total, tiles)),
                      dim3(64 * nw), lds, s, a, ns, tiles);
   return hipGetLastError();
 }
 
-// Blocks per wave: the fewest turns of at most four blocks over eight waves,
-// evenly filled.
+// Blocks per wave: one while eight waves hold all of K, else two.
 template <int G, int TM>
 hipError_t launch_rows(const moe_host::QLinearArgs& a, hipStream_t s) {
-  const int nblk = moe_host::ceil_div_host(a.K, kBlockK);
-  const int turns = moe_host::ceil_div_host(nblk, 4 * kRowsWaves);
-  switch (moe_host::ceil_div_host(nblk, turns * kRowsWaves)) {
-    case 1: return launch_rows_nb<G, TM, 1>(a, s);
-    case 2: return launch_rows_nb<G, TM, 2>(a, s);
-    case 3: return launch_rows_nb<G, TM, 3>(a, s);
-    default: return launch_rows_nb<G, TM, 4>(a, s);
-  }
+  if (a.K <= kRowsWaves * kBlockK) return launch_rows_nb<G, TM, 1>(a, s);
+  return launch_rows_nb<G, TM, 2>(a, s);
 }
 
 // ---- streaming kernel: few tokens ----

@@ -174,3 +174,9 @@ def test_misaligned_bias():
     lib = _moe().library()
     c = rule(bias=ODD)
     assert lib.moe_select(FAKE, ctypes.addressof(c), 4, 256, FAKE, FAKE, NULL) == -1
+
+
+def test_packed_matrix_is_the_struct():
+    moe = _moe()
+    w = moe.QuantizedMatrix(4, 64, 0x1230, 0x4560, 0x7890)
+    assert moe._pack_matrix(4, 64, 0x1230, 0x4560, 0x7890) == bytes(w)

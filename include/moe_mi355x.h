@@ -536,7 +536,8 @@ typedef struct moe_quantized_matrix {
  *   addend    [M, n_out] bf16 or NULL (0): e.g. the routed experts' output;
  *             may be out itself (added to in place)
  *   out       [M, n_out] bf16 out
- * One launch.  M, N, K < 2^24.
+ * One launch.  M, N, K < 2^24; M*N < 2^40.  A row of x that is not finite
+ * gives NaN in its own row of out.
  */
 int moe_linear_quantized(const uint16_t* x, const moe_quantized_matrix* w, int M, int N, int K,
                          int gated, const float* row_scale, const uint16_t* addend, uint16_t* out,

@@ -269,7 +269,8 @@ constexpr int kRowsSums = 64 * 1024;   // bytes of tile sums at most
 
 template <int G, int TM, int NB>
 __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host::QLinearArgs a,
-                                                                       int ns, int tiles) {
+                                                                       int ns, int tiles,
+                                                                       int wgs) {
   constexpr int NG = 128 / G;        // groups per block
   constexpr int NS = G / 32;         // MFMA steps per group
   constexpr int NGT = NB * NG;       // groups per slice
@@ -283,7 +284,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host:
   const int n_out = a.gated ? a.N / 2 : a.N;
   const int upr = a.K / 32, gpr = a.K / G;
   // gated: tiles 2 j and 2 j + 1 are the gate and up rows of the same outputs
-  const int t0 = blockIdx.x * tiles;
+  const int t0 = blockIdx.x % wgs * tiles, m0 = blockIdx.x / wgs * (16 * TM);
   auto row_of = [&](int tile, int i) {
     const int o = (a.gated ? tile >> 1 : tile) * 16 + i;
     return min(o, n_out - 1) + (a.gated && (tile & 1) ? n_out : 0);
@@ -295,37 +296,40 @@ __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host:
   };
   const WidenConst wc;
   const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-#pragma unroll 1
-  for (int sl = w; sl < ns; sl += nw) {
-    u32x4 cw[NB];
-    uint32_t cs[kPairs], cb[kPairs];
-    auto load = [&](int tile) {
+  u32x4 cw[NB];
+  uint32_t cs[kPairs], cb[kPairs];
+  auto load = [&](int sl, int tile) {
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const int p = 64 * i + lane, u = sl * NB * 4 + p % (NB * 4);
-        // a unit past the row's end is read as unit 0; its x is 0
-        cw[i] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4*>(a.q) +
-            (size_t)row_of(t0 + tile, p / (NB * 4)) * upr + (u < upr ? u : 0));
-      }
+    for (int i = 0; i < NB; ++i) {
+      const int p = 64 * i + lane, u = sl * NB * 4 + p % (NB * 4);
+      // a unit past the row's end is read as unit 0; its x is 0
+      cw[i] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4*>(a.q) +
+          (size_t)row_of(t0 + tile, p / (NB * 4)) * upr + (u < upr ? u : 0));
+    }
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        const int e = (64 * i + lane) % (16 * NGT), gi = sl * NGT + e % NGT;
-        const size_t at = (size_t)row_of(t0 + tile, e / NGT) * gpr + (gi < gpr ? gi : 0);
-        cs[i] = a.scales[at];
-        cb[i] = a.biases[at];
-      }
-    };
-    u32x4 xv[TM][4 * NB];
+    for (int i = 0; i < kPairs; ++i) {
+      const int e = (64 * i + lane) % (16 * NGT), gi = sl * NGT + e % NGT;
+      const size_t at = (size_t)row_of(t0 + tile, e / NGT) * gpr + (gi < gpr ? gi : 0);
+      cs[i] = a.scales[at];
+      cb[i] = a.biases[at];
+    }
+  };
+  u32x4 xv[TM][4 * NB];
+  auto load_x = [&](int sl) {
 #pragma unroll
     for (int t = 0; t < TM; ++t)
 #pragma unroll
       for (int i = 0; i < 4 * NB; ++i) {
         const int p = 64 * i + lane, m = p / (16 * NB);
         const int k = sl * NB * kBlockK + p % (16 * NB) * 8;
-        xv[t][i] = load16_or_zero(a.x + (size_t)min(16 * t + m, a.M - 1) * a.K + k, k < a.K);
+        xv[t][i] = load16_or_zero(a.x + (size_t)min(m0 + 16 * t + m, a.M - 1) * a.K + k, k < a.K);
       }
-    load(0);
+  };
+  load_x(w);
+  load(w, 0);
+#pragma unroll 1
+  for (int sl = w; sl < ns; sl += nw) {
     u32x4 xp[TM][NB][4];
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
@@ -345,6 +349,9 @@ __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host:
                                                          (((4 * st + g) ^ r) << 4));
       __builtin_amdgcn_wave_barrier();
     }
+    // the next turn's x (past the last: not used)
+    const int nsl = min(sl + nw, ns - 1);
+    load_x(nsl);
 #pragma unroll 1
     for (int tile = 0; tile < tiles; ++tile) {
       uint32_t* pl = reinterpret_cast<uint32_t*>(own + NB * 1024);
@@ -364,7 +371,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host:
 #pragma unroll
       for (int j = 0; j < NGT; ++j) pair[j] = pl[r * NGT + j];
       __builtin_amdgcn_wave_barrier();
-      load(min(tile + 1, tiles - 1));
+      load(tile + 1 < tiles ? sl : nsl, tile + 1 < tiles ? tile + 1 : 0);
       f32x4 tot[TM];
 #pragma unroll
       for (int t = 0; t < TM; ++t) tot[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -415,7 +422,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host:
     if (o >= n_out) continue;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int m = 16 * t + 4 * (ln >> 4) + q;
+      const int m = m0 + 16 * t + 4 * (ln >> 4) + q;
       if (m < a.M) store_out(a, a.gated ? silu_mul(y[q], up[q]) : y[q], m, o, n_out);
     }
   }
@@ -430,219 +437,32 @@ hipError_t launch_rows_nb(const moe_host::QLinearArgs& a, hipStream_t s) {
   const int nw = ns < kRowsWaves ? ns : kRowsWaves;
   // tiles per workgroup: about two waves for every SIMD, as far as LDS holds
   // the sums (gated: whole pairs of tiles)
+  const int mtile = ceil_div_host(a.M, 16 * TM);
   const long long want = 8LL * moe_host::device_cu_count() / nw;
-  int tiles = (int)((total + want - 1) / want);
+  int tiles = (int)(((long long)total * mtile + want - 1) / want);
   const int most = kRowsSums / (nw * TM * 1024);
-  tiles = tiles > most ? most : tiles;
   tiles = (tiles + per - 1) / per * per;
+  // one round of workgroups rather than a second, nearly empty one
+  while ((long long)ceil_div_host(total, tiles) * mtile > want && tiles < most) tiles += per;
+  if (tiles > most) tiles = most;
   constexpr int kMost = kRowsWaves * NB * 4096 + kRowsSums;
   static bool set[moe_host::kMaxDevices] = {};
   const hipError_t e = moe_host::ensure_dynamic_lds(
       reinterpret_cast<const void*>(&qlinear_rows_kernel<G, TM, NB>), kMost, set);
   if (e != hipSuccess) return e;
   const size_t lds = (size_t)nw * (NB * 4096 + tiles * TM * 1024);
-  hipLaunchKernelGGL((qlinear_rows_kernel<G, TM, NB>), dim3(ceil_div_host(total, tiles)),
-                     dim3(64 * nw), lds, s, a, ns, tiles);
+  const int wgs = ceil_div_host(total, tiles);
+  hipLaunchKernelGGL((qlinear_rows_kernel<G, TM, NB>), dim3((unsigned)wgs * mtile), dim3(64 * nw),
+                     lds, s, a, ns, tiles, wgs);
   return hipGetLastError();
 }
 
-// Blocks per wave: one while eight waves hold all of K, else two.
-template <int G, int TM>
+template <int G>
 hipError_t launch_rows(const moe_host::QLinearArgs& a, hipStream_t s) {
-  if (a.K <= kRowsWaves * kBlockK) return launch_rows_nb<G, TM, 1>(a, s);
-  return launch_rows_nb<G, TM, 2>(a, s);
-}
-
-// ---- streaming kernel: few tokens ----
-//
-// A wave owns 32 weight rows (gated: 16 gate rows and their 16 up rows) and
-// 16 TM tokens; `kw` waves of a workgroup split K in interleaved blocks and
-// add their sums through LDS.  Weights go from memory to registers once, a
-// few blocks ahead, and every token of the tile reads x from the caches.
-template <int G, int TM, bool kGated, int D>
-__global__ __launch_bounds__(512) void qlinear_stream_kernel(moe_host::QLinearArgs a, int kw,
-                                                             int ntile) {
-  constexpr int NG = 128 / G;      // groups per block
-  constexpr int NS = G / 32;       // MFMA steps per group
-  extern __shared__ __attribute__((aligned(16))) float red[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const int n_out = kGated ? a.N / 2 : a.N;
-  const int per_wg = (blockDim.x >> 6) / kw;                 // row tiles per workgroup
-  const int wg_n = ceil_div(ntile, per_wg);
-  const int bn = blockIdx.x % wg_n, bm = blockIdx.x / wg_n;
-  const int tile = bn * per_wg + wave / kw, part = wave % kw;
-  if (kw == 1 && tile >= ntile) return;   // whole wave; no barrier follows
-  const int m0 = bm * 16 * TM;
-  const int n0 = tile * (kGated ? 16 : 32);   // past the end: nothing is stored
-  const int nblk = ceil_div(a.K, kBlockK);
-  const int upr = a.K / 32, gpr = a.K / G;                   // units and groups per row
-
-  // rows past the ends are read as the last one and never stored
-  const u32x4* wrow[2];
-  const uint16_t *srow[2], *brow[2];
-#pragma unroll
-  for (int f = 0; f < 2; ++f) {
-    const int n = min(n0 + r + (kGated ? 0 : 16 * f), n_out - 1) + (kGated && f ? n_out : 0);
-    wrow[f] = reinterpret_cast<const u32x4*>(a.q) + (size_t)n * upr;
-    srow[f] = a.scales + (size_t)n * gpr;
-    brow[f] = a.biases + (size_t)n * gpr;
-  }
-  const uint16_t* xrow[TM];
-#pragma unroll
-  for (int t = 0; t < TM; ++t) xrow[t] = a.x + (size_t)min(m0 + 16 * t + r, a.M - 1) * a.K;
-
-  const WidenConst wc;
-  f32x4 tot[2][TM];
-#pragma unroll
-  for (int f = 0; f < 2; ++f)
-#pragma unroll
-    for (int t = 0; t < TM; ++t) tot[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  u32x4 wb[D][2], xb[D][TM][4];
-  uint16_t sb[D][2][2];   // scale, bias: joined only when used, so that no load is waited for here
-  auto load = [&](int blk, u32x4 (&w)[2], uint16_t (&p)[2][2], u32x4 (&xv)[TM][4]) {
-    // a unit past the row's end is read as unit 0; its x is cleared below
-    const int u = 4 * blk + g < upr ? 4 * blk + g : 0;
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      w[f] = __builtin_nontemporal_load(wrow[f] + u);
-      const int gi = u * 32 / G;
-      p[f][0] = srow[f][gi];
-      p[f][1] = brow[f][gi];
-    }
-#pragma unroll
-    for (int t = 0; t < TM; ++t)
-#pragma unroll
-      for (int st = 0; st < 4; ++st) {
-        const int k = blk * kBlockK + word_k<G>(st, g);
-        xv[t][st] = load16(xrow[t] + (k < a.K ? k : 0));
-      }
-  };
-  auto compute = [&](int blk, u32x4 (&w)[2], uint16_t (&p)[2][2], u32x4 (&xv)[TM][4]) {
-    if ((blk + 1) * kBlockK > a.K) {
-#pragma unroll
-      for (int st = 0; st < 4; ++st)
-        if (blk * kBlockK + word_k<G>(st, g) >= a.K)
-#pragma unroll
-          for (int t = 0; t < TM; ++t) xv[t][st] = u32x4{0u, 0u, 0u, 0u};
-    }
-    const bool in = 4 * blk + g < upr;
-    uint32_t pair[2][NG];
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      group_words<G>(w[f]);
-      group_pairs<G>(in ? (uint32_t)p[f][0] | ((uint32_t)p[f][1] << 16) : 0u, pair[f]);
-    }
-    const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-#pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      f32x4 acc[2][TM], sx[TM];
-#pragma unroll
-      for (int t = 0; t < TM; ++t) {
-        sx[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        acc[0][t] = acc[1][t] = sx[t];
-      }
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const int st = j * NS + i;
-        const u32x4 w0 = widen8(w[0][st], wc), w1 = widen8(w[1][st], wc);
-#pragma unroll
-        for (int t = 0; t < TM; ++t) {
-          const u32x4 xp = pair8(xv[t][st]);
-          sx[t] = mfma_16x16x32(xp, ones, sx[t]);
-          acc[0][t] = mfma_16x16x32(xp, w0, acc[0][t]);
-          acc[1][t] = mfma_16x16x32(xp, w1, acc[1][t]);
-        }
-      }
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const float s = bf16_lo(pair[f][j]);
-        const float c = __builtin_fmaf(-128.f, s, bf16_hi(pair[f][j]));
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            tot[f][t][q] = __builtin_fmaf(
-                s, acc[f][t][q], __builtin_fmaf(c, sx[t][q], tot[f][t][q]));
-      }
-    }
-  };
-
-  // blocks part, part + kw, ...; loads past the last one repeat it, so that
-  // no load sits behind a branch
-  const int n = (nblk - part + kw - 1) / kw;
-  auto at = [&](int i) { return min(part + i * kw, nblk - 1); };
-#pragma unroll
-  for (int i = 0; i < D; ++i) load(at(i), wb[i], sb[i], xb[i]);
-  int it = 0;
-  for (; it + D <= n; it += D) {
-#pragma unroll
-    for (int i = 0; i < D; ++i) {
-      compute(at(it + i), wb[i], sb[i], xb[i]);
-      load(at(it + i + D), wb[i], sb[i], xb[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < D - 1; ++i)
-    if (it + i < n) compute(at(it + i), wb[i], sb[i], xb[i]);
-  if (kw > 1) {
-    constexpr int kVals = 2 * TM * 4;
-    float* mine = red + (size_t)wave * kVals * 64 + lane;
-    if (part != 0) {
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mine[((f * TM + t) * 4 + q) * 64] = tot[f][t][q];
-    }
-    __syncthreads();
-    if (part != 0) return;
-    for (int o = 1; o < kw; ++o)
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            tot[f][t][q] += mine[(o * kVals + (f * TM + t) * 4 + q) * 64];
-  }
-  // lane: weight row r of each fragment, tokens 4 g .. 4 g + 3 of each tile
-#pragma unroll
-  for (int t = 0; t < TM; ++t)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int m = m0 + 16 * t + 4 * g + q;
-      if (m >= a.M) continue;
-      if (kGated) {
-        if (n0 + r < n_out) store_out(a, silu_mul(tot[0][t][q], tot[1][t][q]), m, n0 + r, n_out);
-      } else {
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-          if (n0 + 16 * f + r < n_out) store_out(a, tot[f][t][q], m, n0 + 16 * f + r, n_out);
-      }
-    }
-}
-
-template <int G, int TM, bool kGated, int D>
-hipError_t launch_stream(const moe_host::QLinearArgs& a, hipStream_t s) {
-  using moe_host::ceil_div_host;
-  const int n_out = kGated ? a.N / 2 : a.N;
-  const int ntile = ceil_div_host(n_out, kGated ? 16 : 32);
-  const int mtile = ceil_div_host(a.M, 16 * TM);
-  const int nblk = ceil_div_host(a.K, kBlockK);
-  // enough waves to keep two on every SIMD, as far as K has blocks to split
-  const long long want = 8LL * moe_host::device_cu_count();
-  int kw = 1;
-  while (kw < 8 && kw < nblk && (long long)ntile * mtile * kw < want) kw *= 2;
-  const int waves = kw < 4 ? 4 : kw;
-  const size_t lds = kw > 1 ? (size_t)waves * 2 * TM * 4 * 64 * sizeof(float) : 0;
-  const dim3 grid((unsigned)ceil_div_host(ntile, waves / kw) * mtile);
-  if (lds > 64 * 1024) return hipErrorInvalidValue;   // 8 waves x 8 KB at most
-  hipLaunchKernelGGL((qlinear_stream_kernel<G, TM, kGated, D>), grid, dim3(64 * waves), lds, s, a,
-                     kw, ntile);
-  return hipGetLastError();
+  if (a.M > 16) return launch_rows_nb<G, 2, 1>(a, s);
+  // one block per wave while eight waves hold all of K
+  if (a.K <= kRowsWaves * kBlockK) return launch_rows_nb<G, 1, 1>(a, s);
+  return launch_rows_nb<G, 1, 2>(a, s);
 }
 
 // ---- tile kernel: many tokens ----
@@ -946,34 +766,37 @@ hipError_t launch_tile_waves(const moe_host::QLinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int G>
-hipError_t launch_tile(const moe_host::QLinearArgs& a, hipStream_t s) {
+// Eight waves share a stage of x; four where that leaves CUs without work.
+int tile_waves(const moe_host::QLinearArgs& a) {
   using moe_host::ceil_div_host;
-  const int mtile = ceil_div_host(a.M, kTileM);
-  // eight waves share a stage of x; four where that leaves CUs without work
-  if (ceil_div_host(a.N, 256) * mtile >= moe_host::device_cu_count())
-    return launch_tile_waves<G, 8, 2>(a, s);
-  return launch_tile_waves<G, 4, 2>(a, s);
+  return ceil_div_host(a.N, 256) * ceil_div_host(a.M, kTileM) >= moe_host::device_cu_count() ? 8 : 4;
 }
 
 template <bool kGated>
 hipError_t launch_few(const moe_host::QLinearArgs& a, hipStream_t s) {
   if (a.M == 1) return launch_gemv<1, kGated>(a, s);
-  if (a.M == 2) return launch_gemv<2, kGated>(a, s);
-  return launch_gemv<4, kGated>(a, s);
+  return launch_gemv<2, kGated>(a, s);
 }
 
-template <int G, bool kGated>
-hipError_t launch_tokens(const moe_host::QLinearArgs& a, hipStream_t s) {
-  if (a.M <= 16) return launch_rows<G, 1>(a, s);
-  if (a.M <= 32) return launch_rows<G, 2>(a, s);
-  if (a.M > 64) return launch_tile<G>(a, s);
-  return launch_stream<G, 4, kGated, 1>(a, s);
+// The row tiles' time grows with 32-token tiles times rows, the LDS tiles'
+// with rounds of workgroups over the CUs, one a CU; both with K.  One round
+// takes as long as the row tiles need for about 170 rows per CU (measured us,
+// row / LDS tiles, K = 5632, N = 2048: 128 tokens 17 / 61, 512 tokens 47 / 62;
+// N = K = 8192: 64 tokens 37 / 86, 128 tokens 72 / 87, 256 tokens 142 / 88).
+bool use_rows(const moe_host::QLinearArgs& a) {
+  using moe_host::ceil_div_host;
+  const int cus = moe_host::device_cu_count();
+  const long long wgs =
+      (long long)ceil_div_host(a.N, 32 * tile_waves(a)) * ceil_div_host(a.M, kTileM);
+  const long long rounds = (wgs + cus - 1) / cus;
+  return (long long)ceil_div_host(a.M, 32) * a.N < rounds * 170 * cus;
 }
 
 template <int G>
 hipError_t launch_group(const moe_host::QLinearArgs& a, hipStream_t s) {
-  return a.gated ? launch_tokens<G, true>(a, s) : launch_tokens<G, false>(a, s);
+  if (a.M <= 16 || use_rows(a)) return launch_rows<G>(a, s);
+  if (tile_waves(a) == 8) return launch_tile_waves<G, 8, 2>(a, s);
+  return launch_tile_waves<G, 4, 2>(a, s);
 }
 
 }  // namespace
@@ -981,7 +804,7 @@ hipError_t launch_group(const moe_host::QLinearArgs& a, hipStream_t s) {
 namespace moe_host {
 
 hipError_t launch_qlinear(const QLinearArgs& a, hipStream_t s) {
-  if (a.M <= 4) return a.gated ? launch_few<true>(a, s) : launch_few<false>(a, s);
+  if (a.M <= 2) return a.gated ? launch_few<true>(a, s) : launch_few<false>(a, s);
   switch (a.group) {
     case 32: return launch_group<32>(a, s);
     case 64: return launch_group<64>(a, s);

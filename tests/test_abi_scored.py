@@ -128,7 +128,7 @@ LINEAR = [
     (dict(bits=8), -2), (dict(group=16), -2), (dict(group=256), -2), (dict(K=96), -2),
     (dict(M=-1), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(gated=2), -1),
     (dict(gated=1, N=33), -1), (dict(M=1 << 24), -2), (dict(N=1 << 24), -2),
-    (dict(K=1 << 24), -2), (dict(M=0, x=NULL, out=NULL), 0), (dict(x=NULL), -1),
+    (dict(K=1 << 24), -2), (dict(M=1 << 20, N=1 << 20), -2), (dict(M=0, x=NULL, out=NULL), 0), (dict(x=NULL), -1),
     (dict(out=NULL), -1), (dict(x=ODD), -1), (dict(out=ODD), -1), (dict(addend=ODD), -1),
     (dict(q=NULL), -1), (dict(scales=NULL), -1), (dict(biases=NULL), -1), (dict(q=ODD), -1),
 ]

@@ -535,7 +535,7 @@ typedef struct moe_quantized_matrix {
  *             weights that moe_route_scored gives for E = top_k = 1
  *   addend    [M, n_out] bf16 or NULL (0): e.g. the routed experts' output;
  *             may be out itself (added to in place)
- *   out       [M, n_out] bf16 out
+ *   out       [M, n_out] bf16 out, not x
  * One launch.  M, N, K < 2^24; M*N < 2^40.  A row of x that is not finite
  * gives NaN in its own row of out.
  */

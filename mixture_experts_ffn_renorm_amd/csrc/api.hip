@@ -679,7 +679,7 @@ int moe_linear_quantized(const uint16_t* x, const moe_quantized_matrix* w, int M
   if (M >= kMaxPairs || N >= kMaxPairs || K >= kMaxPairs) return MOE_ERR_UNSUPPORTED;
   if ((long long)M * N >= 1LL << 40) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
-  if (!x || !w->q || !w->scales || !w->biases || !out) return MOE_ERR_INVALID_ARG;
+  if (!x || !w->q || !w->scales || !w->biases || !out || out == x) return MOE_ERR_INVALID_ARG;
   if (!a16(x) || !a16(w->q) || !a16(w->scales) || !a16(w->biases) || !a16(out) || !a16(addend))
     return MOE_ERR_INVALID_ARG;
   QLinearArgs a{x, w->q, w->scales, w->biases, M, N, K, g, gated, row_scale, addend, out};

@@ -440,7 +440,7 @@ hipError_t launch_rows_nb(const moe_host::QLinearArgs& a, hipStream_t s) {
   const int mtile = ceil_div_host(a.M, 16 * TM);
   const long long want = 8LL * moe_host::device_cu_count() / nw;
   int tiles = (int)(((long long)total * mtile + want - 1) / want);
-  const int most = kRowsSums / (nw * TM * 1024);
+  const int most = kRowsSums / (nw * TM * 1024) / per * per;
   tiles = (tiles + per - 1) / per * per;
   // one round of workgroups rather than a second, nearly empty one
   while ((long long)ceil_div_host(total, tiles) * mtile > want && tiles < most) tiles += per;

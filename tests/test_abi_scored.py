@@ -125,6 +125,7 @@ def test_layers_need_a_rule_and_a_workspace():
 
 
 LINEAR = [
+    (dict(out=FAKE), -1),     # x in place
     (dict(bits=8), -2), (dict(group=16), -2), (dict(group=256), -2), (dict(K=96), -2),
     (dict(M=-1), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(gated=2), -1),
     (dict(gated=1, N=33), -1), (dict(M=1 << 24), -2), (dict(N=1 << 24), -2),
@@ -138,7 +139,7 @@ LINEAR = [
 def test_linear_refusals(change, status):
     moe = _moe()
     a = dict(x=FAKE, bits=4, group=64, q=FAKE, scales=FAKE, biases=FAKE, M=4, N=32, K=128, gated=0,
-             row_scale=NULL, addend=NULL, out=FAKE)
+             row_scale=NULL, addend=NULL, out=2 * FAKE)
     a.update(change)
     w = moe.QuantizedMatrix(a["bits"], a["group"], a["q"], a["scales"], a["biases"])
     assert moe.library().moe_linear_quantized(

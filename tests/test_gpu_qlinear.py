@@ -178,8 +178,10 @@ def test_large_products():
     """A prefill-sized product, checked on a sample of its rows and columns."""
     import torch
     moe = _moe()
+    # the last: more gate and up tiles per workgroup than its LDS holds, an
+    # odd number of K slices
     for M, N, K, group, gated in ((1, 65537, 512, 64, False), (520, 4096, 2048, 64, False),
-                                  (300, 5632, 1408, 128, True)):
+                                  (300, 5632, 1408, 128, True), (7, 480002, 384, 128, True)):
         q, s, b = matrix(N, K, group, 7)
         x = rows(M, K, 8)
         out = moe.moe_linear_quantized(h.dev_bf16(x), to_device(q, s, b, group), gated=gated)

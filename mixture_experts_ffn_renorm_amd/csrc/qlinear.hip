@@ -485,11 +485,12 @@ constexpr int kTileM = 64;
 constexpr int kTileK = 256;
 constexpr int kTileX = kTileM * kTileK * 2;      // bytes of x per stage
 
-template <int G, int W, int F>
+template <int G, int W>
 __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearArgs a, int ntile) {
   constexpr int NG = kTileK / G;                  // groups per stage
   constexpr int NX = (NG + 3) / 4;                // steps of the sums' product
   constexpr int NS = G / 32;                      // MFMA steps per group
+  constexpr int F = 2;                            // row fragments per wave
   constexpr int kSums = NX * 4 * kTileM * 16;     // bytes of sums per stage
   constexpr int kStage = kTileX + kSums;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -515,41 +516,74 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
   // read back from the wave's own LDS (piece c of row i at c ^ ((i >> 1) & 7):
   // 16 rows of an operand fall on distinct banks).  Scales and biases: four
   // lanes load a row's four groups.
+  //
+  // Addresses are a uniform base that moves with the stage and a 32-bit lane
+  // offset that does not (a tile's rows span less than 4 GB).
   const int lrow = lane >> 3, lpc = lane & 7;
-  const u32x4* wsrc[2 * F];
+  const char *wbase[F], *sbase[F], *bbase[F];
+  uint32_t woff[2 * F], soff[F];
 #pragma unroll
-  for (int i = 0; i < 2 * F; ++i)
-    wsrc[i] = reinterpret_cast<const u32x4*>(a.q) + (size_t)row_of(8 * i + lrow) * upr;
-  size_t srow[F];
+  for (int f = 0; f < F; ++f) {
+    const size_t row0 = (size_t)row_of(16 * f);
+    wbase[f] = reinterpret_cast<const char*>(a.q) + row0 * upr * 16;
+    sbase[f] = reinterpret_cast<const char*>(a.scales + row0 * gpr);
+    bbase[f] = reinterpret_cast<const char*>(a.biases + row0 * gpr);
 #pragma unroll
-  for (int f = 0; f < F; ++f) srow[f] = (size_t)row_of(16 * f + (lane >> 2)) * gpr;
+    for (int i = 2 * f; i < 2 * f + 2; ++i)
+      woff[i] = ((uint32_t)(row_of(8 * i + lrow) - row_of(16 * f)) * upr + lpc) * 16;
+    soff[f] = ((uint32_t)(row_of(16 * f + (lane >> 2)) - row_of(16 * f)) * gpr +
+               (lane & (NG < 4 ? NG - 1 : 3))) * 2;
+  }
   uint8_t* wl = lds + 2 * kStage + wave * (F * 2048);
   // x: 32 pieces of 8 elements per token and stage; a row of 16 lanes takes
   // half a token's, so a piece's group lies inside its row of lanes
   constexpr int kPer = kTileM * kTileK / 8 / (64 * W);   // pieces per thread
+  const char* xbase = reinterpret_cast<const char*>(a.x + (size_t)m0 * a.K);
+  uint32_t xoff[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int p = i * 64 * W + tid;
+    xoff[i] = (uint32_t)min(p >> 5, a.M - 1 - m0) * (uint32_t)a.K * 2 + (p & 31) * 16;
+  }
   u32x4 xr[kPer];
   u32x4 wn[2 * F];
   uint32_t sn[F][NX], bn[F][NX];
-  auto load_x = [&](int st) {
+  auto load = [&](int st) {
+    if ((st + 1) * kTileK <= a.K) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int p = i * 64 * W + tid, m = p >> 5, k = st * kTileK + (p & 31) * 8;
-      xr[i] = load16_or_zero(a.x + (size_t)min(m0 + m, a.M - 1) * a.K + k, k < a.K);
-    }
-  };
-  auto load_w = [&](int st) {
-    const int u = st * (kTileK / 32) + lpc;
+      for (int i = 0; i < kPer; ++i) xr[i] = load16(xbase + st * (kTileK * 2) + xoff[i]);
 #pragma unroll
-    for (int i = 0; i < 2 * F; ++i) wn[i] = load16(wsrc[i] + (u < upr ? u : 0));   // past K: its x is 0
+      for (int i = 0; i < 2 * F; ++i)
+        wn[i] = load16(wbase[i / 2] + st * (kTileK / 2) + woff[i]);
 #pragma unroll
-    for (int f = 0; f < F; ++f)
+      for (int f = 0; f < F; ++f)
 #pragma unroll
-      for (int j = 0; j < NX; ++j) {
-        const int gl = 4 * j + (lane & 3), gi = st * NG + gl;
-        const size_t at = srow[f] + (gl < NG && gi < gpr ? gi : 0);
-        sn[f][j] = a.scales[at];
-        bn[f][j] = a.biases[at];
+        for (int j = 0; j < NX; ++j) {
+          sn[f][j] = *reinterpret_cast<const uint16_t*>(sbase[f] + (st * NG + 4 * j) * 2 + soff[f]);
+          bn[f][j] = *reinterpret_cast<const uint16_t*>(bbase[f] + (st * NG + 4 * j) * 2 + soff[f]);
+        }
+    } else {
+      // the last, shorter stage: x past K is 0, codes and groups past it are
+      // read from the row's start
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const bool in = st * kTileK + ((i * 64 * W + tid) & 31) * 8 < a.K;
+        xr[i] = load16_or_zero(xbase + (in ? (uint32_t)(st * (kTileK * 2)) + xoff[i] : 0u), in);
       }
+      const uint32_t u = st * (kTileK / 32) + lpc < upr ? st * (kTileK / 2) : -lpc * 16;
+#pragma unroll
+      for (int i = 0; i < 2 * F; ++i) wn[i] = load16(wbase[i / 2] + (woff[i] + u));
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int j = 0; j < NX; ++j) {
+          const int gl = lane & (NG < 4 ? NG - 1 : 3);
+          const uint32_t at = soff[f] + (uint32_t)(st * NG + 4 * j + gl < gpr
+                                                       ? (st * NG + 4 * j) * 2 : -gl * 2);
+          sn[f][j] = *reinterpret_cast<const uint16_t*>(sbase[f] + at);
+          bn[f][j] = *reinterpret_cast<const uint16_t*>(bbase[f] + at);
+        }
+    }
   };
   auto store_w = [&]() {
 #pragma unroll
@@ -605,8 +639,7 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
       *reinterpret_cast<u32x4*>(lds + (i & 1) * kStage + kTileX + (NG * kTileM + (i >> 1)) * 16) =
           u32x4{0u, 0u, 0u, 0u};
 
-  load_x(0);
-  load_w(0);
+  load(0);
   store_x(0);
   store_w();
   __syncthreads();
@@ -629,8 +662,7 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
         pr[f][j] = (uint32_t)__shfl((int)(sn[f][j] | (bn[f][j] << 16)), 4 * r + g, kWave);
     }
     const int next = min(st + 1, nstage - 1);
-    load_x(next);
-    load_w(next);
+    load(next);
     uint32_t pair[F][NX * 4];
 #pragma unroll
     for (int f = 0; f < F; ++f)
@@ -750,18 +782,18 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
   }
 }
 
-template <int G, int W, int F>
+template <int G, int W>
 hipError_t launch_tile_waves(const moe_host::QLinearArgs& a, hipStream_t s) {
   using moe_host::ceil_div_host;
   constexpr int NX = (kTileK / G + 3) / 4;
-  constexpr int kLds = 2 * (kTileX + NX * 4 * kTileM * 16) + W * F * 2048;
+  constexpr int kLds = 2 * (kTileX + NX * 4 * kTileM * 16) + W * 4096;
   static bool set[moe_host::kMaxDevices] = {};
   const hipError_t e = moe_host::ensure_dynamic_lds(
-      reinterpret_cast<const void*>(&qlinear_tile_kernel<G, W, F>), kLds, set);
+      reinterpret_cast<const void*>(&qlinear_tile_kernel<G, W>), kLds, set);
   if (e != hipSuccess) return e;
-  const int ntile = ceil_div_host(a.gated ? a.N / 2 : a.N, a.gated ? 8 * F : 16 * F);
+  const int ntile = ceil_div_host(a.gated ? a.N / 2 : a.N, a.gated ? 16 : 32);
   const int tiles = ceil_div_host(ntile, W) * ceil_div_host(a.M, kTileM);
-  hipLaunchKernelGGL((qlinear_tile_kernel<G, W, F>), dim3((unsigned)ceil_div_host(tiles, 8) * 8),
+  hipLaunchKernelGGL((qlinear_tile_kernel<G, W>), dim3((unsigned)ceil_div_host(tiles, 8) * 8),
                      dim3(64 * W), kLds, s, a, ntile);
   return hipGetLastError();
 }
@@ -795,8 +827,8 @@ bool use_rows(const moe_host::QLinearArgs& a) {
 template <int G>
 hipError_t launch_group(const moe_host::QLinearArgs& a, hipStream_t s) {
   if (a.M <= 16 || use_rows(a)) return launch_rows<G>(a, s);
-  if (tile_waves(a) == 8) return launch_tile_waves<G, 8, 2>(a, s);
-  return launch_tile_waves<G, 4, 2>(a, s);
+  if (tile_waves(a) == 8) return launch_tile_waves<G, 8>(a, s);
+  return launch_tile_waves<G, 4>(a, s);
 }
 
 }  // namespace

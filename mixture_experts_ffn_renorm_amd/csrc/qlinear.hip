@@ -673,6 +673,8 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
 #pragma unroll
         for (int i = 0; i < 4; ++i) pair[f][4 * j + i] = p[i];
       }
+    // the wave that multiplies goes before the one that stages (2%)
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll 1
     for (int b = 0; b < 2; ++b) {
       if (NX == 2 || b == 0) {
@@ -733,6 +735,7 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
         for (int j = 0; j < NG / 2; ++j) pair[f][j] = pair[f][NG / 2 + j];
       }
     }
+    __builtin_amdgcn_s_setprio(0);
     if (st + 1 < nstage) {
       store_x(st + 1);
       store_w();

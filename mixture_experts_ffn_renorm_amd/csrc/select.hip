@@ -20,6 +20,9 @@ namespace {
 
 constexpr int kSelMaxE = 512;
 constexpr int kSelWaves = 4;
+// Candidates a token may have before its row is done over: with eight lanes
+// of sixteen experts open and top_k 8, 64 are too few for one token in 8000.
+constexpr int kSelCands = 128;
 
 // Order-preserving 64-bit key: larger value, larger key; -0 and +0 equal;
 // -inf above NaN above 0, the key of an expert that cannot be chosen.
@@ -354,9 +357,7 @@ template <int L, int C, int V>
 __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, int lpg) {
   constexpr int T = 64 / L;                    // tokens per wave
   constexpr int kList = 64;                    // rows to do over, per wave
-  // candidates a token may have: with eight lanes of sixteen experts open and
-  // top_k 8, 64 are too few for one token in 8000, 128 always enough
-  constexpr int kCands = L == 16 ? 128 : 64;
+  constexpr int kCands = kSelCands;
   struct TokenLds {
     uint64_t cand[kCands];                     // candidates' keys
     uint64_t top[34];                          // by rank
@@ -756,13 +757,22 @@ int per_lane(int L, int V, int G, int gs) {
 template <int V>
 hipError_t launch_select_v(const SelectArgs& a, hipStream_t s) {
   const int G = a.n_group, gs = a.E / G;
-  // A wave per token while the chip has waves for them; above, four or two
-  // tokens per wave, as far as the lane maxima (L of them) bound top_k well.
+  // Sixteen lanes a token where a lane has at most four experts, or where the
+  // batch fills the chip all the same; else 32, as far as the lane maxima
+  // bound top_k well.  Measured us, 16 / 32 / 64 lanes: 60 experts, 4096
+  // tokens 4.7 / 5.2 / 6.9; 128 experts, 1024 tokens 5.2 / 4.5 / 4.8, 65536
+  // 17.4 / 26.6 / 55.6; 512 experts, 8192 tokens 10.8 / 10.0 / 13.7, 65536
+  // 50.8 / 52.1 / 86.2; 256 experts in 8 groups, 64 tokens 9.1 / 6.3 / 6.8,
+  // 65536 45 / 52 / 107; 256 experts, top_k 16, 65536 tokens 81 / 41 / 73.
+  auto bounds = [&](int lanes) {
+    // else every expert of the groups that stay is a candidate
+    return lanes / G * a.topk_group >= a.top_k || a.topk_group * gs <= kSelCands;
+  };
+  const int n16 = per_lane(16, V, G, gs);
   int L = 64;
-  if (a.M > 16 * device_cu_count()) {
-    if (a.top_k <= 12 && per_lane(16, V, G, gs) <= 32) L = 16;
-    else if (a.top_k <= 26 && per_lane(32, V, G, gs) <= 16) L = 32;
-  }
+  if (a.top_k <= 12 && n16 <= 32 && bounds(16) &&
+      (n16 <= 4 || a.M > 4 * device_cu_count() * n16)) L = 16;
+  else if (a.top_k <= 26 && per_lane(32, V, G, gs) <= 16 && bounds(32)) L = 32;
   const int n = per_lane(L, V, G, gs), lpg = L / G;
   if (L == 64) {
     if (n <= 4) go<64, 4, V>(a, lpg, s);
@@ -804,9 +814,15 @@ hipError_t go_backward(const SelectArgs& a, const float* grad_weights, float* gr
 template <int V>
 hipError_t launch_backward_v(const SelectArgs& a, const float* grad_weights, float* grad_logits,
                              hipStream_t s) {
-  // as launch_select: a wave per token while the chip has waves for them
-  if (a.M <= 16 * device_cu_count()) return go_backward<64, V>(a, grad_weights, grad_logits, s);
-  if (a.top_k <= 16) return go_backward<16, V>(a, grad_weights, grad_logits, s);
+  // As launch_select.  Measured us, 16 / 32 lanes a token: 60 experts, 8192
+  // tokens 3.5 / 3.9; 128 experts, 1024 tokens 3.7 / 3.3, 16384 4.2 / 4.8; 512
+  // experts, 8192 tokens 5.8 / 5.5, 65536 34 / 38.  With a gradient for every
+  // logit, 128 experts, 65536 tokens 17.4 / 14.9.  (64 lanes: 512 experts, 1024
+  // tokens 3.4 against 3.5 with 32, 65536 tokens 41.)
+  const bool dense = !a.sigmoid && !a.renormalize;
+  const bool many = a.M > 4 * device_cu_count() * ceil_div_host(a.E, 16);
+  if (a.top_k <= 16 && (a.E <= 64 || (!dense && many)))
+    return go_backward<16, V>(a, grad_weights, grad_logits, s);
   return go_backward<32, V>(a, grad_weights, grad_logits, s);
 }
 

@@ -342,11 +342,12 @@ __device__ __forceinline__ void select_exactly(const SelectParams& a, int t, dou
 // 3. The top_k-th largest of the L lane maxima bounds the top_k-th largest c
 //    from below, so the experts at or above it (less the error) hold every
 //    one that can be chosen: usually little more than top_k.  They are packed
-//    into LDS, a sigmoid's choice scores evaluated again in double precision,
-//    and ranked against each other.
+//    into LDS and ranked against each other; where two neighbours in a biased
+//    sigmoid's order are closer than the error of c, again with choice scores
+//    in double precision.
 // 4. A row that this cannot decide is done over in double precision by the
 //    whole wave: two groups, or two neighbours in a biased softmax's order,
-//    closer than the error of c; -inf or NaN among the chosen; more than
+//    closer than the error of c; a sigmoid's closer than double precision's; -inf or NaN among the chosen; more than
 //    kCands candidates (rows of ties).
 //
 // Error of c: sigmoid 2^-22 (its slope times the exponent's rounding, two
@@ -532,53 +533,63 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
         }
       }
       __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-      for (int q = li; q < most; q += L) {
-        uint64_t key = 0ull;
-        if (q < total) {
-          const int id = s.id[q];
-          const float v = row[id];
-          if (refine) {
-            const double u = 1.0 + exp_f64(-(double)v);
-            key = (choice_key(1.0 / u + (double)a.bias[id]) & ~(uint64_t)(kSelMaxE - 1)) |
-                  (uint64_t)(kSelMaxE - 1 - id);
-          } else {
-            key = cand_key(by_logit ? v : hw_exp(v - mx) * rz + a.bias[id], id);
-          }
-        }
-        s.cand[q] = key;
-      }
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-      for (int q = li; q < most; q += L) {
-        const uint64_t my = s.cand[q];
-        int rank = 0;
-#pragma unroll 4
-        for (int o = 0; o < most; ++o) rank += s.cand[o] > my;
-        if (q < total && rank <= k) s.top[rank] = my;
-      }
-      __builtin_amdgcn_wave_barrier();
-      // lane j: slot j
+      // lane j: slot j, after a second turn with a sigmoid's keys in double
+      // precision if any token of the wave needs one
       int id = 0;
       float lj = -INFINITY;
-      if (li < k) {
-        const uint64_t my = s.top[li];
-        id = min(cand_id(my), E - 1);   // unset in a row that is done over
-        lj = by_logit ? cand_value(my) : row[id];
-        if (!by_logit && li + 1 < total) {
-          const uint64_t nx = s.top[li + 1];
-          bool close;
-          if (refine) {
-            // the keys dropped the last nine bits, and the doubles are an
-            // ulp or two off
-            close = my - nx < 2ull * kSelMaxE;
-          } else {
-            const float x = cand_value(my), y = cand_value(nx);
-            close = !(x - y > eps + 0x1p-22f * fmaxf(fabsf(x), fabsf(y)));
+      bool fine = false, close;
+#pragma unroll 1
+      for (;;) {
+#pragma unroll 1
+        for (int q = li; q < most; q += L) {
+          uint64_t key = 0ull;
+          if (q < total) {
+            const int id = s.id[q];
+            const float v = row[id];
+            if (fine) {
+              const double u = 1.0 + exp_f64(-(double)v);
+              key = (choice_key(1.0 / u + (double)a.bias[id]) & ~(uint64_t)(kSelMaxE - 1)) |
+                    (uint64_t)(kSelMaxE - 1 - id);
+            } else if (by_logit) {
+              key = cand_key(v, id);
+            } else {
+              const float e = __builtin_amdgcn_exp2f(kLog2e * (a.sigmoid ? -v : v - mx));
+              key = cand_key((a.sigmoid ? __builtin_amdgcn_rcpf(1.f + e) : e * rz) + a.bias[id], id);
+            }
           }
-          unsure = unsure || close;
+          s.cand[q] = key;
         }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int q = li; q < most; q += L) {
+          const uint64_t my = s.cand[q];
+          int rank = 0;
+#pragma unroll 4
+          for (int o = 0; o < most; ++o) rank += s.cand[o] > my;
+          if (q < total && rank <= k) s.top[rank] = my;
+        }
+        __builtin_amdgcn_wave_barrier();
+        close = false;
+        if (li < k) {
+          const uint64_t my = s.top[li];
+          id = min(cand_id(my), E - 1);   // unset in a row that is done over
+          lj = by_logit ? cand_value(my) : row[id];
+          if (!by_logit && li + 1 < total) {
+            const uint64_t nx = s.top[li + 1];
+            if (fine) {
+              // the keys dropped the last nine bits, and the doubles are an
+              // ulp or two off
+              close = my - nx < 2ull * kSelMaxE;
+            } else {
+              const float x = cand_value(my), y = cand_value(nx);
+              close = !(x - y > eps + 0x1p-22f * fmaxf(fabsf(x), fabsf(y)));
+            }
+          }
+        }
+        if (!refine || fine || !__any(close)) break;
+        fine = true;
       }
+      unsure = unsure || close;
       if (!by_logit) unsure = lanes_max<L>(unsure ? 1.f : 0.f) > 0.f;
       float wt;
       if (a.renormalize) {
@@ -742,8 +753,10 @@ void go(const SelectArgs& a, int lpg, hipStream_t s) {
                        a.n_group, a.topk_group, a.group_top, a.scale, a.topk_ids,
                        a.topk_weights};
   constexpr int per = kSelWaves * 64 / L;
-  // waves of a large batch take several turns: the bias stays in registers
-  const int wgs = ceil_div_host(a.M, per), most = 8 * device_cu_count();
+  // waves of a large batch take several turns: two rounds of the workgroups
+  // that a CU holds (five; three with 32 experts a lane).  Eight for all took
+  // 50.7 us where this takes 47.2 (65536 x 512), 17.4 against 15.9 (65536 x 128)
+  const int wgs = ceil_div_host(a.M, per), most = (C == 32 ? 6 : 10) * device_cu_count();
   hipLaunchKernelGGL((select_kernel<L, C, V>), dim3(wgs < most ? wgs : most), dim3(64 * kSelWaves),
                      0, s, p, lpg);
 }

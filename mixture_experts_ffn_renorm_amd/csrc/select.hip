@@ -347,13 +347,20 @@ __device__ __forceinline__ void select_exactly(const SelectParams& a, int t, dou
 //    in double precision.
 // 4. A row that this cannot decide is done over in double precision by the
 //    whole wave: two groups, or two neighbours in a biased softmax's order,
-//    closer than the error of c; a sigmoid's closer than double precision's; -inf or NaN among the chosen; more than
-//    kCands candidates (rows of ties).
+//    closer than the error of c; a sigmoid's closer than double precision's;
+//    -inf or NaN among the chosen; more than kCands candidates (rows of ties).
 //
 // Error of c: sigmoid 2^-22 (its slope times the exponent's rounding, two
 // hardware transcendentals, two roundings), softmax 2^-19 of the largest
 // probability (the common sum of C / 4 + 6 terms in a row, each rounding
 // once), and 2^-24 |c| for the bias.
+//
+// Bound by vector instructions, two transcendentals per expert among them,
+// and, for few tokens, by the chain of steps: 65536 x 512, sigmoid with a
+// bias, top_k 10, in 47.5 us (2.9 TB/s of logits; 37 us for a softmax without
+// one), 8192 x 256 in 8 groups in 9.3, one token in 5.6 (3 of them the
+// launch).  A wave per token with every comparison in double precision, the
+// simplest form, took 192 and 37 us for the first two.
 template <int L, int C, int V>
 __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, int lpg) {
   constexpr int T = 64 / L;                    // tokens per wave
@@ -594,7 +601,9 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
       float wt;
       if (a.renormalize) {
         const float m = lanes_max<L>(lj);
-        const float sh = li < k ? fast_score(lj, a.sigmoid ? fminf(m, 0.f) : m, a.sigmoid) : 0.f;
+        // a bias may choose experts whose logits are -inf, and those alone
+        const float sh = li < k && m > -INFINITY
+                             ? fast_score(lj, a.sigmoid ? fminf(m, 0.f) : m, a.sigmoid) : 0.f;
         const float sum = lanes_sum<L>(sh);
         wt = sum == 0.f ? 0.f : a.scale * (sh * __builtin_amdgcn_rcpf(sum));
       } else if (a.sigmoid) {
@@ -773,10 +782,10 @@ hipError_t launch_select_v(const SelectArgs& a, hipStream_t s) {
   // Sixteen lanes a token where a lane has at most four experts, or where the
   // batch fills the chip all the same; else 32, as far as the lane maxima
   // bound top_k well.  Measured us, 16 / 32 / 64 lanes: 60 experts, 4096
-  // tokens 4.7 / 5.2 / 6.9; 128 experts, 1024 tokens 5.2 / 4.5 / 4.8, 65536
-  // 17.4 / 26.6 / 55.6; 512 experts, 8192 tokens 10.8 / 10.0 / 13.7, 65536
-  // 50.8 / 52.1 / 86.2; 256 experts in 8 groups, 64 tokens 9.1 / 6.3 / 6.8,
-  // 65536 45 / 52 / 107; 256 experts, top_k 16, 65536 tokens 81 / 41 / 73.
+  // tokens 4.7 / 5.2 / 6.9; 128 experts, 1024 tokens 5.1 / 4.5 / 4.8, 65536
+  // 16.8 / 26.1 / 54.2; 512 experts, 8192 tokens 11.6 / 9.9 / 13.1, 65536
+  // 47.5 / 48.8 / 78.5; 256 experts in 8 groups, 64 tokens 8.8 / 6.0 / 6.5,
+  // 65536 40 / 49 / 97; 256 experts, top_k 16, 65536 tokens 77 / 39 / 67.
   auto bounds = [&](int lanes) {
     // else every expert of the groups that stay is a candidate
     return lanes / G * a.topk_group >= a.top_k || a.topk_group * gs <= kSelCands;

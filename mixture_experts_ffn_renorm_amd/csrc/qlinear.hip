@@ -40,17 +40,8 @@ __device__ __forceinline__ void group_words(u32x4& w) {
   w = u32x4{a, b, c, d};
 }
 
-// The k offset inside a block of the 8 codes that lane group g holds in word
-// st after group_words.
-template <int G>
-__device__ __forceinline__ int word_k(int st, int g) {
-  if (G == 128) return 32 * g + 8 * st;
-  if (G == 64) return (g < 2 ? 32 * g : 32 * (g - 2) + 16) + 64 * (st >> 1) + 8 * (st & 1);
-  return 32 * st + 8 * g;
-}
-
 // 4 word + lane group of the operand that takes piece c (8 elements) of a
-// block: word_k's inverse.
+// block: where group_words puts the codes of elements 8 c .. 8 c + 7.
 template <int G>
 __device__ __forceinline__ int word_slot(int c) {
   if (G == 128) return ((c & 3) << 2) | (c >> 2);
@@ -58,24 +49,15 @@ __device__ __forceinline__ int word_slot(int c) {
   return c;
 }
 
-// Each group's (scale, bias) pair in every lane of its row, from the pair of
-// the lane's own unit.
-template <int G>
-__device__ __forceinline__ void group_pairs(uint32_t own, uint32_t (&p)[128 / G]) {
+// The four lanes' values of a row, each in every lane of that row.
+__device__ __forceinline__ void row_values(uint32_t own, uint32_t (&p)[4]) {
+  uint32_t other = own;
   p[0] = own;
-  if constexpr (G <= 64) {
-    uint32_t other = own;
-    swap32(p[0], other);
-    if constexpr (G == 64) {
-      p[1] = other;
-    } else {
-      p[2] = other;
-      p[1] = p[0];
-      p[3] = p[2];
-      swap16(p[0], p[1]);
-      swap16(p[2], p[3]);
-    }
-  }
+  swap32(p[0], other);
+  p[1] = p[0];
+  p[2] = p[3] = other;
+  swap16(p[0], p[1]);
+  swap16(p[2], p[3]);
 }
 
 // 8 codes as bf16 values 128 + q, pairs (i, i + 4).  The constants are kept
@@ -114,7 +96,7 @@ __device__ __forceinline__ void store_out(const moe_host::QLinearArgs& a, float 
   a.out[at] = (uint16_t)f32_to_bf16(y);
 }
 
-// ---- GEMV: one to four tokens ----
+// ---- GEMV: one or two tokens ----
 //
 // A lane keeps one unit (32 elements) of each token's x in registers, as the
 // pairs that the codes widen to, and walks over weight rows: four rows at a
@@ -123,6 +105,12 @@ __device__ __forceinline__ void store_out(const moe_host::QLinearArgs& a, float 
 // (more than kGemvWaves slices: in turns, x read again).  The four rows' sums
 // over the lanes share their first two steps (lane swaps), and the sums wait
 // in LDS until the workgroup's rows are done.
+//
+// Bound by the codes' bytes where there are many (131072 x 2048, one token:
+// 29 us, 5.2 TB/s, what a large copy reaches) and by launch, load and join
+// where there are few (2048 x 2048: 3.9 us, of which an empty kernel takes 3).
+// Two tokens: N = K = 8192 13.2 us against 15.3 with the row tiles below,
+// N = 2048, K = 5632 5.3 / 8.4; three are faster there (15.1 / 16.3).
 constexpr int kGemvWaves = 8;
 constexpr int kGemvMaxRows = 64;   // weight rows per wave group
 
@@ -264,6 +252,10 @@ hipError_t launch_gemv(const moe_host::QLinearArgs& a, hipStream_t s) {
 // Memory is read in runs of a row (x 256 NB bytes, codes 64 NB bytes at a
 // time) and turned to operands through the wave's own LDS: loads in operand
 // order touch 16 rows each and took three times as long.
+//
+// Bound by the latency of its loads: a workgroup reads all of its tokens' x
+// before the first product.  16 tokens, N = 11264 gated, K = 2048, groups of
+// 32: 9.1 us (1.6 TB/s); N = K = 8192: 15.7 us (2.4 TB/s).
 constexpr int kRowsWaves = 8;
 constexpr int kRowsSums = 64 * 1024;   // bytes of tile sums at most
 
@@ -460,8 +452,13 @@ hipError_t launch_rows_nb(const moe_host::QLinearArgs& a, hipStream_t s) {
 template <int G>
 hipError_t launch_rows(const moe_host::QLinearArgs& a, hipStream_t s) {
   if (a.M > 16) return launch_rows_nb<G, 2, 1>(a, s);
-  // one block per wave while eight waves hold all of K
-  if (a.K <= kRowsWaves * kBlockK) return launch_rows_nb<G, 1, 1>(a, s);
+  // One block per wave where eight waves hold all of K and a CU has few codes
+  // to read.  Measured us, one / two blocks: K = 512, N = 8192 4.3 / 4.8,
+  // 65536 10.2 / 9.0; K = 1024, N = 2048 4.3 / 4.5, 65536 18.0 / 12.4; K = 2048,
+  // N = 11264 9.5 / 7.7; N = K = 8192 21.2 / 15.7.
+  if (a.K <= kRowsWaves * kBlockK &&
+      (long long)a.N * a.K <= 32768LL * moe_host::device_cu_count())
+    return launch_rows_nb<G, 1, 1>(a, s);
   return launch_rows_nb<G, 1, 2>(a, s);
 }
 
@@ -481,6 +478,13 @@ hipError_t launch_rows(const moe_host::QLinearArgs& a, hipStream_t s) {
 // s themselves, eight k slots per group [b b b s s s 0 0] x
 // [h m l -128h -128m -128l 0 0], so one more MFMA step per four groups adds it
 // to the fp32 sums, where FMAs would cost as much vector time as the scaling.
+//
+// 2048 tokens, N = 2048, K = 5632, groups of 128: 63.5 us (744 TFLOP/s; a
+// large library product in bf16 reaches 1204), groups of 64 68 us, of 32 85.
+// Bound by the two waves that a SIMD holds: matrix instructions fill 31% of
+// its time, vector ones (widening, scaling, staging) overlap them in part.
+// Tiles of 64 x 64 per wave, one wave a SIMD, took 95 us; 32 tokens per wave
+// and four waves a SIMD 75; both blocks of a stage unrolled up to 2.4 times.
 constexpr int kTileM = 64;
 constexpr int kTileK = 256;
 constexpr int kTileX = kTileM * kTileK * 2;      // bytes of x per stage
@@ -669,7 +673,7 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
 #pragma unroll
       for (int j = 0; j < NX; ++j) {
         uint32_t p[4];
-        group_pairs<32>(pr[f][j], p);
+        row_values(pr[f][j], p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) pair[f][4 * j + i] = p[i];
       }
@@ -801,7 +805,9 @@ hipError_t launch_tile_waves(const moe_host::QLinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Eight waves share a stage of x; four where that leaves CUs without work.
+// Eight waves share a stage of x; four where that leaves CUs without work
+// (measured us, eight / four: 2048 tokens, N = 2048, K = 5632 69 / 122; 1024
+// tokens 66 / 62; 256 tokens, N = K = 8192 96 / 88).
 int tile_waves(const moe_host::QLinearArgs& a) {
   using moe_host::ceil_div_host;
   return ceil_div_host(a.N, 256) * ceil_div_host(a.M, kTileM) >= moe_host::device_cu_count() ? 8 : 4;

@@ -537,7 +537,8 @@ typedef struct moe_quantized_matrix {
  *             may be out itself (added to in place)
  *   out       [M, n_out] bf16 out, not x
  * One launch.  M, N, K < 2^24; M*N < 2^40.  A row of x that is not finite
- * gives NaN in its own row of out.
+ * gives NaN in its own row of out; so may one with |x| of 2^112 or more (a
+ * group's sums of (128 + code) x are held in fp32).
  */
 int moe_linear_quantized(const uint16_t* x, const moe_quantized_matrix* w, int M, int N, int K,
                          int gated, const float* row_scale, const uint16_t* addend, uint16_t* out,

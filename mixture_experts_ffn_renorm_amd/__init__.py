@@ -673,10 +673,14 @@ def _raw_stream(device: int, stream) -> int:
 
 
 def _empty(shape, dtype, device: int, stream):
-    """A new tensor that the call's stream may use."""
-    t = _torch().empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    """A new tensor that the call's stream may write at once (memory of the
+    current stream may still be in use there) and the current one may read."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -879,7 +883,7 @@ def moe_linear_quantized(x, weight: dict, gated: bool = False, row_scale=None, a
     [N, K/group_size] (bf16).  ``gated``: the first N/2 rows are gates and
     f = SiLU(gate) * up, n_out = N/2; else f is the identity, n_out = N.
     ``row_scale`` [M] fp32 and ``addend`` [M, n_out] bf16 (``out`` itself, to
-    add in place) are optional."""
+    add in place) are optional.  |x| is below 2^112 (a group's sums in fp32)."""
     torch = _torch()
     M, K = x.shape
     bits, group = int(weight["bits"]), int(weight.get("group_size", 64))

@@ -195,3 +195,24 @@ def test_product_tiles_keep_rows_apart_and_replay(M, N):
     out = [[moe.moe_linear_quantized(x, w, stream=s) for w, s in zip(ws, streams)] for _ in range(4)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for rnd in out for a, b in zip(rnd, want))
+
+
+def test_outputs_for_another_stream_do_not_take_the_current_ones_memory():
+    """What the current stream freed it may still be using: a tensor made for
+    a call on another stream comes from elsewhere."""
+    import torch
+    moe = ts._moe()
+    E, k, M = 64, 4, 1 << 18
+    l = h.dev_f32(ts.draw(M, E, 1))
+    r = moe.Routing(k)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    before = [torch.empty((M, k), dtype=torch.int32, device="cuda"),
+              torch.empty((M, k), dtype=torch.float32, device="cuda")]
+    used = {t.data_ptr() for t in before}
+    del before
+    ids, w = moe.moe_select(l, r, stream=s)
+    assert not {ids.data_ptr(), w.data_ptr()} & used
+    torch.cuda.current_stream().wait_stream(s)
+    a, b = moe.moe_select(l, r)
+    assert torch.equal(ids, a) and torch.equal(w, b)

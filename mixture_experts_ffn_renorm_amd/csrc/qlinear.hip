@@ -109,8 +109,8 @@ __device__ __forceinline__ void store_out(const moe_host::QLinearArgs& a, float 
 // Bound by the codes' bytes where there are many (131072 x 2048, one token:
 // 29 us, 5.2 TB/s, what a large copy reaches) and by launch, load and join
 // where there are few (2048 x 2048: 3.9 us, of which an empty kernel takes 3).
-// Two tokens: N = K = 8192 13.2 us against 15.3 with the row tiles below,
-// N = 2048, K = 5632 5.3 / 8.4; three are faster there (15.1 / 16.3).
+// Two tokens: N = K = 8192 13.2 us against 14.0 with the row tiles below,
+// N = 2048, K = 5632 5.3 / 8.1; three are faster there (13.5 / 16.3).
 constexpr int kGemvWaves = 8;
 constexpr int kGemvMaxRows = 64;   // weight rows per wave group
 
@@ -253,9 +253,17 @@ hipError_t launch_gemv(const moe_host::QLinearArgs& a, hipStream_t s) {
 // time) and turned to operands through the wave's own LDS: loads in operand
 // order touch 16 rows each and took three times as long.
 //
-// Bound by the latency of its loads: a workgroup reads all of its tokens' x
-// before the first product.  16 tokens, N = 11264 gated, K = 2048, groups of
-// 32: 9.1 us (1.6 TB/s); N = K = 8192: 15.7 us (2.4 TB/s).
+// A group's sum of x is formed once per slice (a product with ones) and kept.
+// The codes' loads are ordinary ones: token tiles of one N share them in the
+// caches (512 tokens, N = 2048, K = 5632 39 us, non-temporal 43), and one
+// token tile gains as well (N = K = 8192 13.8 / 15.1).
+//
+// Up to 16 tokens bound by the latency of its loads: a workgroup reads all of
+// its tokens' x before the first product.  16 tokens, N = 11264 gated, K =
+// 2048, groups of 32: 8.8 us (1.7 TB/s); N = K = 8192: 13.8 us (2.7 TB/s).
+// Above, by vector instructions (two thirds of the time): 512 tokens, N =
+// 2048, K = 5632 39 us (300 TFLOP/s).  Two to four tiles' codes in flight in
+// place of one changed nothing.
 constexpr int kRowsWaves = 8;
 constexpr int kRowsSums = 64 * 1024;   // bytes of tile sums at most
 
@@ -290,13 +298,19 @@ __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host:
   const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
   u32x4 cw[NB];
   uint32_t cs[kPairs], cb[kPairs];
-  auto load = [&](int sl, int tile) {
+  // the next piece to load: slice, tile
+  int lsl = w, ltile = 0;
+  auto load = [&]() {
+    const int sl = lsl, tile = ltile;
+    if (++ltile == tiles) {
+      ltile = 0;
+      lsl = min(lsl + nw, ns - 1);   // past the last slice: not used
+    }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       const int p = 64 * i + lane, u = sl * NB * 4 + p % (NB * 4);
       // a unit past the row's end is read as unit 0; its x is 0
-      cw[i] = __builtin_nontemporal_load(
-          reinterpret_cast<const u32x4*>(a.q) +
+      cw[i] = *(reinterpret_cast<const u32x4*>(a.q) +
           (size_t)row_of(t0 + tile, p / (NB * 4)) * upr + (u < upr ? u : 0));
     }
 #pragma unroll
@@ -319,10 +333,11 @@ __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host:
       }
   };
   load_x(w);
-  load(w, 0);
-#pragma unroll 1
-  for (int sl = w; sl < ns; sl += nw) {
-    u32x4 xp[TM][NB][4];
+  load();
+  u32x4 xp[TM][NB][4];
+  f32x4 sx[TM][NGT];   // each group's sums of x
+  int sl = w, tile = 0;
+  auto turn_x = [&]() {
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
       // as in the tile kernel: piece of word st, lane group g at (4 st + g) ^ m
@@ -341,63 +356,73 @@ __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host:
                                                          (((4 * st + g) ^ r) << 4));
       __builtin_amdgcn_wave_barrier();
     }
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+#pragma unroll
+      for (int j = 0; j < NGT; ++j) {
+        sx[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+          sx[t][j] = mfma_16x16x32(xp[t][j / NG][j % NG * NS + i], ones, sx[t][j]);
+      }
     // the next turn's x (past the last: not used)
-    const int nsl = min(sl + nw, ns - 1);
-    load_x(nsl);
+    load_x(min(sl + nw, ns - 1));
+  };
 #pragma unroll 1
-    for (int tile = 0; tile < tiles; ++tile) {
-      uint32_t* pl = reinterpret_cast<uint32_t*>(own + NB * 1024);
+  while (sl < ns) {
+    if (tile == 0) turn_x();
+    uint32_t* pl = reinterpret_cast<uint32_t*>(own + NB * 1024);
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const int p = 64 * i + lane;
-        *reinterpret_cast<u32x4*>(own + code_at(p / (NB * 4), p % (NB * 4))) = cw[i];
-      }
+    for (int i = 0; i < NB; ++i) {
+      const int p = 64 * i + lane;
+      *reinterpret_cast<u32x4*>(own + code_at(p / (NB * 4), p % (NB * 4))) = cw[i];
+    }
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) pl[(64 * i + lane) % (16 * NGT)] = cs[i] | (cb[i] << 16);
-      __builtin_amdgcn_wave_barrier();
-      u32x4 wd[NB];
-      uint32_t pair[NGT];
+    for (int i = 0; i < kPairs; ++i) pl[(64 * i + lane) % (16 * NGT)] = cs[i] | (cb[i] << 16);
+    __builtin_amdgcn_wave_barrier();
+    u32x4 wd[NB];
+    uint32_t pair[NGT];
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        wd[b] = *reinterpret_cast<const u32x4*>(own + code_at(r, 4 * b + g));
+    for (int b = 0; b < NB; ++b)
+      wd[b] = *reinterpret_cast<const u32x4*>(own + code_at(r, 4 * b + g));
 #pragma unroll
-      for (int j = 0; j < NGT; ++j) pair[j] = pl[r * NGT + j];
-      __builtin_amdgcn_wave_barrier();
-      load(tile + 1 < tiles ? sl : nsl, tile + 1 < tiles ? tile + 1 : 0);
-      f32x4 tot[TM];
+    for (int j = 0; j < NGT; ++j) pair[j] = pl[r * NGT + j];
+    __builtin_amdgcn_wave_barrier();
+    load();
+    f32x4 tot[TM];
 #pragma unroll
-      for (int t = 0; t < TM; ++t) tot[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < TM; ++t) tot[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        group_words<G>(wd[b]);
+    for (int b = 0; b < NB; ++b) {
+      group_words<G>(wd[b]);
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          f32x4 acc[TM], sx[TM];
+      for (int j = 0; j < NG; ++j) {
+        f32x4 acc[TM];
 #pragma unroll
-          for (int t = 0; t < TM; ++t) acc[t] = sx[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < TM; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            const u32x4 wv = widen8(wd[b][j * NS + i], wc);
+        for (int i = 0; i < NS; ++i) {
+          const u32x4 wv = widen8(wd[b][j * NS + i], wc);
 #pragma unroll
-            for (int t = 0; t < TM; ++t) {
-              sx[t] = mfma_16x16x32(xp[t][b][j * NS + i], ones, sx[t]);
-              acc[t] = mfma_16x16x32(xp[t][b][j * NS + i], wv, acc[t]);
-            }
-          }
-          const float s = bf16_lo(pair[b * NG + j]);
-          const float c = __builtin_fmaf(-128.f, s, bf16_hi(pair[b * NG + j]));
-#pragma unroll
-          for (int t = 0; t < TM; ++t)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              tot[t][q] = __builtin_fmaf(s, acc[t][q], __builtin_fmaf(c, sx[t][q], tot[t][q]));
+          for (int t = 0; t < TM; ++t) acc[t] = mfma_16x16x32(xp[t][b][j * NS + i], wv, acc[t]);
         }
-      }
+        const float s = bf16_lo(pair[b * NG + j]);
+        const float c = __builtin_fmaf(-128.f, s, bf16_hi(pair[b * NG + j]));
 #pragma unroll
-      for (int t = 0; t < TM; ++t) {
-        f32x4* p = sums + ((size_t)(w * tiles + tile) * TM + t) * 64 + lane;
-        *p = sl == w ? tot[t] : *p + tot[t];
+        for (int t = 0; t < TM; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            tot[t][q] = __builtin_fmaf(s, acc[t][q], __builtin_fmaf(c, sx[t][b * NG + j][q], tot[t][q]));
       }
+    }
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      f32x4* p = sums + ((size_t)(w * tiles + tile) * TM + t) * 64 + lane;
+      *p = sl == w ? tot[t] : *p + tot[t];
+    }
+    if (++tile == tiles) {
+      tile = 0;
+      sl += nw;
     }
   }
   __syncthreads();
@@ -453,9 +478,9 @@ template <int G>
 hipError_t launch_rows(const moe_host::QLinearArgs& a, hipStream_t s) {
   if (a.M > 16) return launch_rows_nb<G, 2, 1>(a, s);
   // One block per wave where eight waves hold all of K and a CU has few codes
-  // to read.  Measured us, one / two blocks: K = 512, N = 8192 4.3 / 4.8,
-  // 65536 10.2 / 9.0; K = 1024, N = 2048 4.3 / 4.5, 65536 18.0 / 12.4; K = 2048,
-  // N = 11264 9.5 / 7.7; N = K = 8192 21.2 / 15.7.
+  // to read.  Measured us, one / two blocks: K = 512, N = 8192 4.4 / 5.1,
+  // 65536 9.0 / 8.7; K = 1024, N = 2048 4.3 / 4.4, 65536 14.7 / 12.0; K = 2048,
+  // N = 11264 8.3 / 7.2; N = K = 8192 16.3 / 14.0.
   if (a.K <= kRowsWaves * kBlockK &&
       (long long)a.N * a.K <= 32768LL * moe_host::device_cu_count())
     return launch_rows_nb<G, 1, 1>(a, s);
@@ -837,16 +862,17 @@ hipError_t launch_few(const moe_host::QLinearArgs& a, hipStream_t s) {
 
 // The row tiles' time grows with 32-token tiles times rows, the LDS tiles'
 // with rounds of workgroups over the CUs, one a CU; both with K.  One round
-// takes as long as the row tiles need for about 170 rows per CU (measured us,
-// row / LDS tiles, K = 5632, N = 2048: 128 tokens 17 / 61, 512 tokens 47 / 62;
-// N = K = 8192: 64 tokens 37 / 86, 128 tokens 72 / 87, 256 tokens 142 / 88).
+// takes as long as the row tiles need for about 200 rows per CU (measured us,
+// row / LDS tiles, K = 5632, N = 2048: 128 tokens 15 / 61, 512 39 / 62, 768
+// 58 / 63; N = K = 8192: 64 tokens 30 / 86, 128 56 / 87, 192 83 / 88, 256
+// 110 / 89; K = 2048: 1024 tokens, N = 2048 36 / 26).
 bool use_rows(const moe_host::QLinearArgs& a) {
   using moe_host::ceil_div_host;
   const int cus = moe_host::device_cu_count();
   const long long wgs =
       (long long)ceil_div_host(a.N, 32 * tile_waves(a)) * ceil_div_host(a.M, kTileM);
   const long long rounds = (wgs + cus - 1) / cus;
-  return (long long)ceil_div_host(a.M, 32) * a.N < rounds * 170 * cus;
+  return (long long)ceil_div_host(a.M, 32) * a.N < rounds * 200 * cus;
 }
 
 template <int G>

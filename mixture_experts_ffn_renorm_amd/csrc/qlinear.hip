@@ -255,17 +255,17 @@ hipError_t launch_gemv(const moe_host::QLinearArgs& a, hipStream_t s) {
 //
 // A group's sum of x is formed once per slice (a product with ones) and kept.
 // The codes' loads are ordinary ones: token tiles of one N share them in the
-// caches (512 tokens, N = 2048, K = 5632 39 us, non-temporal 43), and one
-// token tile gains as well (N = K = 8192 13.8 / 15.1).
+// caches (64 tokens, N = K = 8192 30 us, non-temporal 35), and one token tile
+// gains as well (16 tokens 13.8 / 15.1).
 //
 // Up to 16 tokens bound by the latency of its loads: a workgroup reads all of
 // its tokens' x before the first product.  16 tokens, N = 11264 gated, K =
 // 2048, groups of 32: 8.8 us (1.7 TB/s); N = K = 8192: 13.8 us (2.7 TB/s).
 // Above, by vector instructions (two thirds of the time): 512 tokens, N =
-// 2048, K = 5632 39 us (300 TFLOP/s).  Two to four tiles' codes in flight in
+// 2048, K = 5632 34 us (347 TFLOP/s).  Two to four tiles' codes in flight in
 // place of one changed nothing.
 constexpr int kRowsWaves = 8;
-constexpr int kRowsSums = 64 * 1024;   // bytes of tile sums at most
+constexpr int kRowsLds = 160 * 1024;   // a workgroup's LDS at most
 
 template <int G, int TM, int NB>
 __global__ __launch_bounds__(64 * kRowsWaves) void qlinear_rows_kernel(moe_host::QLinearArgs a,
@@ -457,15 +457,16 @@ hipError_t launch_rows_nb(const moe_host::QLinearArgs& a, hipStream_t s) {
   const int mtile = ceil_div_host(a.M, 16 * TM);
   const long long want = 8LL * moe_host::device_cu_count() / nw;
   int tiles = (int)(((long long)total * mtile + want - 1) / want);
-  const int most = kRowsSums / (nw * TM * 1024) / per * per;
+  const int most = (kRowsLds - nw * NB * 4096) / (nw * TM * 1024) / per * per;
   tiles = (tiles + per - 1) / per * per;
-  // one round of workgroups rather than a second, nearly empty one
-  while ((long long)ceil_div_host(total, tiles) * mtile > want && tiles < most) tiles += per;
-  if (tiles > most) tiles = most;
-  constexpr int kMost = kRowsWaves * NB * 4096 + kRowsSums;
+  // as few full rounds of workgroups as LDS allows, and none nearly empty (64
+  // tokens, N = 11264 gated, K = 2048: 13 us in one round, 19 in one and a half)
+  const int turns = ceil_div_host(tiles, most);
+  tiles = ceil_div_host(ceil_div_host(tiles, turns), per) * per;
+  while ((long long)ceil_div_host(total, tiles) * mtile > want * turns && tiles < most) tiles += per;
   static bool set[moe_host::kMaxDevices] = {};
   const hipError_t e = moe_host::ensure_dynamic_lds(
-      reinterpret_cast<const void*>(&qlinear_rows_kernel<G, TM, NB>), kMost, set);
+      reinterpret_cast<const void*>(&qlinear_rows_kernel<G, TM, NB>), kRowsLds, set);
   if (e != hipSuccess) return e;
   const size_t lds = (size_t)nw * (NB * 4096 + tiles * TM * 1024);
   const int wgs = ceil_div_host(total, tiles);
@@ -863,9 +864,9 @@ hipError_t launch_few(const moe_host::QLinearArgs& a, hipStream_t s) {
 // The row tiles' time grows with 32-token tiles times rows, the LDS tiles'
 // with rounds of workgroups over the CUs, one a CU; both with K.  One round
 // takes as long as the row tiles need for about 200 rows per CU (measured us,
-// row / LDS tiles, K = 5632, N = 2048: 128 tokens 15 / 61, 512 39 / 62, 768
-// 58 / 63; N = K = 8192: 64 tokens 30 / 86, 128 56 / 87, 192 83 / 88, 256
-// 110 / 89; K = 2048: 1024 tokens, N = 2048 36 / 26).
+// row / LDS tiles, K = 5632, N = 2048: 128 tokens 15 / 61, 512 34 / 62, 768
+// 59 / 63; N = K = 8192: 64 tokens 30 / 86, 128 48 / 87, 192 84 / 88, 256
+// 92 / 89; K = 2048: 1024 tokens, N = 2048 30 / 26).
 bool use_rows(const moe_host::QLinearArgs& a) {
   using moe_host::ceil_div_host;
   const int cus = moe_host::device_cu_count();

@@ -518,8 +518,10 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
       }
       const float bound = -lanes_max<L>(gt < k ? -lmax : -INFINITY);
       const float tol = by_logit ? 0.f : 2.f * eps + 0x1p-22f * fabsf(bound);
-      // fewer than top_k lanes hold anything: every finite expert
-      const float cut = !open ? INFINITY : bound > -INFINITY ? bound - tol : -3.4028235e38f;
+      // Never -inf, which experts that are not there have for their c: fewer
+      // than top_k lanes hold anything, or a bias of the type's lowest value
+      // is the bound, whose difference overflows.
+      const float cut = open ? fmaxf(bound - tol, -3.4028235e38f) : INFINITY;
       // this lane's candidates, expert i at bit C - 1 - i
       uint32_t mask = 0u;
 #pragma unroll

@@ -489,10 +489,18 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, 
         }
         open = open && rank < a.topk_group;
         if (scored && a.topk_group < G) {
-          // the worst group that stays and the best that does not
-          const float lo = -lanes_max<L>(open ? -score : -INFINITY);
-          const float hi = lanes_max<L>(!open && grp < G ? score : -INFINITY);
-          unsure = !(lo - hi > 2.f * eps + 0x1p-21f * fmaxf(fabsf(lo), fabsf(hi)));
+          // The worst group that stays and the best that does not, each moved
+          // by the error that its c have from their own magnitudes (a sum of a
+          // large positive and a large negative c keeps the error of both).
+          // -inf: masked by the bias, behind every finite sum; a sum past the
+          // type's range counts as its end.
+          const float last = a.group_top == 2 ? m2 : m1;
+          const float by = 0x1p-22f * fabsf(m1) + (a.group_top == 2 ? 0x1p-22f * fabsf(m2) : 0.f);
+          const bool some = last > -INFINITY;
+          const float sum = fminf(fmaxf(score, -3.4028235e38f), 3.4028235e38f);
+          const float lo = -lanes_max<L>(!open ? -INFINITY : some ? by - sum : INFINITY);
+          const float hi = lanes_max<L>(!open && grp < G && some ? sum + by : -INFINITY);
+          unsure = !(lo - hi > 2.f * eps);
         } else {
           // a group of -inf (or NaN) alone among those that stay
           unsure = lanes_max<L>(open && !(score > -INFINITY) ? 1.f : 0.f) > 0.f;

@@ -1,4 +1,5 @@
-"""Scored routing where a plain fp32 evaluation goes wrong: masks of the type's lowest value."""
+"""Scored routing where a plain fp32 evaluation goes wrong: masks of the type's lowest value, group sums of
+large biases that cancel."""
 
 from __future__ import annotations
 
@@ -46,3 +47,40 @@ def test_masking_biases_where_lanes_have_spare_experts(E, G, M, score, low):
     k = min(E, 6)
     ids, _ = ts.check(l, k, score, True, bias, G, min(G, 2), 1)
     assert np.all((ids >= 0) & (ids < E))
+
+
+# ---------------------------------------------------------------------------
+# group sums of large biases that cancel
+# ---------------------------------------------------------------------------
+
+def cancelling(score, B, G, M, seed):
+    """M rows of G groups of two whose biases are +B and -B: a group's sum is
+    s0 + s1, all of them within 2e-5 of each other, and each group's c was
+    rounded at the magnitude B.  Rows whose two sums at the border of the kept
+    groups lie closer than 2e-7 are left out: below B = 1e4 double precision
+    tells the others apart (its c rounds by 2^-53 B = 1.1e-12)."""
+    rng = np.random.default_rng(seed)
+    n = 3 * M
+    if score == "sigmoid":
+        total = 1.0
+    else:
+        total = 1.0 / G
+    s0 = total * rng.uniform(0.2, 0.8, size=(n, G))
+    s1 = total + rng.uniform(-1e-5, 1e-5, size=(n, G)) - s0
+    s = np.stack([s0, s1], axis=2).reshape(n, 2 * G)
+    l = np.log(s / (1.0 - s)) if score == "sigmoid" else np.log(s)
+    l = l.astype(np.float32)
+    sums = np.sort(np.exp(mo.log_scores(l, score)).reshape(n, G, 2).sum(2), axis=1)
+    kept = max(1, G // 3)
+    l = l[sums[:, G - kept] - sums[:, G - kept - 1] > 2e-7][:M]
+    assert l.shape[0] == M
+    return l, np.tile(np.float32([B, -B]), G), kept
+
+
+@pytest.mark.parametrize("M", [700, 4096])
+@pytest.mark.parametrize("G", [2, 8, 16])
+@pytest.mark.parametrize("B", [16.0, 100.0, 1e4])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_group_sums_of_cancelling_biases(score, B, G, M):
+    l, bias, kept = cancelling(score, B, G, M, int(B) + G)
+    ts.check(l, kept, score, True, bias, G, kept, 2)

@@ -429,7 +429,9 @@ int moe_forward_mxfp8(const uint16_t* x, const uint16_t* w_router, const float* 
  *     lowest ids that are left follow.  Renormalized weights stay exact
  *     where every chosen score underflows; a row whose chosen logits are all
  *     -inf gets weights 0.  A NaN choice score ranks below all others;
- *     weights follow the formula, NaN included.
+ *     weights follow the formula, NaN included (renormalized softmax weights
+ *     are formed from the chosen logits alone, so a NaN logit that is not
+ *     chosen does not reach them).
  *   - select_bias may hold -inf (such an expert comes after all others), not
  *     +inf.
  */

@@ -165,9 +165,9 @@ __device__ __forceinline__ int lanes_scan(int v) {
 // A chosen expert's score up to a factor common to the row, so that
 // renormalized weights stay right where every score underflows: softmax
 // e^(l - m), sigmoid e^(l - min(m, 0)) / (1 + e^l) (or its mirror for l >= 0),
-// with m the largest chosen logit.  Zero where every chosen logit is -inf.
+// with m the largest chosen logit.  Without such a one: 0, NaN for NaN.
 __device__ __forceinline__ float shifted_score(float l, float m, bool sigmoid) {
-  if (m == -INFINITY) return 0.f;
+  if (m == -INFINITY) return l != l ? l : 0.f;
   if (!sigmoid) return expf(l - m);
   return l >= 0.f ? 1.f / (1.f + expf(-l)) : expf(l - fminf(m, 0.f)) / (1.f + expf(l));
 }
@@ -708,8 +708,10 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_backward_kernel(
     float g;
     if (a.renormalize) {
       const float m = lanes_max<L>(l);
-      const float sh = used && m > -INFINITY
-                           ? fast_score(l, sigmoid ? fminf(m, 0.f) : m, sigmoid) : 0.f;
+      // no logit above -inf: 0, NaN for NaN
+      const float none = l != l ? l : 0.f;
+      const float sh = !used ? 0.f : m > -INFINITY
+                           ? fast_score(l, sigmoid ? fminf(m, 0.f) : m, sigmoid) : none;
       const float total = lanes_sum<L>(sh);
       const float hat = total == 0.f ? 0.f : sh * __builtin_amdgcn_rcpf(total);
       g = hat * (d - lanes_sum<L>(hat * d));

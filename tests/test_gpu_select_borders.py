@@ -1,5 +1,5 @@
 """Scored routing where a plain fp32 evaluation goes wrong: masks of the type's lowest value, group sums of
-large biases that cancel."""
+large biases that cancel, NaN among the chosen experts."""
 
 from __future__ import annotations
 
@@ -84,3 +84,72 @@ def cancelling(score, B, G, M, seed):
 def test_group_sums_of_cancelling_biases(score, B, G, M):
     l, bias, kept = cancelling(score, B, G, M, int(B) + G)
     ts.check(l, kept, score, True, bias, G, kept, 2)
+
+
+# ---------------------------------------------------------------------------
+# NaN among the chosen
+# ---------------------------------------------------------------------------
+
+def by_formula(l, ids, score, renorm):
+    """Weights as the formula has them in float64.  Renormalized softmax
+    weights are formed from the chosen logits alone."""
+    l = l.astype(np.float64)
+    lk = np.take_along_axis(l, ids.astype(np.int64), axis=1)
+    with np.errstate(invalid="ignore"):
+        if renorm and score == "softmax":
+            m = np.where(np.isnan(lk), -np.inf, lk).max(axis=1, keepdims=True)
+            s = np.exp(lk - np.where(np.isneginf(m), 0.0, m))
+        elif score == "softmax":
+            s = np.exp(lk) / np.exp(l).sum(axis=1, keepdims=True)
+        else:
+            s = 1.0 / (1.0 + np.exp(-lk))
+        w = s / s.sum(axis=1, keepdims=True) if renorm else s
+    # a chosen row of -inf alone: 0
+    return np.where(np.isneginf(lk).all(axis=1, keepdims=True), 0.0, w)
+
+
+@pytest.mark.parametrize("G", [1, 4])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_chosen_nan_reaches_the_weights(score, renorm, biased, G):
+    """Rows with too few numbers to choose from: NaN logits are chosen last,
+    and their weights, and the gradient through them, are NaN, never 0."""
+    moe = ts._moe()
+    E, k, nan = 64, 5, np.float32(np.nan)
+    l = ts.draw(8, E, 31)
+    l[1] = nan
+    l[2, 3:] = nan
+    l[3] = nan
+    l[3, 7] = l[3, 40] = -INF
+    l[4] = nan
+    l[4, 9], l[4, 41] = 0.5, -INF
+    l[6] = -INF
+    r = moe.Routing(k, score=score, renormalize=renorm, n_group=G, topk_group=min(G, 2), scale=2.5,
+                    select_bias=h.dev_f32(ts.steps(E, 32)) if biased else None)
+    ids, w = ts.run_select(l, r)
+    assert all(len(set(row)) == k for row in ids.tolist())
+    assert np.all((ids >= 0) & (ids < E))
+    want = 2.5 * by_formula(l, ids, score, renorm)
+    lk = np.take_along_axis(l, ids.astype(np.int64), axis=1)
+    assert np.isnan(lk[[1, 2, 3, 4]]).any(axis=1).all()
+    assert np.array_equal(np.isnan(w), np.isnan(want))
+    ok = ~np.isnan(want)
+    assert np.all(np.abs(w - want)[ok] <= ts.rel_tol(l, k) * np.abs(want[ok]) + 2.0 ** -126 * 2.5)
+    g = ts.draw(8, k, 33)
+    got = ts.run_backward(l, ids, g, r)
+    at = np.take_along_axis(got, ids.astype(np.int64), axis=1)
+    if renorm or score == "softmax":
+        # every chosen expert's weight holds the NaN
+        assert np.isnan(at[[1, 2, 3, 4]]).all()
+    else:
+        assert np.array_equal(np.isnan(at), np.isnan(lk))
+    if renorm or score == "sigmoid":
+        rest = got.copy()
+        np.put_along_axis(rest, ids.astype(np.int64), 0.0, axis=1)
+        assert np.all(rest == 0.0)
+    fine = [0, 5, 7]
+    ref = mo.select_backward(l[fine], ids[fine], g[fine], score, renorm, 2.5)
+    tol = (3 * ts.rel_tol(l, k) + 2 * k * 2.0 ** -23) * 2.5 * np.abs(g[fine]).sum(1, keepdims=True)
+    assert np.all(np.abs(got[fine] - ref) <= tol + 2.0 ** -126)
+    assert np.all(got[6] == 0.0)

@@ -713,7 +713,8 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_backward_kernel(
       const float sh = !used ? 0.f : m > -INFINITY
                            ? fast_score(l, sigmoid ? fminf(m, 0.f) : m, sigmoid) : none;
       const float total = lanes_sum<L>(sh);
-      const float hat = total == 0.f ? 0.f : sh * __builtin_amdgcn_rcpf(total);
+      // a true quotient: one weight alone is 1 and its gradient exactly 0
+      const float hat = total == 0.f ? 0.f : sh / total;
       g = hat * (d - lanes_sum<L>(hat * d));
     } else if (sigmoid) {
       g = hw_sigmoid(l) * d;

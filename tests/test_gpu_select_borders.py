@@ -1,5 +1,6 @@
-"""Scored routing where a plain fp32 evaluation goes wrong: masks of the type's lowest value, group sums of
-large biases that cancel, NaN among the chosen experts."""
+"""Scored routing where a plain fp32 evaluation goes wrong: masks of the
+type's lowest value, group sums of large biases that cancel, NaN among the
+chosen experts, a single renormalized weight."""
 
 from __future__ import annotations
 
@@ -153,3 +154,14 @@ def test_chosen_nan_reaches_the_weights(score, renorm, biased, G):
     tol = (3 * ts.rel_tol(l, k) + 2 * k * 2.0 ** -23) * 2.5 * np.abs(g[fine]).sum(1, keepdims=True)
     assert np.all(np.abs(got[fine] - ref) <= tol + 2.0 ** -126)
     assert np.all(got[6] == 0.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [1, 60, 512])
+def test_gradient_of_one_renormalized_weight_is_zero(E, score):
+    """w = scale * s / s is constant: its gradient is 0, not a rounding."""
+    moe = ts._moe()
+    l = ts.draw(600, E, 41, 3.0)
+    ids = mo.select_ids(l, 1, score)
+    got = ts.run_backward(l, ids, ts.draw(600, 1, 42), moe.Routing(1, score=score, scale=2.5))
+    assert np.all(got == 0.0)

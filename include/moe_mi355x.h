@@ -454,6 +454,7 @@ typedef struct moe_routing {
  *   logits       [M, E] fp32, 16-byte aligned
  *   topk_ids     [M, top_k] int32 out
  *   topk_weights [M, top_k] fp32 out
+ * The outputs overlap neither each other nor logits nor select_bias.
  */
 int moe_select(const float* logits, const moe_routing* routing, int M, int E, int32_t* topk_ids,
                float* topk_weights, void* stream);
@@ -468,7 +469,7 @@ int moe_select(const float* logits, const moe_routing* routing, int M, int E, in
  *                gets the sum of its slots' gradients
  *   grad_weights [M, top_k] fp32: dL/dw
  *   grad_logits  [M, E] fp32 out: dL/dl, every entry written; 16-byte
- *                aligned, and not logits itself
+ *                aligned, overlapping none of the inputs
  */
 int moe_select_backward(const float* logits, const int32_t* topk_ids, const float* grad_weights,
                         const moe_routing* routing, int M, int E, float* grad_logits,
@@ -537,7 +538,8 @@ typedef struct moe_quantized_matrix {
  *             weights that moe_route_scored gives for E = top_k = 1
  *   addend    [M, n_out] bf16 or NULL (0): e.g. the routed experts' output;
  *             may be out itself (added to in place)
- *   out       [M, n_out] bf16 out, not x
+ *   out       [M, n_out] bf16 out, overlapping no input but an addend that is
+ *             out itself
  * One launch.  M, N, K < 2^24; M*N < 2^40.  A row of x that is not finite
  * gives NaN in its own row of out; so may one with |x| of 2^112 or more (a
  * group's sums of (128 + code) x are held in fp32).

@@ -78,6 +78,13 @@ bool gemm_block_ok(int B) {
 // The kernels copy 16-byte pieces of every tensor.
 bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether an output shares memory with another operand (null: it does not).
+bool overlap(const void* out, size_t out_bytes, const void* p, size_t bytes) {
+  if (out == nullptr || p == nullptr) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(out), b = reinterpret_cast<uintptr_t>(p);
+  return a < b + bytes && b < a + out_bytes;
+}
+
 // Small batches run the top-k and the index lists in one launch.
 bool fused_route(int M, int top_k) { return align_segments(M * top_k) == 1; }
 
@@ -618,6 +625,11 @@ int moe_select(const float* logits, const moe_routing* routing, int M, int E, in
   if (M == 0) return MOE_OK;
   if (!logits || !topk_ids || !topk_weights) return MOE_ERR_INVALID_ARG;
   if (!a16(logits)) return MOE_ERR_INVALID_ARG;
+  const size_t row = (size_t)M * E * 4, pairs = (size_t)M * routing->top_k * 4;
+  if (overlap(topk_ids, pairs, topk_weights, pairs)) return MOE_ERR_INVALID_ARG;
+  for (const void* out : {static_cast<const void*>(topk_ids), static_cast<const void*>(topk_weights)})
+    if (overlap(out, pairs, logits, row) || overlap(out, pairs, routing->select_bias, (size_t)E * 4))
+      return MOE_ERR_INVALID_ARG;
   MOE_TRY_HIP(launch_select(select_args(*routing, logits, M, E, topk_ids, topk_weights),
                             static_cast<hipStream_t>(stream)));
   return MOE_OK;
@@ -633,8 +645,11 @@ int moe_select_backward(const float* logits, const int32_t* topk_ids, const floa
   if (st != MOE_OK) return st;
   if (M == 0) return MOE_OK;
   if (!logits || !topk_ids || !grad_weights || !grad_logits) return MOE_ERR_INVALID_ARG;
-  if (grad_logits == logits) return MOE_ERR_INVALID_ARG;
   if (!a16(logits) || !a16(grad_logits)) return MOE_ERR_INVALID_ARG;
+  const size_t row = (size_t)M * E * 4, pairs = (size_t)M * routing->top_k * 4;
+  if (overlap(grad_logits, row, logits, row) || overlap(grad_logits, row, topk_ids, pairs) ||
+      overlap(grad_logits, row, grad_weights, pairs))
+    return MOE_ERR_INVALID_ARG;
   SelectArgs a = select_args(*routing, logits, M, E, const_cast<int32_t*>(topk_ids), nullptr);
   MOE_TRY_HIP(launch_select_backward(a, grad_weights, grad_logits,
                                      static_cast<hipStream_t>(stream)));
@@ -679,8 +694,16 @@ int moe_linear_quantized(const uint16_t* x, const moe_quantized_matrix* w, int M
   if (M >= kMaxPairs || N >= kMaxPairs || K >= kMaxPairs) return MOE_ERR_UNSUPPORTED;
   if ((long long)M * N >= 1LL << 40) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
-  if (!x || !w->q || !w->scales || !w->biases || !out || out == x) return MOE_ERR_INVALID_ARG;
+  if (!x || !w->q || !w->scales || !w->biases || !out) return MOE_ERR_INVALID_ARG;
   if (!a16(x) || !a16(w->q) || !a16(w->scales) || !a16(w->biases) || !a16(out) || !a16(addend))
+    return MOE_ERR_INVALID_ARG;
+  // addend may be out itself: each output is read where it is written
+  const size_t written = (size_t)M * (gated ? N / 2 : N) * 2, per_group = (size_t)N * (K / g) * 2;
+  if (overlap(out, written, x, (size_t)M * K * 2) ||
+      overlap(out, written, w->q, (size_t)N * (K / 2)) ||
+      overlap(out, written, w->scales, per_group) || overlap(out, written, w->biases, per_group) ||
+      overlap(out, written, row_scale, (size_t)M * 4) ||
+      (addend != out && overlap(out, written, addend, written)))
     return MOE_ERR_INVALID_ARG;
   QLinearArgs a{x, w->q, w->scales, w->biases, M, N, K, g, gated, row_scale, addend, out};
   MOE_TRY_HIP(launch_qlinear(a, static_cast<hipStream_t>(stream)));

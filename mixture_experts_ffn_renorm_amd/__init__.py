@@ -565,6 +565,10 @@ def moe_forward_mxfp8(x, w_router, mxw: dict, top_k: int, renormalize: bool = Tr
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
+# ctypes keeps the low 32 bits of a larger number without a word, so the calls
+# below refuse sizes from here on (a tensor of 2^32 + 5 rows fits the memory)
+_INT_END = 1 << 31
+
 
 class Routing:
     """A routing rule (moe_routing in the header): how a token's experts are
@@ -587,12 +591,16 @@ class Routing:
             raise ValueError(f"score must be one of {tuple(_SCORES)}, got {score!r}")
         if select_bias is not None:
             _check(select_bias, "select_bias", (_torch().float32,))
+        numbers = [int(v) for v in (top_k, n_group, n_group if topk_group is None else topk_group,
+                                    group_top)]
+        for name, v in zip(("top_k", "n_group", "topk_group", "group_top"), numbers):
+            if not -_INT_END <= v < _INT_END:   # the struct would keep its low bits
+                raise ValueError(f"{name} {v} is not a C int")
         set_ = object.__setattr__
         set_(self, "select_bias", select_bias)
-        set_(self, "top_k", int(top_k))
+        set_(self, "top_k", numbers[0])
         set_(self, "_c", RoutingRule(
-            _SCORES[score], int(top_k), int(bool(renormalize)), int(n_group),
-            int(n_group if topk_group is None else topk_group), int(group_top), float(scale),
+            _SCORES[score], numbers[0], int(bool(renormalize)), *numbers[1:], float(scale),
             None if select_bias is None else select_bias.data_ptr()))
         set_(self, "_address", ctypes.addressof(self._c))
 
@@ -688,10 +696,12 @@ def moe_select(logits, routing: Routing, topk_ids=None, topk_weights=None, strea
     """Expert ids [M, top_k] int32 and weights [M, top_k] fp32 of logits
     [M, E] fp32 under a routing rule."""
     torch = _torch()
+    M, E = logits.shape
+    if M >= _INT_END or E >= _INT_END:
+        raise MoeError("moe_select", -2)
     dev = logits.get_device()
     if not _current(dev):
         return _elsewhere(dev, moe_select, logits, routing, topk_ids, topk_weights, stream)
-    M, E = logits.shape
     out = (M, routing.top_k)
     _need(logits, "logits", torch.float32, (M, E), dev)
     if topk_ids is None:
@@ -714,11 +724,13 @@ def moe_select_backward(logits, topk_ids, grad_weights, routing: Routing, grad_l
     """Gradient [M, E] fp32 of moe_select's weights with respect to its
     logits, for the ids it gave and the weights' gradient [M, top_k] fp32."""
     torch = _torch()
+    M, E = logits.shape
+    if M >= _INT_END or E >= _INT_END:
+        raise MoeError("moe_select_backward", -2)
     dev = logits.get_device()
     if not _current(dev):
         return _elsewhere(dev, moe_select_backward, logits, topk_ids, grad_weights, routing,
                           grad_logits, stream)
-    M, E = logits.shape
     pairs = (M, routing.top_k)
     _need(logits, "logits", torch.float32, (M, E), dev)
     _need(topk_ids, "topk_ids", torch.int32, pairs, dev)
@@ -739,12 +751,14 @@ def moe_route_scored(x, w_router, routing: Routing, logit_bias=None, topk_ids=No
                      topk_weights=None, logits_out=None, ws=None, stream=None):
     """moe_route with a routing rule: (topk_ids, topk_weights)."""
     torch = _torch()
+    M, H = x.shape
+    E = w_router.shape[0]
+    if M >= _INT_END or H >= _INT_END or E >= _INT_END:
+        raise MoeError("moe_route_scored", -2)
     dev = x.get_device()
     if not _current(dev):
         return _elsewhere(dev, moe_route_scored, x, w_router, routing, logit_bias, topk_ids,
                           topk_weights, logits_out, ws, stream)
-    M, H = x.shape
-    E = w_router.shape[0]
     out = (M, routing.top_k)
     _need(x, "x", torch.bfloat16, (M, H), dev)
     _need(w_router, "w_router", torch.bfloat16, (E, H), dev)
@@ -778,13 +792,15 @@ def _layer_scored(call: str, x, w_router, routing: Routing, weights, weight_args
     """A layer call with a routing rule: ``weights`` are (name, tensor, dtype,
     shape) to check, ``weight_args`` what the C call takes for them."""
     torch = _torch()
+    M, H = x.shape
+    E = w_router.shape[0]
+    k = routing.top_k
+    if max(M, E, H, I) >= _INT_END:
+        raise MoeError(call, -2)
     dev = x.get_device()
     if not _current(dev):
         return _elsewhere(dev, _layer_scored, call, x, w_router, routing, weights, weight_args, I,
                           ws_size, logit_bias, out, topk_ids_out, topk_weights_out, ws, stream)
-    M, H = x.shape
-    E = w_router.shape[0]
-    k = routing.top_k
     _need(x, "x", torch.bfloat16, (M, H), dev)
     _need(w_router, "w_router", torch.bfloat16, (E, H), dev)
     for name, t, dtype, shape in weights:
@@ -887,15 +903,16 @@ def moe_linear_quantized(x, weight: dict, gated: bool = False, row_scale=None, a
     torch = _torch()
     M, K = x.shape
     bits, group = int(weight["bits"]), int(weight.get("group_size", 64))
-    if bits != 4 or group not in (32, 64, 128) or K % group != 0:
+    q, scales, biases = weight["q"], weight["scales"], weight["biases"]
+    N = q.shape[0]
+    if bits != 4 or group not in (32, 64, 128) or K % group != 0 or M >= _INT_END or \
+            N >= _INT_END or K >= _INT_END:
         raise MoeError("moe_linear_quantized", -2)
     dev = x.get_device()
     if not _current(dev):
         return _elsewhere(dev, moe_linear_quantized, x, weight, gated, row_scale, addend, out,
                           stream)
     bf16 = torch.bfloat16
-    q, scales, biases = weight["q"], weight["scales"], weight["biases"]
-    N = q.shape[0]
     shape = (M, N // 2 if gated else N)
     _need(x, "x", bf16, (M, K), dev)
     _need(q, "q", _word_type(q), (N, K // 8), dev)

@@ -541,8 +541,10 @@ typedef struct moe_quantized_matrix {
  *   out       [M, n_out] bf16 out, overlapping no input but an addend that is
  *             out itself
  * One launch.  M, N, K < 2^24; M*N < 2^40.  A row of x that is not finite
- * gives NaN in its own row of out; so may one with |x| of 2^112 or more (a
- * group's sums of (128 + code) x are held in fp32).
+ * gives results that are not finite (NaN or an infinity, which of them depends
+ * on the kernel that M chooses) in its own row of out and in no other; so may
+ * one with |x| of 2^112 or more (a group's sums of (128 + code) x are held in
+ * fp32).
  */
 int moe_linear_quantized(const uint16_t* x, const moe_quantized_matrix* w, int M, int N, int K,
                          int gated, const float* row_scale, const uint16_t* addend, uint16_t* out,

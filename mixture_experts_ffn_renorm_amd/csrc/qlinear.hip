@@ -10,6 +10,8 @@
 // acc = sum (128 + q) x and sx = sum x over one group in fp32, and
 //   s * sum q x + b * sum x = s * acc + (b - 128 s) * sx
 // is added to the output's fp32 sum, two FMAs per group and output.
+#include <algorithm>
+
 #include "moe_common.h"
 #include "qunit.h"
 
@@ -458,12 +460,16 @@ hipError_t launch_rows_nb(const moe_host::QLinearArgs& a, hipStream_t s) {
   const long long want = 8LL * moe_host::device_cu_count() / nw;
   int tiles = (int)(((long long)total * mtile + want - 1) / want);
   const int most = (kRowsLds - nw * NB * 4096) / (nw * TM * 1024) / per * per;
-  tiles = (tiles + per - 1) / per * per;
+  // no more than there are: 65536 tokens, N = 16, K = 512 17 us, 101 with
+  // tiles past the last row multiplied and dropped
+  tiles = std::min((tiles + per - 1) / per * per, total);
   // as few full rounds of workgroups as LDS allows, and none nearly empty (64
   // tokens, N = 11264 gated, K = 2048: 13 us in one round, 19 in one and a half)
   const int turns = ceil_div_host(tiles, most);
   tiles = ceil_div_host(ceil_div_host(tiles, turns), per) * per;
-  while ((long long)ceil_div_host(total, tiles) * mtile > want * turns && tiles < most) tiles += per;
+  while ((long long)ceil_div_host(total, tiles) * mtile > want * turns &&
+         tiles < std::min(most, total))
+    tiles += per;
   static bool set[moe_host::kMaxDevices] = {};
   const hipError_t e = moe_host::ensure_dynamic_lds(
       reinterpret_cast<const void*>(&qlinear_rows_kernel<G, TM, NB>), kRowsLds, set);

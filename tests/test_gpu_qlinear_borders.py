@@ -1,5 +1,5 @@
 """Dense 4-bit products at the borders of their contract: rows of x that are
-not finite."""
+not finite, few weight rows for many tokens."""
 
 from __future__ import annotations
 
@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 
 import moe_workloads as wl
+from oracle import moe_oracle as mo
 from tests import helpers as h
 from tests import test_gpu_qlinear as tl
 
@@ -37,3 +38,32 @@ def test_rows_that_are_not_finite(M, bad, gated):
     assert torch.isfinite(good).all()
     assert not torch.isfinite(got[M - 1]).any()
     assert torch.equal(got[:M - 1], good[:M - 1])
+
+
+def sampled(M, N, K, group, gated=False, seed=7):
+    """A product checked on a sample of its tokens, the rows behind it
+    untouched."""
+    import torch
+    moe = tl._moe()
+    q, s, b = tl.matrix(N, K, group, seed)
+    x = tl.rows(M, K, seed + 1)
+    n_out = N // 2 if gated else N
+    buf = torch.full((M * n_out + 16,), -7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[:M * n_out].view(M, n_out)
+    moe.moe_linear_quantized(h.dev_bf16(x), tl.to_device(q, s, b, group), gated=gated, out=out)
+    torch.cuda.synchronize()
+    assert (buf[M * n_out:] == -7.0).all()
+    r = np.unique(np.concatenate([[0, M - 1], np.random.default_rng(seed).integers(0, M, 60)]))
+    ref = mo.linear_quantized(x[r], q, s, b, group, gated)
+    e = tl.error_bound(x[r], q, s, b, group, gated, None, None)
+    got = h.host_bf16_to_f64(out[torch.from_numpy(r).cuda()])
+    assert np.all(np.abs(got - ref) <= e + (np.abs(ref) + e) * 2.0 ** -8)
+
+
+@pytest.mark.parametrize("M,N,K,group,gated", [
+    (16384, 16, 512, 64, False), (16385, 64, 512, 32, False), (32768, 64, 512, 128, False),
+    (16384, 32, 256, 64, True), (20000, 2, 512, 64, True), (65536, 16, 64, 64, False),
+    (16400, 1, 2048, 128, False)])
+def test_few_weight_rows_for_many_tokens(M, N, K, group, gated):
+    """Fewer tiles of weight rows than a workgroup would walk."""
+    sampled(M, N, K, group, gated)

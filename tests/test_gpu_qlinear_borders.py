@@ -1,5 +1,5 @@
 """Dense 4-bit products at the borders of their contract: rows of x that are
-not finite, few weight rows for many tokens."""
+not finite, few weight rows for many tokens, more slices of K than waves."""
 
 from __future__ import annotations
 
@@ -67,3 +67,10 @@ def sampled(M, N, K, group, gated=False, seed=7):
 def test_few_weight_rows_for_many_tokens(M, N, K, group, gated):
     """Fewer tiles of weight rows than a workgroup would walk."""
     sampled(M, N, K, group, gated)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("K,group", [(16384 + 32, 32), (18432, 128), (32768 + 64, 64), (40960, 128)])
+@pytest.mark.parametrize("M", [1, 2, 16, 33])
+def test_more_slices_of_k_than_waves(M, K, group, gated):
+    tl.check(M, 24, K, group, K, gated, True, True)

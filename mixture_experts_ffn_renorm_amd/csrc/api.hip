@@ -409,10 +409,10 @@ int moe_grouped_gemm_w2_combine(const uint16_t* act, const uint16_t* w2,
 
 namespace {
 
-int forward_rule(const uint16_t* x, const uint16_t* w_router, const float* logit_bias, const
-                 uint16_t* w13, const uint16_t* w2, int M, int E, const Rule& rule, int H, int I,
-                 uint16_t* out, int32_t* topk_ids_out, float* topk_weights_out, void* workspace,
-                 size_t ws_bytes, moe_dispatch_info* info, void* stream) {
+int forward_rule(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
+                 const uint16_t* w13, const uint16_t* w2, int M, int E, const Rule& rule, int H,
+                 int I, uint16_t* out, int32_t* topk_ids_out, float* topk_weights_out,
+                 void* workspace, size_t ws_bytes, moe_dispatch_info* info, void* stream) {
   const int top_k = rule.top_k;
   int st = check_sizes(M, E, top_k, H, I);
   if (st != MOE_OK) return st;
@@ -481,8 +481,8 @@ int forward_rule(const uint16_t* x, const uint16_t* w_router, const float* logit
 int forward_quantized_rule(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
                            const moe_quantized_weights* qw, int M, int E, const Rule& rule, int H,
                            int I, uint16_t* out, int32_t* topk_ids_out, float* topk_weights_out,
-                           void* workspace, size_t ws_bytes, moe_dispatch_info* info, void* stream)
-                           {
+                           void* workspace, size_t ws_bytes, moe_dispatch_info* info,
+                           void* stream) {
   const int top_k = rule.top_k;
   int st = check_sizes(M, E, top_k, H, I);
   if (st != MOE_OK) return st;
@@ -769,10 +769,10 @@ size_t moe_mx_workspace_size(int M_max, int E, int top_k, int H, int I) {
 
 namespace {
 
-int forward_mxfp8_rule(const uint16_t* x, const uint16_t* w_router, const float* logit_bias, const
-                       moe_mx_weights* w, int M, int E, const Rule& rule, int H, int I, uint16_t*
-                       out, int32_t* topk_ids_out, float* topk_weights_out, void* workspace, size_t
-                       ws_bytes, moe_dispatch_info* info, void* stream) {
+int forward_mxfp8_rule(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
+                       const moe_mx_weights* w, int M, int E, const Rule& rule, int H, int I,
+                       uint16_t* out, int32_t* topk_ids_out, float* topk_weights_out,
+                       void* workspace, size_t ws_bytes, moe_dispatch_info* info, void* stream) {
   const int top_k = rule.top_k;
   int st = check_sizes(M, E, top_k, H, I);
   if (st != MOE_OK) return st;
@@ -881,25 +881,24 @@ int forward_mxfp8_rule(const uint16_t* x, const uint16_t* w_router, const float*
 extern "C" {
 
 int moe_forward_mxfp8(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
-                          const moe_mx_weights* w, int M, int E, int top_k, int H, int I,
-                          int renormalize, uint16_t* out, int32_t* topk_ids_out,
-                          float* topk_weights_out, void* workspace, size_t ws_bytes,
-                          moe_dispatch_info* info, void* stream) {
-  return forward_mxfp8_rule(x, w_router, logit_bias, w, M, E,
-                                Rule{top_k, renormalize, nullptr}, H, I, out, topk_ids_out,
-                                topk_weights_out, workspace, ws_bytes, info, stream);
+                      const moe_mx_weights* w, int M, int E, int top_k, int H, int I,
+                      int renormalize, uint16_t* out, int32_t* topk_ids_out,
+                      float* topk_weights_out, void* workspace, size_t ws_bytes,
+                      moe_dispatch_info* info, void* stream) {
+  return forward_mxfp8_rule(x, w_router, logit_bias, w, M, E, Rule{top_k, renormalize, nullptr}, H,
+                            I, out, topk_ids_out, topk_weights_out, workspace, ws_bytes, info,
+                            stream);
 }
 
-int moe_forward_mxfp8_scored(const uint16_t* x, const uint16_t* w_router,
-                                 const float* logit_bias, const moe_routing* routing,
-                                 const moe_mx_weights* w, int M, int E, int H, int I,
-                                 uint16_t* out, int32_t* topk_ids_out, float* topk_weights_out,
-                                 void* workspace, size_t ws_bytes, moe_dispatch_info* info,
-                                 void* stream) {
+int moe_forward_mxfp8_scored(const uint16_t* x, const uint16_t* w_router, const float* logit_bias,
+                             const moe_routing* routing, const moe_mx_weights* w, int M, int E,
+                             int H, int I, uint16_t* out, int32_t* topk_ids_out,
+                             float* topk_weights_out, void* workspace, size_t ws_bytes,
+                             moe_dispatch_info* info, void* stream) {
   if (routing == nullptr) return MOE_ERR_INVALID_ARG;
-  return forward_mxfp8_rule(x, w_router, logit_bias, w, M, E,
-                                Rule{routing->top_k, 0, routing}, H, I, out, topk_ids_out,
-                                topk_weights_out, workspace, ws_bytes, info, stream);
+  return forward_mxfp8_rule(x, w_router, logit_bias, w, M, E, Rule{routing->top_k, 0, routing}, H,
+                            I, out, topk_ids_out, topk_weights_out, workspace, ws_bytes, info,
+                            stream);
 }
 
 }  // extern "C"

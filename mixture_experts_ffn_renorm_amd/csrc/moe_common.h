@@ -213,6 +213,11 @@ __device__ __forceinline__ float dpp_max_with(float v) {
   const int s = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xf, 0xf, false);
   return __builtin_fmaxf(v, __builtin_bit_cast(float, s));
 }
+template <int kCtrl>
+__device__ __forceinline__ float dpp_add_with(float v) {
+  const int s = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xf, 0xf, false);
+  return v + __builtin_bit_cast(float, s);
+}
 __device__ __forceinline__ float row16_max(float v) {
   v = dpp_max_with<0xb1>(v);    // quad_perm [1, 0, 3, 2]
   v = dpp_max_with<0x4e>(v);    // quad_perm [2, 3, 0, 1]

@@ -83,12 +83,6 @@ __device__ __forceinline__ u32x4 pair8(u32x4 X) {
   return __builtin_bit_cast(u32x4, __builtin_shufflevector(v, v, 0, 4, 1, 5, 2, 6, 3, 7));
 }
 
-template <int kCtrl>
-__device__ __forceinline__ float dpp_add_lanes(float v) {
-  const int s = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xf, 0xf, false);
-  return v + __builtin_bit_cast(float, s);
-}
-
 // The epilogue of one output value.
 __device__ __forceinline__ void store_out(const moe_host::QLinearArgs& a, float y, int m, int n,
                                           int n_out) {
@@ -645,10 +639,10 @@ __global__ __launch_bounds__(64 * W) void qlinear_tile_kernel(moe_host::QLinearA
       float s = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) s = dot2_bf16(xr[i][j], 0x3f803f80u, s);
-      s = dpp_add_lanes<0xb1>(s);                 // quad_perm [1, 0, 3, 2]
-      s = dpp_add_lanes<0x4e>(s);                 // quad_perm [2, 3, 0, 1]
-      if (G >= 64) s = dpp_add_lanes<0x141>(s);   // row_half_mirror
-      if (G == 128) s = dpp_add_lanes<0x140>(s);  // row_mirror
+      s = dpp_add_with<0xb1>(s);                 // quad_perm [1, 0, 3, 2]
+      s = dpp_add_with<0x4e>(s);                 // quad_perm [2, 3, 0, 1]
+      if (G >= 64) s = dpp_add_with<0x141>(s);   // row_half_mirror
+      if (G == 128) s = dpp_add_with<0x140>(s);  // row_mirror
       sum[i / kLanes] = i % kLanes == 0 || mine == i % kLanes ? s : sum[i / kLanes];
     }
 #pragma unroll

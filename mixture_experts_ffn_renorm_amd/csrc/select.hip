@@ -121,11 +121,6 @@ __device__ __forceinline__ float lanes_max(float v) {
   }
   return v;
 }
-template <int kCtrl>
-__device__ __forceinline__ float dpp_add_with(float v) {
-  const int s = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xf, 0xf, false);
-  return v + __builtin_bit_cast(float, s);
-}
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
   v = dpp_add_with<0xb1>(v);    // quad_perm [1, 0, 3, 2]

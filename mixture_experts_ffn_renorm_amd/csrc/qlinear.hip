@@ -236,7 +236,7 @@ hipError_t launch_gemv(const moe_host::QLinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// ---- row-tile kernel: up to 32 tokens ----
+// ---- row-tile kernel: 3 to 16 tokens, and more where use_rows says so ----
 //
 // A wave keeps the x of 16 TM tokens and NB blocks (its slice of K) in
 // registers as MFMA operands and walks over tiles of 16 weight rows, one
@@ -257,9 +257,10 @@ hipError_t launch_gemv(const moe_host::QLinearArgs& a, hipStream_t s) {
 // Up to 16 tokens bound by the latency of its loads: a workgroup reads all of
 // its tokens' x before the first product.  16 tokens, N = 11264 gated, K =
 // 2048, groups of 32: 8.8 us (1.7 TB/s); N = K = 8192: 13.8 us (2.7 TB/s).
-// Above, by vector instructions (two thirds of the time): 512 tokens, N =
-// 2048, K = 5632 34 us (347 TFLOP/s).  Two to four tiles' codes in flight in
-// place of one changed nothing.
+// Above, by vector instructions (55 % of the time, matrix ones 18 %): 512
+// tokens, N = 2048, K = 5632 32 us (370 TFLOP/s); 64 tokens, N = K = 8192
+// 29.4 us.  Each 32 tokens widen the codes again.  Two to four tiles' codes in
+// flight in place of one changed nothing.
 constexpr int kRowsWaves = 8;
 constexpr int kRowsLds = 160 * 1024;   // a workgroup's LDS at most
 
@@ -505,12 +506,13 @@ hipError_t launch_rows(const moe_host::QLinearArgs& a, hipStream_t s) {
 // [h m l -128h -128m -128l 0 0], so one more MFMA step per four groups adds it
 // to the fp32 sums, where FMAs would cost as much vector time as the scaling.
 //
-// 2048 tokens, N = 2048, K = 5632, groups of 128: 63.5 us (744 TFLOP/s; a
+// 2048 tokens, N = 2048, K = 5632, groups of 128: 63 us (750 TFLOP/s; a
 // large library product in bf16 reaches 1204), groups of 64 68 us, of 32 85.
-// Bound by the two waves that a SIMD holds: matrix instructions fill 31% of
-// its time, vector ones (widening, scaling, staging) overlap them in part.
-// Tiles of 64 x 64 per wave, one wave a SIMD, took 95 us; 32 tokens per wave
-// and four waves a SIMD 75; both blocks of a stage unrolled up to 2.4 times.
+// Bound by the two waves that a SIMD holds: matrix instructions fill 36 % of
+// its time, vector ones (widening, scaling, staging) 51 %, and overlap them in
+// part.  Tiles of 64 x 64 per wave, one wave a SIMD, took 95 us; 32 tokens per
+// wave and four waves a SIMD 75; both blocks of a stage unrolled up to 2.4
+// times.
 constexpr int kTileM = 64;
 constexpr int kTileK = 256;
 constexpr int kTileX = kTileM * kTileK * 2;      // bytes of x per stage

@@ -197,8 +197,9 @@ struct SelectParams {
 
 // The choice for one token by a whole wave, every comparison in double
 // precision: for the rows that the fp32 pass below cannot decide.  `c` holds
-// E doubles of this wave.  Kept small (no unrolled element loops): it runs
-// seldom.
+// E doubles of this wave.  Kept small (no unrolled element loops), so that it
+// takes no registers from that pass; how often it runs depends on the rule and
+// the logits (below).
 __device__ __forceinline__ void select_exactly(const SelectParams& a, int t, double* c) {
   int lane = threadIdx.x & 63, E = a.E, G = a.n_group;
   const int k = a.top_k;
@@ -345,17 +346,29 @@ __device__ __forceinline__ void select_exactly(const SelectParams& a, int t, dou
 //    closer than the error of c; a sigmoid's closer than double precision's;
 //    -inf or NaN among the chosen; more than kCands candidates (rows of ties).
 //
+//    One such row takes its wave 3 to 4 us, several are done in turn.  A
+//    biased sigmoid without groups has next to none (65536 x 512, two batches
+//    of logits in turn, std 0.9, 4 and 6: 42, 43, 44 us).  A biased softmax
+//    has many where one probability stands far above those at the border (the
+//    same: 48, 179, 292 us; 8192 x 256, by the biases drawn: 12, 13 to 26, 12
+//    to 28), a sum of two a few where the border of the groups lies close (8192
+//    x 256 in 8 groups: none 9 us, a few 13 to 17; softmax with a bias, std 6:
+//    20 to 39).  Rows whose choice reaches masked experts (a bias or logits of
+//    -inf) are all done over, and where top_k is more than the lanes that are
+//    open, with more than kCands experts in them.
+//
 // Error of c: sigmoid 2^-22 (its slope times the exponent's rounding, two
 // hardware transcendentals, two roundings), softmax 2^-19 of the largest
 // probability (the common sum of C / 4 + 6 terms in a row, each rounding
 // once), and 2^-24 |c| for the bias.
 //
-// Bound by vector instructions, two transcendentals per expert among them,
+// Bound by vector instructions (72 to 75 % of the time), two transcendentals
+// per expert among them, the rest loads that few waves per SIMD do not hide,
 // and, for few tokens, by the chain of steps: 65536 x 512, sigmoid with a
-// bias, top_k 10, in 47.5 us (2.9 TB/s of logits; 37 us for a softmax without
-// one), 8192 x 256 in 8 groups in 9.3, one token in 5.6 (3 of them the
-// launch).  A wave per token with every comparison in double precision, the
-// simplest form, took 192 and 37 us for the first two.
+// bias, top_k 10, in 47 us (2.9 TB/s of logits; 33 us without one), 8192 x 256
+// in 8 groups in 9.1 (3 the launch; 6.6 by the logits alone, 7.7 with scores
+// and bias), one token in 5.5.  A wave per token with every comparison in
+// double precision, the simplest form, took 192 and 37 us for the first two.
 template <int L, int C, int V>
 __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelectParams a, int lpg) {
   constexpr int T = 64 / L;                    // tokens per wave

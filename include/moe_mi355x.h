@@ -543,8 +543,9 @@ typedef struct moe_quantized_matrix {
  * One launch.  M, N, K < 2^24; M*N < 2^40.  A row of x that is not finite
  * gives results that are not finite (NaN or an infinity, which of them depends
  * on the kernel that M chooses) in its own row of out and in no other; so may
- * one with |x| of 2^112 or more (a group's sums of (128 + code) x are held in
- * fp32).
+ * one whose |x| (271 |scale| + |bias|), summed over K, passes fp32's range
+ * (sums of (128 + code) x are held in fp32, and 128 x is taken off again), or
+ * with |x| of 2^112 or more.
  */
 int moe_linear_quantized(const uint16_t* x, const moe_quantized_matrix* w, int M, int N, int K,
                          int gated, const float* row_scale, const uint16_t* addend, uint16_t* out,

@@ -694,7 +694,8 @@ def _empty(shape, dtype, device: int, stream):
 
 def moe_select(logits, routing: Routing, topk_ids=None, topk_weights=None, stream=None):
     """Expert ids [M, top_k] int32 and weights [M, top_k] fp32 of logits
-    [M, E] fp32 under a routing rule."""
+    [M, E] fp32 under a routing rule.  The outputs overlap neither each other
+    nor an operand."""
     torch = _torch()
     M, E = logits.shape
     if M >= _INT_END or E >= _INT_END:
@@ -722,7 +723,8 @@ def moe_select(logits, routing: Routing, topk_ids=None, topk_weights=None, strea
 def moe_select_backward(logits, topk_ids, grad_weights, routing: Routing, grad_logits=None,
                         stream=None):
     """Gradient [M, E] fp32 of moe_select's weights with respect to its
-    logits, for the ids it gave and the weights' gradient [M, top_k] fp32."""
+    logits, for the ids it gave and the weights' gradient [M, top_k] fp32.
+    ``grad_logits`` overlaps no operand."""
     torch = _torch()
     M, E = logits.shape
     if M >= _INT_END or E >= _INT_END:
@@ -899,7 +901,9 @@ def moe_linear_quantized(x, weight: dict, gated: bool = False, row_scale=None, a
     [N, K/group_size] (bf16).  ``gated``: the first N/2 rows are gates and
     f = SiLU(gate) * up, n_out = N/2; else f is the identity, n_out = N.
     ``row_scale`` [M] fp32 and ``addend`` [M, n_out] bf16 (``out`` itself, to
-    add in place) are optional.  |x| is below 2^112 (a group's sums in fp32)."""
+    add in place) are optional; ``out`` overlaps no other operand.  |x| is
+    below 2^112, and |x| (271 |scale| + |bias|) summed over K within fp32's
+    range."""
     torch = _torch()
     M, K = x.shape
     bits, group = int(weight["bits"]), int(weight.get("group_size", 64))

@@ -423,7 +423,8 @@ int moe_forward_mxfp8(const uint16_t* x, const uint16_t* w_router, const float* 
  *   - Exact ties go to the lower expert id, and to the lower group.  Choice
  *     scores and group sums are compared as double precision gives them (no
  *     fp32 rounding decides a choice).  Without select_bias experts are
- *     ordered by their logits, which order the scores.
+ *     ordered by their logits, which order the scores, and so are groups by
+ *     their best expert (group_top 1), also where scores round to one value.
  *   - Logits may be -inf (a masked expert: score 0).  Ids are always top_k
  *     different ones in [0, E): where fewer experts can be told apart, the
  *     lowest ids that are left follow.  Renormalized weights stay exact

@@ -1,6 +1,6 @@
 """Scored routing where a plain fp32 evaluation goes wrong: masks of the
 type's lowest value, group sums of large biases that cancel, NaN among the
-chosen experts, a single renormalized weight."""
+chosen experts, a single renormalized weight, saturated scores."""
 
 from __future__ import annotations
 
@@ -165,3 +165,16 @@ def test_gradient_of_one_renormalized_weight_is_zero(E, score):
     ids = mo.select_ids(l, 1, score)
     got = ts.run_backward(l, ids, ts.draw(600, 1, 42), moe.Routing(1, score=score, scale=2.5))
     assert np.all(got == 0.0)
+
+
+@pytest.mark.parametrize("G,kept", [(1, 1), (8, 3)])
+@pytest.mark.parametrize("shift", [300.0, -1000.0])
+def test_saturated_scores_are_ordered_by_their_logits(shift, G, kept):
+    """Sigmoid scores that all round to 1, or to 0: without a bias experts and
+    groups go by the logits, as a softmax's scores of the same logits do."""
+    moe = ts._moe()
+    l = ts.draw(70, 128, 51, 3.0) + np.float32(shift)
+    ids, w = ts.run_select(l, moe.Routing(6, score="sigmoid", n_group=G, topk_group=kept))
+    assert np.array_equal(ids, mo.select_ids(l, 6, "softmax", None, G, kept, 1))
+    wr = mo.select_weights(l, ids, "sigmoid", True)
+    assert np.all(np.abs(w - wr) <= ts.rel_tol(l, 6) * wr)

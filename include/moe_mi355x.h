@@ -552,6 +552,61 @@ int moe_linear_quantized(const uint16_t* x, const moe_quantized_matrix* w, int M
                          int gated, const float* row_scale, const uint16_t* addend, uint16_t* out,
                          void* stream);
 
+/* Bytes of workspace of moe_token_logprobs (0: unsupported sizes). */
+size_t moe_token_logprobs_workspace_size(int logits_fp32, int M, int V, int top);
+
+/*
+ * moe_token_logprobs -- what is read from an output head's logits: the log
+ * probability of one given token per row, the entropy, and the most likely
+ * alternatives (two launches).
+ *
+ *   p = softmax(l)                      over the V logits of a row
+ *   logprobs[m] = log p[tokens[m]]      0 where tokens[m] is outside [0, V)
+ *   entropy[m]  = -sum_v p_v log p_v    (p = 0 adds 0)
+ *   lse[m]      = log sum_v e^(l_v)
+ *   top_ids[m, :], top_logprobs[m, :]: the `top` largest logits in descending
+ *               order, exact ties to the lower id, and their log p
+ *
+ *   logits      [M, V] bf16 (logits_fp32 0) or fp32 (1), 16-byte aligned; rows
+ *               follow one another without padding, V of any size
+ *   tokens      [M] int32
+ *   logprobs, entropy, lse [M] fp32 out
+ *   top_ids [M, top] int32, top_logprobs [M, top] fp32 out (top 0: not read)
+ *   workspace   moe_token_logprobs_workspace_size(...) bytes, 16-byte aligned
+ * Outputs and workspace overlap neither each other nor an input.  M < 2^21,
+ * V <= 2^19, M*V <= 2^35, top <= min(V, 32).
+ * Logits may be -inf (a token ruled out).  A row of -inf throughout has log
+ * probabilities and lse -inf, entropy 0, and the lowest ids as alternatives.
+ * A row with a NaN or +inf has NaN in all its fp32 outputs; its alternatives'
+ * ids stay in order, NaN after -inf.  No sum depends on the other rows or on
+ * timing: equal inputs give equal bits.
+ */
+int moe_token_logprobs(const void* logits, int logits_fp32, const int32_t* tokens, int M, int V,
+                       int top, float* logprobs, float* entropy, float* lse, int32_t* top_ids,
+                       float* top_logprobs, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * moe_token_logprobs_backward -- gradient of moe_token_logprobs's logprobs
+ * and entropy with respect to the logits (one launch).
+ *
+ *   grad_logits[m, v] = grad_logprobs[m] (1{v = tokens[m]} - p_v)
+ *                       - grad_entropy[m] p_v (log p_v + entropy[m]),
+ *   log p_v = l_v - lse[m]
+ *
+ *   logits, tokens, M, V as given to moe_token_logprobs, lse and entropy as it
+ *   wrote them; entropy is not read where grad_entropy is NULL (0)
+ *   grad_logprobs, grad_entropy [M] fp32
+ *   grad_logits  [M, V] of the logits' type out, 16-byte aligned; logits
+ *                itself, or overlapping no input
+ * A token outside [0, V) leaves its logprob without a gradient.  A row whose
+ * lse is below -1e30 (no logit, or only a mask's lowest value, which fp32
+ * cannot tell from its lse) has gradient 0.
+ */
+int moe_token_logprobs_backward(const void* logits, int logits_fp32, const int32_t* tokens,
+                                const float* lse, const float* entropy,
+                                const float* grad_logprobs, const float* grad_entropy, int M,
+                                int V, void* grad_logits, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,8 +12,9 @@ moe_forward_quantized, moe_forward_mxfp8, moe_mx_quantize, plus
 moe_workspace_size, moe_mx_workspace_size, moe_pick_block_m,
 moe_forward_list_offsets and moe_strerror; and, with a :class:`Routing` rule,
 moe_select, moe_select_backward, moe_route_scored, moe_forward_scored,
-moe_forward_quantized_scored and moe_forward_mxfp8_scored; and
-moe_linear_quantized.
+moe_forward_quantized_scored and moe_forward_mxfp8_scored;
+moe_linear_quantized; and moe_token_logprobs with its gradient
+moe_token_logprobs_backward.
 """
 
 from __future__ import annotations
@@ -137,6 +138,11 @@ _SIGNATURES = {
                                  [_c_int] * 4 + [_c_void_p] * 4 +
                                  [_c_size_t, ctypes.POINTER(DispatchInfo), _c_void_p]),
     "moe_linear_quantized": (_c_int, [_c_void_p] * 2 + [_c_int] * 4 + [_c_void_p] * 4),
+    "moe_token_logprobs_workspace_size": (_c_size_t, [_c_int] * 4),
+    "moe_token_logprobs": (_c_int, [_c_void_p, _c_int, _c_void_p] + [_c_int] * 3 +
+                           [_c_void_p] * 6 + [_c_size_t, _c_void_p]),
+    "moe_token_logprobs_backward": (_c_int, [_c_void_p, _c_int] + [_c_void_p] * 5 + [_c_int] * 2 +
+                                    [_c_void_p] * 2),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -937,3 +943,128 @@ def moe_linear_quantized(x, weight: dict, gated: bool = False, row_scale=None, a
     if st:
         _raise("moe_linear_quantized", st)
     return out
+
+
+# ---------------------------------------------------------------------------
+# log probabilities of tokens
+# ---------------------------------------------------------------------------
+
+def _workspace_of(call: str, nbytes: int, ws, device: int, stream):
+    """The workspace of a call that needs nbytes (0: sizes it refuses)."""
+    if nbytes == 0:
+        raise MoeError(call, -2)
+    if ws is None:
+        return _empty((nbytes,), _torch().uint8, device, stream)
+    _need(ws, "ws", _torch().uint8, (ws.numel(),), device)
+    return ws
+
+
+def _logits_type(call: str, logits):
+    """(M, V, fp32 flag) of a tensor of logit rows."""
+    torch = _torch()
+    M, V = logits.shape
+    if M >= _INT_END or V >= _INT_END:
+        raise MoeError(call, -2)
+    if logits.dtype is not torch.bfloat16 and logits.dtype is not torch.float32:
+        raise ValueError(f"logits has dtype {logits.dtype}, expected bfloat16 or float32")
+    return M, V, 1 if logits.dtype is torch.float32 else 0
+
+
+def moe_token_logprobs_workspace_size(M: int, V: int, top: int = 0, fp32: bool = False) -> int:
+    """Workspace bytes of moe_token_logprobs (0: unsupported sizes)."""
+    if max(M, V, top) >= _INT_END:
+        return 0
+    return int(library().moe_token_logprobs_workspace_size(int(bool(fp32)), M, V, top))
+
+
+def token_logprobs_workspace(M: int, V: int, top: int = 0, device=None):
+    """Workspace tensor (uint8) for moe_token_logprobs calls of these sizes,
+    for either type of logits."""
+    n = [moe_token_logprobs_workspace_size(M, V, top, fp32) for fp32 in (False, True)]
+    if min(n) == 0:
+        raise MoeError("moe_token_logprobs_workspace_size", -2)
+    return _torch().empty(max(n), dtype=_torch().uint8, device=device or "cuda")
+
+
+def moe_token_logprobs(logits, tokens, top: int = 0, logprobs=None, entropy=None, lse=None,
+                       top_ids=None, top_logprobs=None, ws=None, stream=None):
+    """Of each row of logits [M, V] (bf16 or fp32): the log probability of its
+    token (``tokens`` [M] int32; 0 where a token lies outside [0, V)), the
+    entropy of its softmax and the logarithm of its sum of exponentials, all
+    [M] fp32, and the ``top`` most likely tokens (at most 32) with their log
+    probabilities, [M, top] int32 and fp32, the most likely first, ties to the
+    lower id.  Returns (logprobs, entropy, lse, top_ids, top_logprobs), the
+    last two None without ``top``.  Logits may be -inf (a token ruled out); a
+    row that is -inf throughout has log probabilities and lse -inf and entropy
+    0.  A row with NaN or +inf gives NaN; its alternatives stay in order, NaN
+    last."""
+    torch = _torch()
+    M, V, fp32 = _logits_type("moe_token_logprobs", logits)
+    top = int(top)
+    if not 0 <= top < _INT_END:
+        raise MoeError("moe_token_logprobs", -1)
+    dev = logits.get_device()
+    if not _current(dev):
+        return _elsewhere(dev, moe_token_logprobs, logits, tokens, top, logprobs, entropy, lse,
+                          top_ids, top_logprobs, ws, stream)
+    _need(logits, "logits", logits.dtype, (M, V), dev)
+    _need(tokens, "tokens", torch.int32, (M,), dev)
+    need = library().moe_token_logprobs_workspace_size(fp32, M, V, top)
+    ws = _workspace_of("moe_token_logprobs", need, ws, dev, stream)
+    f32 = torch.float32
+    outs = []
+    for name, t, dtype, shape in (("logprobs", logprobs, f32, (M,)), ("entropy", entropy, f32, (M,)),
+                                  ("lse", lse, f32, (M,)),
+                                  ("top_ids", top_ids, torch.int32, (M, top)),
+                                  ("top_logprobs", top_logprobs, f32, (M, top))):
+        if top == 0 and len(shape) == 2:
+            t = None
+        elif t is None:
+            t = _empty(shape, dtype, dev, stream)
+        else:
+            _need(t, name, dtype, shape, dev)
+        outs.append(t)
+    st = library().moe_token_logprobs(logits.data_ptr(), fp32, tokens.data_ptr(), M, V, top,
+                                      *map(_ptr, outs), ws.data_ptr(), ws.numel(),
+                                      _raw_stream(dev, stream))
+    if st:
+        _raise("moe_token_logprobs", st)
+    return tuple(outs)
+
+
+def moe_token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs, grad_entropy=None,
+                                grad_logits=None, stream=None):
+    """Gradient [M, V], in the type of the logits, of moe_token_logprobs's
+    logprobs and entropy with respect to its logits, for the lse and entropy
+    that it gave and their gradients [M] fp32 (``grad_entropy`` None: the
+    entropy has none, and ``entropy`` may be None).  ``grad_logits`` may be
+    ``logits`` itself; else it overlaps no operand.  A token outside [0, V)
+    leaves its logprob without a gradient; a row whose lse is below -1e30
+    (every logit ruled out) has gradient 0."""
+    torch = _torch()
+    M, V, fp32 = _logits_type("moe_token_logprobs_backward", logits)
+    dev = logits.get_device()
+    if not _current(dev):
+        return _elsewhere(dev, moe_token_logprobs_backward, logits, tokens, lse, entropy,
+                          grad_logprobs, grad_entropy, grad_logits, stream)
+    _need(logits, "logits", logits.dtype, (M, V), dev)
+    _need(tokens, "tokens", torch.int32, (M,), dev)
+    for name, t, optional in (("lse", lse, False), ("entropy", entropy, grad_entropy is None),
+                              ("grad_logprobs", grad_logprobs, False),
+                              ("grad_entropy", grad_entropy, True)):
+        if t is None and optional:
+            continue
+        if t is None:
+            raise ValueError(f"{name} is required")
+        _need(t, name, torch.float32, (M,), dev)
+    if grad_logits is None:
+        grad_logits = _empty((M, V), logits.dtype, dev, stream)
+    else:
+        _need(grad_logits, "grad_logits", logits.dtype, (M, V), dev)
+    st = library().moe_token_logprobs_backward(
+        logits.data_ptr(), fp32, tokens.data_ptr(), lse.data_ptr(), _ptr(entropy),
+        grad_logprobs.data_ptr(), _ptr(grad_entropy), M, V, grad_logits.data_ptr(),
+        _raw_stream(dev, stream))
+    if st:
+        _raise("moe_token_logprobs_backward", st)
+    return grad_logits

@@ -1,0 +1,110 @@
+// C ABI of the dense operators around the routed experts: argument checks and
+// launches.  Declarations and the contract of every call are in
+// include/moe_mi355x.h.
+#include <initializer_list>
+
+#include "dense.h"
+#include "moe_mi355x.h"
+
+using namespace moe_host;
+
+namespace {
+
+bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// An operand's memory (null: the operand is absent).
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  if (a.p == nullptr || b.p == nullptr) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.bytes && y < x + a.bytes;
+}
+// Whether an output shares memory with another output or an input.
+bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span* q = o + 1; q != outs.end(); ++q)
+      if (overlap(*o, *q)) return true;
+    for (const Span& i : ins)
+      if (overlap(*o, i)) return true;
+  }
+  return false;
+}
+
+#define MOE_TRY_LAUNCH(expr) \
+  do {                       \
+    if ((expr) != hipSuccess) return MOE_ERR_HIP; \
+  } while (0)
+
+constexpr int kMaxVocabulary = 1 << 19;
+constexpr int kMaxLogitRows = 1 << 21;
+constexpr long long kMaxLogits = 1LL << 35;
+constexpr int kMaxAlternatives = 32;
+
+int check_logits(int logits_fp32, int M, int V) {
+  if (M < 0 || V <= 0 || (logits_fp32 != 0 && logits_fp32 != 1)) return MOE_ERR_INVALID_ARG;
+  if (M >= kMaxLogitRows || V > kMaxVocabulary || (long long)M * V > kMaxLogits)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_token_logprobs_workspace_size(int logits_fp32, int M, int V, int top) {
+  if (check_logits(logits_fp32, M, V) != MOE_OK || top < 0 || top > kMaxAlternatives || top > V)
+    return 0;
+  const size_t n = logprob_partial_bytes(M, V, top, !logits_fp32);
+  return n > 16 ? n : 16;
+}
+
+int moe_token_logprobs(const void* logits, int logits_fp32, const int32_t* tokens, int M, int V,
+                       int top, float* logprobs, float* entropy, float* lse, int32_t* top_ids,
+                       float* top_logprobs, void* workspace, size_t ws_bytes, void* stream) {
+  const int st = check_logits(logits_fp32, M, V);
+  if (st != MOE_OK) return st;
+  if (top < 0 || top > V) return MOE_ERR_INVALID_ARG;
+  if (top > kMaxAlternatives) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!logits || !tokens || !logprobs || !entropy || !lse || (top > 0 && (!top_ids || !top_logprobs)))
+    return MOE_ERR_INVALID_ARG;
+  if (!a16(logits) || !a16(workspace)) return MOE_ERR_INVALID_ARG;
+  const size_t need = logprob_partial_bytes(M, V, top, !logits_fp32);
+  if (workspace == nullptr || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  const size_t row = (size_t)M * 4, alt = row * top;
+  if (clash({{logprobs, row}, {entropy, row}, {lse, row}, {top > 0 ? top_ids : nullptr, alt},
+             {top > 0 ? top_logprobs : nullptr, alt}, {workspace, need}},
+            {{logits, (size_t)M * V * (logits_fp32 ? 4 : 2)}, {tokens, row}}))
+    return MOE_ERR_INVALID_ARG;
+  const LogprobArgs a{logits, !logits_fp32, tokens, M, V, top, logprobs, entropy, lse, top_ids,
+                      top_logprobs, workspace};
+  MOE_TRY_LAUNCH(launch_token_logprobs(a, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+int moe_token_logprobs_backward(const void* logits, int logits_fp32, const int32_t* tokens,
+                                const float* lse, const float* entropy,
+                                const float* grad_logprobs, const float* grad_entropy, int M,
+                                int V, void* grad_logits, void* stream) {
+  const int st = check_logits(logits_fp32, M, V);
+  if (st != MOE_OK) return st;
+  if (M == 0) return MOE_OK;
+  if (!logits || !tokens || !lse || !grad_logprobs || !grad_logits || (grad_entropy && !entropy))
+    return MOE_ERR_INVALID_ARG;
+  if (!a16(logits) || !a16(grad_logits)) return MOE_ERR_INVALID_ARG;
+  const size_t all = (size_t)M * V * (logits_fp32 ? 4 : 2), row = (size_t)M * 4;
+  // grad_logits may be logits itself: each logit is read where its gradient is written
+  if (clash({{grad_logits, all}},
+            {{grad_logits == logits ? nullptr : logits, all}, {tokens, row}, {lse, row},
+             {grad_entropy ? entropy : nullptr, row}, {grad_logprobs, row}, {grad_entropy, row}}))
+    return MOE_ERR_INVALID_ARG;
+  const LogprobGradArgs a{logits, !logits_fp32, tokens, lse, entropy, grad_logprobs, grad_entropy,
+                          M, V, grad_logits};
+  MOE_TRY_LAUNCH(launch_token_logprobs_backward(a, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,54 @@
+"""float64 numpy forms of the dense operators around the routed experts: token
+log probabilities, the gated block and adapters, with their gradients.  Each
+follows its definition; nothing here is shared with the GPU path."""
+
+from __future__ import annotations
+
+import numpy as np
+
+
+def token_logprobs(logits: np.ndarray, tokens: np.ndarray, top: int = 0) -> dict:
+    """logits [M, V] (any float type, read as they are), tokens [M]."""
+    l = logits.astype(np.float64)
+    M, V = l.shape
+    out = dict(logprobs=np.zeros(M), entropy=np.zeros(M), lse=np.zeros(M),
+               top_ids=np.zeros((M, top), np.int64), top_logprobs=np.zeros((M, top)))
+    with np.errstate(invalid="ignore", divide="ignore"):
+        for m in range(M):
+            r = l[m]
+            if np.all(r == -np.inf):
+                lse, logp, ent = -np.inf, np.full(V, -np.inf), 0.0
+            elif np.isnan(r).any() or (r == np.inf).any():
+                lse, logp, ent = np.nan, np.full(V, np.nan), np.nan
+            else:
+                x = r - r.max()
+                lz = np.log(np.exp(x).sum())
+                lse, logp = r.max() + lz, x - lz
+                p = np.exp(logp)
+                ent = -np.where(p > 0, p * np.where(p > 0, logp, 0.0), 0.0).sum()
+            out["lse"][m], out["entropy"][m] = lse, ent
+            if 0 <= tokens[m] < V:
+                out["logprobs"][m] = logp[tokens[m]]
+            # NaN after everything, then by logit, then by id
+            order = np.lexsort((np.arange(V), -np.where(np.isnan(r), -np.inf, r), np.isnan(r)))
+            out["top_ids"][m] = order[:top]
+            out["top_logprobs"][m] = logp[order[:top]]
+    return out
+
+
+def token_logprobs_backward(logits, tokens, lse, entropy, g, h) -> np.ndarray:
+    """From the lse and entropy given, g and h the gradients of logprobs and
+    entropy."""
+    l = logits.astype(np.float64)
+    out = np.zeros_like(l)
+    for m in range(l.shape[0]):
+        if lse[m] < -1e30:
+            continue
+        logp = l[m] - np.float64(lse[m])
+        p = np.exp(logp)
+        gm = np.float64(g[m]) if 0 <= tokens[m] < l.shape[1] else 0.0
+        inner = gm + np.float64(h[m]) * (np.where(p > 0, logp, 0.0) + np.float64(entropy[m]))
+        out[m] = -p * inner
+        if gm:
+            out[m, tokens[m]] += gm
+    return out

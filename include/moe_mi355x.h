@@ -552,7 +552,49 @@ int moe_linear_quantized(const uint16_t* x, const moe_quantized_matrix* w, int M
                          int gated, const float* row_scale, const uint16_t* addend, uint16_t* out,
                          void* stream);
 
-/* Bytes of workspace of moe_token_logprobs (0: unsupported sizes). */
+/*
+ * moe_linear_gated -- a gated feed-forward block's activations with bf16
+ * weights, for any batch: a shared expert beside the routed ones (its down
+ * rows are an ordinary product).
+ *
+ *   out[m, i] = bf16(SiLU(x[m] . w13[i]) * (x[m] . w13[I + i]))    fp32 sums
+ *
+ *   x [M, H], w13 [2I, H] (gate rows first, as one expert's W13), out [M, I],
+ *   bf16; out overlaps no operand
+ * One launch, no workspace.  H and I multiples of 8, at most 2^17; M < 2^21.
+ * A row of x that is not finite gives results that are not finite in its own
+ * row of out and in no other.
+ */
+int moe_linear_gated(const uint16_t* x, const uint16_t* w13, int M, int H, int I, uint16_t* out,
+                     void* stream);
+
+/* Bytes of workspace of moe_linear_gated_backward for any batch of at most M
+ * rows (0: unsupported sizes). */
+size_t moe_linear_gated_backward_workspace_size(int M, int H, int I);
+
+/*
+ * moe_linear_gated_backward -- gradient of moe_linear_gated with respect to x
+ * and w13.  The forward pass leaves nothing behind: gate and up are formed
+ * again (three products of 4 M H I operations; two where a gradient is not
+ * wanted).
+ *
+ *   s = sigmoid(gate),  d = grad_out
+ *   d_up = d * gate * s,  d_gate = d * up * s * (1 + gate (1 - s))
+ *   grad_x   = [d_gate d_up] w13          grad_w13 = [d_gate d_up]^T x
+ *
+ *   x, w13, M, H, I as given to moe_linear_gated; grad_out [M, I] bf16
+ *   grad_x [M, H], grad_w13 [2I, H] bf16 out, either may be NULL (not wanted)
+ *   workspace  moe_linear_gated_backward_workspace_size(...) bytes
+ * d_gate and d_up are rounded to bf16, the sums are fp32.  Outputs and
+ * workspace overlap neither each other nor an input.  M = 0: grad_w13 is set
+ * to 0.  Equal inputs give equal bits.
+ */
+int moe_linear_gated_backward(const uint16_t* x, const uint16_t* w13, const uint16_t* grad_out,
+                              int M, int H, int I, uint16_t* grad_x, uint16_t* grad_w13,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of moe_token_logprobs for any batch of at most M rows
+ * (0: unsupported sizes). */
 size_t moe_token_logprobs_workspace_size(int logits_fp32, int M, int V, int top);
 
 /*

@@ -13,8 +13,8 @@ moe_workspace_size, moe_mx_workspace_size, moe_pick_block_m,
 moe_forward_list_offsets and moe_strerror; and, with a :class:`Routing` rule,
 moe_select, moe_select_backward, moe_route_scored, moe_forward_scored,
 moe_forward_quantized_scored and moe_forward_mxfp8_scored;
-moe_linear_quantized; and moe_token_logprobs with its gradient
-moe_token_logprobs_backward.
+moe_linear_quantized; moe_linear_gated and moe_token_logprobs with their
+gradients moe_linear_gated_backward and moe_token_logprobs_backward.
 """
 
 from __future__ import annotations
@@ -138,6 +138,10 @@ _SIGNATURES = {
                                  [_c_int] * 4 + [_c_void_p] * 4 +
                                  [_c_size_t, ctypes.POINTER(DispatchInfo), _c_void_p]),
     "moe_linear_quantized": (_c_int, [_c_void_p] * 2 + [_c_int] * 4 + [_c_void_p] * 4),
+    "moe_linear_gated": (_c_int, [_c_void_p] * 2 + [_c_int] * 3 + [_c_void_p] * 2),
+    "moe_linear_gated_backward_workspace_size": (_c_size_t, [_c_int] * 3),
+    "moe_linear_gated_backward": (_c_int, [_c_void_p] * 3 + [_c_int] * 3 + [_c_void_p] * 3 +
+                                  [_c_size_t, _c_void_p]),
     "moe_token_logprobs_workspace_size": (_c_size_t, [_c_int] * 4),
     "moe_token_logprobs": (_c_int, [_c_void_p, _c_int, _c_void_p] + [_c_int] * 3 +
                            [_c_void_p] * 6 + [_c_size_t, _c_void_p]),
@@ -946,7 +950,7 @@ def moe_linear_quantized(x, weight: dict, gated: bool = False, row_scale=None, a
 
 
 # ---------------------------------------------------------------------------
-# log probabilities of tokens
+# a gated block in bf16 and its gradient
 # ---------------------------------------------------------------------------
 
 def _workspace_of(call: str, nbytes: int, ws, device: int, stream):
@@ -958,6 +962,95 @@ def _workspace_of(call: str, nbytes: int, ws, device: int, stream):
     _need(ws, "ws", _torch().uint8, (ws.numel(),), device)
     return ws
 
+
+def moe_linear_gated(x, w13, out=None, stream=None):
+    """out [M, I] bf16 = SiLU(x Wg^T) * (x Wu^T) for x [M, H] and w13 [2I, H]
+    (gate rows first), bf16: a dense gated block, e.g. a shared expert's.  H and
+    I are multiples of 8; ``out`` overlaps no operand."""
+    torch = _torch()
+    M, H = x.shape
+    two_i = w13.shape[0]
+    if max(M, H, two_i) >= _INT_END or two_i % 2 != 0:
+        raise MoeError("moe_linear_gated", -2)
+    dev = x.get_device()
+    if not _current(dev):
+        return _elsewhere(dev, moe_linear_gated, x, w13, out, stream)
+    bf16, shape = torch.bfloat16, (M, two_i // 2)
+    _need(x, "x", bf16, (M, H), dev)
+    _need(w13, "w13", bf16, (two_i, H), dev)
+    if out is None:
+        out = _empty(shape, bf16, dev, stream)
+    else:
+        _need(out, "out", bf16, shape, dev)
+    st = library().moe_linear_gated(x.data_ptr(), w13.data_ptr(), M, H, two_i // 2, out.data_ptr(),
+                                    _raw_stream(dev, stream))
+    if st:
+        _raise("moe_linear_gated", st)
+    return out
+
+
+def moe_linear_gated_backward_workspace_size(M: int, H: int, I: int) -> int:
+    """Workspace bytes of moe_linear_gated_backward (0: unsupported sizes)."""
+    if max(M, H, I) >= _INT_END:
+        return 0
+    return int(library().moe_linear_gated_backward_workspace_size(M, H, I))
+
+
+def linear_gated_backward_workspace(M: int, H: int, I: int, device=None):
+    """Workspace tensor (uint8) for moe_linear_gated_backward calls of at most M
+    rows."""
+    n = moe_linear_gated_backward_workspace_size(M, H, I)
+    if n == 0:
+        raise MoeError("moe_linear_gated_backward_workspace_size", -2)
+    return _torch().empty(n, dtype=_torch().uint8, device=device or "cuda")
+
+
+def moe_linear_gated_backward(x, w13, grad_out, grad_x=None, grad_w13=None, need_x: bool = True,
+                              need_w13: bool = True, ws=None, stream=None):
+    """Gradients (grad_x [M, H], grad_w13 [2I, H]), bf16, of moe_linear_gated
+    for the gradient grad_out [M, I] bf16 of its output; gate and up are formed
+    again from x and w13.  ``need_x`` or ``need_w13`` False: that gradient is
+    not formed, and None is in its place.  Outputs overlap neither each other
+    nor an operand."""
+    torch = _torch()
+    M, H = x.shape
+    two_i = w13.shape[0]
+    if max(M, H, two_i) >= _INT_END or two_i % 2 != 0:
+        raise MoeError("moe_linear_gated_backward", -2)
+    dev = x.get_device()
+    if not _current(dev):
+        return _elsewhere(dev, moe_linear_gated_backward, x, w13, grad_out, grad_x, grad_w13,
+                          need_x, need_w13, ws, stream)
+    if not need_x and not need_w13:
+        raise MoeError("moe_linear_gated_backward", -1)
+    bf16 = torch.bfloat16
+    _need(x, "x", bf16, (M, H), dev)
+    _need(w13, "w13", bf16, (two_i, H), dev)
+    _need(grad_out, "grad_out", bf16, (M, two_i // 2), dev)
+    outs = []
+    for name, t, shape, need in (("grad_x", grad_x, (M, H), need_x),
+                                 ("grad_w13", grad_w13, (two_i, H), need_w13)):
+        if not need:
+            if t is not None:
+                raise ValueError(f"{name} is given but not needed")
+        elif t is None:
+            t = _empty(shape, bf16, dev, stream)
+        else:
+            _need(t, name, bf16, shape, dev)
+        outs.append(t)
+    need = library().moe_linear_gated_backward_workspace_size(M, H, two_i // 2)
+    ws = _workspace_of("moe_linear_gated_backward", need, ws, dev, stream)
+    st = library().moe_linear_gated_backward(
+        x.data_ptr(), w13.data_ptr(), grad_out.data_ptr(), M, H, two_i // 2, *map(_ptr, outs),
+        ws.data_ptr(), ws.numel(), _raw_stream(dev, stream))
+    if st:
+        _raise("moe_linear_gated_backward", st)
+    return tuple(outs)
+
+
+# ---------------------------------------------------------------------------
+# log probabilities of tokens
+# ---------------------------------------------------------------------------
 
 def _logits_type(call: str, logits):
     """(M, V, fp32 flag) of a tensor of logit rows."""
@@ -978,7 +1071,7 @@ def moe_token_logprobs_workspace_size(M: int, V: int, top: int = 0, fp32: bool =
 
 
 def token_logprobs_workspace(M: int, V: int, top: int = 0, device=None):
-    """Workspace tensor (uint8) for moe_token_logprobs calls of these sizes,
+    """Workspace tensor (uint8) for moe_token_logprobs calls of at most M rows,
     for either type of logits."""
     n = [moe_token_logprobs_workspace_size(M, V, top, fp32) for fp32 in (False, True)]
     if min(n) == 0:

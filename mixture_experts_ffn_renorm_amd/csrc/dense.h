@@ -36,4 +36,29 @@ struct LogprobGradArgs {
 };
 hipError_t launch_token_logprobs_backward(const LogprobGradArgs& a, hipStream_t s);
 
+// Gated block: act = SiLU(x Wg^T) * (x Wu^T), w13 = [Wg; Wu].
+struct GatedArgs {
+  const uint16_t* x;         // [M, H]
+  const uint16_t* w13;       // [2I, H]
+  int M, H, I;
+  uint16_t* out;             // [M, I]
+};
+hipError_t launch_gated(const GatedArgs& a, hipStream_t s);
+
+// Its gradient, with gate and up formed again.
+struct GatedGradArgs {
+  const uint16_t* x;         // [M, H]
+  const uint16_t* w13;       // [2I, H]
+  const uint16_t* grad_out;  // [M, I]
+  int M, H, I;
+  uint16_t* grad_x;          // [M, H] or null
+  uint16_t* grad_w13;        // [2I, H] or null
+  void* workspace;           // gated_backward_bytes
+};
+size_t gated_backward_bytes(int M, int H, int I);
+hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s);
+
+// bytes (a multiple of 16) of zeros
+hipError_t launch_zero(void* p, size_t bytes, hipStream_t s);
+
 }  // namespace moe_host

@@ -42,6 +42,8 @@ constexpr int kMaxVocabulary = 1 << 19;
 constexpr int kMaxLogitRows = 1 << 21;
 constexpr long long kMaxLogits = 1LL << 35;
 constexpr int kMaxAlternatives = 32;
+constexpr int kMaxRows = 1 << 21;
+constexpr int kMaxFeatures = 1 << 17;
 
 int check_logits(int logits_fp32, int M, int V) {
   if (M < 0 || V <= 0 || (logits_fp32 != 0 && logits_fp32 != 1)) return MOE_ERR_INVALID_ARG;
@@ -50,9 +52,60 @@ int check_logits(int logits_fp32, int M, int V) {
   return MOE_OK;
 }
 
+// Sizes of the gated block: as for the layer's experts, one expert.
+int check_gated(int M, int H, int I) {
+  if (M < 0 || H <= 0 || I <= 0) return MOE_ERR_INVALID_ARG;
+  if (H % 8 != 0 || I % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (M >= kMaxRows || H > kMaxFeatures || I > kMaxFeatures) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+int moe_linear_gated(const uint16_t* x, const uint16_t* w13, int M, int H, int I, uint16_t* out,
+                     void* stream) {
+  const int st = check_gated(M, H, I);
+  if (st != MOE_OK) return st;
+  if (M == 0) return MOE_OK;
+  if (!x || !w13 || !out || !a16(x) || !a16(w13) || !a16(out)) return MOE_ERR_INVALID_ARG;
+  if (clash({{out, (size_t)M * I * 2}}, {{x, (size_t)M * H * 2}, {w13, (size_t)I * H * 4}}))
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY_LAUNCH(launch_gated(GatedArgs{x, w13, M, H, I, out}, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_linear_gated_backward_workspace_size(int M, int H, int I) {
+  if (check_gated(M, H, I) != MOE_OK) return 0;
+  const size_t n = M == 0 ? 0 : gated_backward_bytes(M, H, I);
+  return n > 16 ? n : 16;
+}
+
+int moe_linear_gated_backward(const uint16_t* x, const uint16_t* w13, const uint16_t* grad_out,
+                              int M, int H, int I, uint16_t* grad_x, uint16_t* grad_w13,
+                              void* workspace, size_t ws_bytes, void* stream) {
+  const int st = check_gated(M, H, I);
+  if (st != MOE_OK) return st;
+  if (!grad_x && !grad_w13 && M > 0) return MOE_ERR_INVALID_ARG;
+  if (!a16(x) || !a16(w13) || !a16(grad_out) || !a16(grad_x) || !a16(grad_w13) || !a16(workspace))
+    return MOE_ERR_INVALID_ARG;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const size_t rows = (size_t)M * H * 2, weights = (size_t)I * H * 4;
+  if (M == 0) {   // no rows: the weights' gradient is 0
+    if (grad_w13) MOE_TRY_LAUNCH(launch_zero(grad_w13, weights, s));
+    return MOE_OK;
+  }
+  if (!x || !w13 || !grad_out) return MOE_ERR_INVALID_ARG;
+  const size_t need = gated_backward_bytes(M, H, I);
+  if (workspace == nullptr || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (clash({{grad_x, rows}, {grad_w13, weights}, {workspace, need}},
+            {{x, rows}, {w13, weights}, {grad_out, (size_t)M * I * 2}}))
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY_LAUNCH(launch_gated_backward(
+      GatedGradArgs{x, w13, grad_out, M, H, I, grad_x, grad_w13, workspace}, s));
+  return MOE_OK;
+}
 
 size_t moe_token_logprobs_workspace_size(int logits_fp32, int M, int V, int top) {
   if (check_logits(logits_fp32, M, V) != MOE_OK || top < 0 || top > kMaxAlternatives || top > V)

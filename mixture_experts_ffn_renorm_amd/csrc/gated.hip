@@ -1,0 +1,416 @@
+// A gated feed-forward block in bf16 and its gradient:
+//   gate = x Wg^T,  up = x Wu^T,  act = SiLU(gate) * up      w13 = [Wg; Wu]
+//   s = 1 / (1 + e^-gate)
+//   d_up = d_act * gate * s,  d_gate = d_act * up * s * (1 + gate (1 - s))
+//   d_x = [d_gate d_up] w13,  d_w13 = [d_gate d_up]^T x
+//
+// Four products on one tile kernel.  d_gate and d_up are rounded to bf16 once,
+// as the matrix cores take them; every sum is fp32.
+#include <algorithm>
+#include <type_traits>
+
+#include "dense.h"
+
+using namespace moe;
+
+namespace {
+
+constexpr int kBK = 32;            // elements of the summed axis per stage
+constexpr int kStages = 4;         // stages in LDS
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// Which product a tile kernel forms.  n is the output's contiguous axis.
+//   kAct, kGradAct: out[m, i] from gate and up, both [m, n] = x w13^T
+//   kGradX:  out[m, n] = sum_k d[m, k] w13[k, n]
+//   kGradW:  out[m, n] = sum_k d[k, m] x[k, n]
+enum Op { kAct, kGradAct, kGradX, kGradW };
+
+// One operand: its rows (the output's axis) by k.
+//   across false: element (r, k) at p[r * ld + k];  true: at p[k * ld + r].
+struct TileArgs {
+  const uint16_t* m_side;
+  const uint16_t* n_side;
+  int m_ld, n_ld;
+  int rows, cols, K;         // output rows and columns (gated: columns of out), summed length
+  int tiles_m, tiles_n, splits, k_per;   // K split into `splits` ranges of k_per
+  const uint16_t* grad_out;  // kGradAct: [rows, cols]
+  uint16_t* out;             // [rows, out_ld]
+  int out_ld;
+  float* partial;            // splits > 1: [splits, rows, cols]
+};
+
+// Swizzles of the LDS tiles, in 16-byte pieces.  Rows of 32 k (64 bytes):
+// piece c of row r lies at c ^ (r / 2 % 4), so that eight rows of one beat of
+// a 16-byte read lie in different banks.  Rows of R columns: the pairs of
+// pieces are exchanged by the bits of k in which the lanes of a transposing
+// read differ.
+__device__ __forceinline__ int along_swizzle(int r) { return (r >> 1) & 3; }
+__device__ __forceinline__ int across_swizzle(int k) { return ((k & 3) | ((k >> 1) & 4)) << 1; }
+
+// load_lds16 whose completion the kernel waits for itself (wait_vmem): the
+// compiler, which cannot tell the stages of the ring apart, would wait for
+// every copy in flight before each read of LDS.  `lds` is a byte address in
+// LDS, the same for the whole wave.  (m0 is reserved: nothing else in these
+// kernels uses it.)
+__device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :
+               : "v"(src), "s"(lds)
+               : "memory");
+}
+
+// The loads of one operand's stages: R rows by kBK k, by W waves.
+template <int R, int W, bool kAcross>
+struct Loader {
+  static constexpr int kInstr = R * kBK * 2 / 1024 / W;   // 1 KB each
+  const uint8_t* src[kInstr];
+  int k[kInstr];             // k of the lane's piece within a stage
+  size_t step;
+  // row(r): the operand's row of tile row r (clamped to one that exists);
+  // across: the tile's first column and how many columns there are
+  template <class F>
+  __device__ __forceinline__ void init(const uint16_t* p, int ld, int k0, F row, int c0, int ncols,
+                                       int wave, int lane) {
+#pragma unroll
+    for (int i = 0; i < kInstr; ++i) {
+      const int q = wave * kInstr + i;
+      if (kAcross) {
+        constexpr int kPieces = R / 8;                    // per k
+        k[i] = q * (64 / kPieces) + lane / kPieces;
+        const int c = (lane % kPieces) ^ across_swizzle(k[i]);
+        const int col = min(c0 + c * 8, ncols - 8);
+        src[i] = reinterpret_cast<const uint8_t*>(p + (size_t)(k0 + k[i]) * ld + col);
+      } else {
+        const int r = q * 16 + (lane >> 2), c = (lane & 3) ^ along_swizzle(r);
+        k[i] = c * 8;
+        src[i] = reinterpret_cast<const uint8_t*>(p + (size_t)row(r) * ld + k0 + k[i]);
+      }
+    }
+    step = kAcross ? (size_t)kBK * ld * 2 : kBK * 2;
+  }
+  // The next stage into LDS; `left` elements of k are there from its first on
+  // (none or fewer: zeros).
+  __device__ __forceinline__ void issue(uint32_t lds, int wave, int left) {
+#pragma unroll
+    for (int i = 0; i < kInstr; ++i) {
+      copy16(k[i] < left ? (const void*)src[i] : (const void*)kZeroPage,
+             lds + (wave * kInstr + i) * 1024);
+      src[i] += step;
+    }
+  }
+};
+
+// Fragments (16 rows by 32 k) of one operand's LDS tile.
+template <int R, bool kAcross>
+struct Reader {
+  int base, col, swz;        // bytes
+  __device__ __forceinline__ Reader(int row0, int lane) {
+    const int g = lane >> 4, i = lane & 15;
+    if (kAcross) {
+      const int k = 8 * g + (i >> 2);
+      base = k * R * 2 + (i & 1) * 8;
+      col = row0 * 2 + ((i & 2) << 3);
+      swz = across_swizzle(k) * 16;
+    } else {
+      base = (row0 + i) * 64 + ((g ^ along_swizzle(i)) << 4);
+      col = swz = 0;
+    }
+  }
+  __device__ __forceinline__ u32x4 read(const uint8_t* lds, int f) const {
+    if (kAcross) {
+      const uint8_t* p = lds + base + ((col + f * 32) ^ swz);
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * R * 2));
+      const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
+      return u32x4{x[0], x[1], y[0], y[1]};
+    }
+    return load16(lds + base + f * 1024);
+  }
+};
+
+// Derivatives of SiLU(g) u times d.
+__device__ __forceinline__ void gated_grad(float g, float u, float d, float& dg, float& du) {
+  const float s = 1.0f / (1.0f + __expf(-g));
+  du = d * (g * s);
+  dg = d * u * (s * (1.0f + g * (1.0f - s)));
+}
+
+template <int BM, int BN, int WM, int WN, Op kOp>
+__global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
+  constexpr int W = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  constexpr bool kGated = kOp == kAct || kOp == kGradAct;
+  constexpr bool kMAcross = kOp == kGradW, kNAcross = kOp == kGradX || kOp == kGradW;
+  constexpr int kMBytes = BM * kBK * 2, kStage = (BM + BN) * kBK * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * kStage];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  // tiles of one XCD are neighbours: columns of up to 8 tiles of m
+  int t = xcd_contiguous_tile(blockIdx.x, a.tiles_m * a.tiles_n * a.splits);
+  if (t < 0) return;
+  const int split = t / (a.tiles_m * a.tiles_n);
+  t %= a.tiles_m * a.tiles_n;
+  const int band = t / (8 * a.tiles_n), high = min(8, a.tiles_m - band * 8);
+  t -= band * 8 * a.tiles_n;
+  const int m0 = (band * 8 + t % high) * BM, tn = t / high;
+  const int n0 = tn * (kGated ? BN / 2 : BN);
+  const int k0 = split * a.k_per, K = min(a.K - k0, a.k_per);
+
+  Loader<BM, W, kMAcross> lm;
+  Loader<BN, W, kNAcross> ln;
+  lm.init(a.m_side, a.m_ld, k0, [&](int r) { return min(m0 + r, a.rows - 1); }, m0, a.rows, wave,
+          lane);
+  ln.init(a.n_side, a.n_ld, k0,
+          [&](int r) {
+            if (!kGated) return min(n0 + r, a.cols - 1);
+            // a wave's TN rows: TN/2 gates, then their ups
+            const int q = r % TN, f = min(n0 + r / TN * (TN / 2) + q % (TN / 2), a.cols - 1);
+            return q < TN / 2 ? f : a.cols + f;
+          },
+          n0, a.cols, wave, lane);
+  const Reader<BM, kMAcross> rm(wm * TM, lane);
+  const Reader<BN, kNAcross> rn(wn * TN, lane);
+
+  f32x4 acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // Stage kt of K, while the stages kt + 1 and kt + 2 are on their way:
+  // fragments to registers, the copies of stage kt + 3 sent into the LDS of
+  // stage kt - 1, which every wave has read; then the products.  Eight waves
+  // are two halves, half a stage apart, so that of the two waves of a SIMD one
+  // multiplies while the other reads.
+  constexpr bool kHalves = W == 8;
+  constexpr int kCopies = Loader<BM, W, kMAcross>::kInstr + Loader<BN, W, kNAcross>::kInstr;
+  const int nk = ceil_div(K, kBK);
+  const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds;
+  auto issue = [&](int kt) {
+    const uint32_t to = lds_at + (uint32_t)(kt % kStages) * kStage;
+    lm.issue(to, wave, K - kt * kBK);
+    ln.issue(to + kMBytes, wave, K - kt * kBK);
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  wait_vmem<(kStages - 2) * kCopies>();
+  barrier_nofence();
+  if (kHalves && wave >= W / 2) barrier_nofence();
+#pragma unroll 1
+  for (int kt = 0; kt < nk; ++kt) {
+    const uint8_t* at = lds + (kt % kStages) * kStage;
+    u32x4 fn[FN], fm[FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) fn[i] = rn.read(at + kMBytes, i);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) fm[j] = rm.read(at, j);
+    issue(kt + kStages - 1);
+    wait_lgkm0();
+    wait_vmem<(kStages - 2) * kCopies>();          // stage kt + 1 is there
+    barrier_nofence();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = mfma_16x16x32(fn[i], fm[j], acc[i][j]);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (kHalves) barrier_nofence();
+  }
+  if (kHalves && wave < W / 2) barrier_nofence();
+  wait_vmem<0>();                      // the copies past the end, of zeros
+
+  // a lane holds 4 consecutive n of one m
+  const int ml = m0 + wm * TM + (lane & 15), nq = 4 * (lane >> 4);
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const int m = ml + j * 16;
+    if (m >= a.rows) continue;
+    if (kGated) {
+#pragma unroll
+      for (int i = 0; i < FN / 2; ++i) {
+        const int n = n0 + wn * (TN / 2) + i * 16 + nq;
+        if (n >= a.cols) continue;
+        const f32x4 g = acc[i][j], u = acc[i + FN / 2][j];
+        if (kOp == kAct) {
+          u32x2 o;
+          o[0] = pack_bf16x2(silu_mul(g[0], u[0]), silu_mul(g[1], u[1]));
+          o[1] = pack_bf16x2(silu_mul(g[2], u[2]), silu_mul(g[3], u[3]));
+          *reinterpret_cast<u32x2*>(a.out + (size_t)m * a.out_ld + n) = o;
+        } else {
+          const u32x2 d = *reinterpret_cast<const u32x2*>(a.grad_out + (size_t)m * a.cols + n);
+          float dg[4], du[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            gated_grad(g[r], u[r], r & 1 ? bf16_hi(d[r >> 1]) : bf16_lo(d[r >> 1]), dg[r], du[r]);
+          uint16_t* o = a.out + (size_t)m * a.out_ld + n;
+          *reinterpret_cast<u32x2*>(o) =
+              u32x2{pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3])};
+          *reinterpret_cast<u32x2*>(o + a.cols) =
+              u32x2{pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3])};
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        const int n = n0 + wn * TN + i * 16 + nq;
+        if (n >= a.cols) continue;
+        const f32x4 v = acc[i][j];
+        if (a.splits > 1)
+          *reinterpret_cast<f32x4*>(a.partial + ((size_t)split * a.rows + m) * a.cols + n) = v;
+        else
+          *reinterpret_cast<u32x2*>(a.out + (size_t)m * a.out_ld + n) =
+              u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      }
+    }
+  }
+}
+
+// out = bf16(sum of the splits, in their order); n a multiple of 8
+__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ partial, int splits,
+                                                   size_t n, uint16_t* __restrict__ out) {
+  for (size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; at < n;
+       at += (size_t)gridDim.x * 2048) {
+    f32x4 s[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    for (int i = 0; i < splits; ++i) {
+      const f32x4* p = reinterpret_cast<const f32x4*>(partial + (size_t)i * n + at);
+      s[0] += p[0];
+      s[1] += p[1];
+    }
+    *reinterpret_cast<u32x4*>(out + at) =
+        u32x4{pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
+              pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
+  }
+}
+
+__global__ __launch_bounds__(256) void zero_kernel(u32x4* p, size_t n) {
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256)
+    p[i] = u32x4{0u, 0u, 0u, 0u};
+}
+
+using moe_host::ceil_div_host;
+
+constexpr int kMaxSplits = 16;
+constexpr int kSplitTiles = 1024;
+
+// Tile size and ranges of K of one product.
+struct Plan {
+  bool big;                  // 256 x 256 tiles, else 128 x 128
+  int splits, k_per;
+};
+Plan plan_of(int rows, int n_rows, int K, bool can_split) {
+  Plan p{true, 1, 0};
+  const int cu = 256;
+  const long long big = (long long)ceil_div_host(rows, 256) * ceil_div_host(n_rows, 256);
+  p.big = big >= cu / 2;
+  const long long tiles =
+      p.big ? big : (long long)ceil_div_host(rows, 128) * ceil_div_host(n_rows, 128);
+  const int stages = ceil_div_host(K, kBK);
+  if (can_split && tiles < cu) {
+    // whole stages, at least 8 to a range
+    const long long most = std::min(stages / 8, kMaxSplits), room = kSplitTiles / (p.big ? 4 : 1);
+    p.splits = (int)std::max<long long>(1, std::min(room / tiles, most));
+  }
+  p.k_per = ceil_div_host(stages, p.splits) * kBK;
+  p.splits = ceil_div_host(K, p.k_per);
+  return p;
+}
+
+template <Op kOp>
+hipError_t launch_tiles(TileArgs a, int n_rows, const Plan& p, hipStream_t s) {
+  a.splits = p.splits;
+  a.k_per = p.k_per;
+  a.tiles_m = ceil_div_host(a.rows, p.big ? 256 : 128);
+  a.tiles_n = ceil_div_host(n_rows, p.big ? 256 : 128);
+  const unsigned grid = (unsigned)ceil_div_host(a.tiles_m * a.tiles_n * a.splits, 8) * 8;
+  if (p.big)
+    tile_kernel<256, 256, 2, 4, kOp><<<grid, 512, 0, s>>>(a);
+  else
+    tile_kernel<128, 128, 2, 2, kOp><<<grid, 256, 0, s>>>(a);
+  if (p.splits > 1) {
+    const size_t n = (size_t)a.rows * a.cols;
+    const unsigned g = (unsigned)std::min<size_t>((n / 8 + 255) / 256, 4096);
+    join_kernel<<<g, 256, 0, s>>>(a.partial, p.splits, n, a.out);
+  }
+  return hipGetLastError();
+}
+
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+// Room for the ranges' sums of any product with at most so many rows: a plan
+// has at most kMaxSplits ranges and, where it has more than one, no more than
+// kSplitTiles tiles of 128 x 128 over all of them.
+size_t partial_bytes(int rows, int cols) {
+  return std::min<size_t>((size_t)kMaxSplits * rows * cols * 4, (size_t)kSplitTiles * 128 * 128 * 4);
+}
+
+}  // namespace
+
+namespace moe_host {
+
+hipError_t launch_gated(const GatedArgs& a, hipStream_t s) {
+  TileArgs t{};
+  t.m_side = a.x;
+  t.n_side = a.w13;
+  t.m_ld = t.n_ld = t.K = a.H;
+  t.rows = a.M;
+  t.cols = t.out_ld = a.I;
+  t.out = a.out;
+  return launch_tiles<kAct>(t, 2 * a.I, plan_of(a.M, 2 * a.I, a.H, false), s);
+}
+
+hipError_t launch_zero(void* p, size_t bytes, hipStream_t s) {
+  const size_t n = bytes / 16;
+  zero_kernel<<<(unsigned)std::min<size_t>((n + 255) / 256, 4096), 256, 0, s>>>(
+      static_cast<u32x4*>(p), n);
+  return hipGetLastError();
+}
+
+// [d_gate d_up] [M, 2I], then the larger of the two products' partial sums
+size_t gated_backward_bytes(int M, int H, int I) {
+  return align256((size_t)M * 2 * I * 2) +
+         std::max(partial_bytes(M, H), partial_bytes(2 * I, H));
+}
+
+hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s) {
+  uint16_t* d = static_cast<uint16_t*>(a.workspace);
+  float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
+                                            align256((size_t)a.M * 2 * a.I * 2));
+  TileArgs t{};
+  t.m_side = a.x;
+  t.n_side = a.w13;
+  t.m_ld = t.n_ld = t.K = a.H;
+  t.rows = a.M;
+  t.cols = a.I;
+  t.grad_out = a.grad_out;
+  t.out = d;
+  t.out_ld = 2 * a.I;
+  hipError_t err = launch_tiles<kGradAct>(t, 2 * a.I, plan_of(a.M, 2 * a.I, a.H, false), s);
+  if (err == hipSuccess && a.grad_x != nullptr) {
+    TileArgs g{};
+    g.m_side = d;
+    g.n_side = a.w13;
+    g.m_ld = g.K = 2 * a.I;
+    g.n_ld = g.cols = g.out_ld = a.H;
+    g.rows = a.M;
+    g.out = a.grad_x;
+    g.partial = partial;
+    err = launch_tiles<kGradX>(g, a.H, plan_of(a.M, a.H, 2 * a.I, true), s);
+  }
+  if (err == hipSuccess && a.grad_w13 != nullptr) {
+    TileArgs g{};
+    g.m_side = d;
+    g.n_side = a.x;
+    g.m_ld = g.rows = 2 * a.I;
+    g.n_ld = g.cols = g.out_ld = a.H;
+    g.K = a.M;
+    g.out = a.grad_w13;
+    g.partial = partial;
+    err = launch_tiles<kGradW>(g, a.H, plan_of(2 * a.I, a.H, a.M, true), s);
+  }
+  return err;
+}
+
+}  // namespace moe_host

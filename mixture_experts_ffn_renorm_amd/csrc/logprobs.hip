@@ -9,6 +9,8 @@
 // of the type's lowest value (a mask) is as exact as any other; sums are fp32,
 // of one register's logits first, then of lanes, waves and chunks in a fixed
 // order (bitwise repeatable).
+#include <algorithm>
+
 #include "dense.h"
 
 using namespace moe;
@@ -20,6 +22,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMaxChunks = 64;      // the join keeps one chunk's list per lane
+constexpr int kFill = 512;          // workgroups that fill the chip
 constexpr int kMaxCand = 512;       // candidates of a chunk that are ranked in LDS
 
 typedef unsigned long long u64;
@@ -312,7 +315,7 @@ int chunks_of(int V, int bf16, int loads) {
 // smaller chunks, so that more CUs read.
 int loads_of(int M, int V, int bf16) {
   int loads = 8;
-  while (loads > 1 && (long long)M * chunks_of(V, bf16, loads) < 512 &&
+  while (loads > 1 && (long long)M * chunks_of(V, bf16, loads) < kFill &&
          chunks_of(V, bf16, loads / 2) <= kMaxChunks)
     loads /= 2;
   return loads;
@@ -396,7 +399,9 @@ __global__ __launch_bounds__(256) void logprob_backward_kernel(moe_host::Logprob
 namespace moe_host {
 
 size_t logprob_partial_bytes(int M, int V, int top, int bf16) {
-  return (size_t)M * chunks_of(V, bf16, loads_of(M, V, bf16)) * partial_stride(top);
+  // halved chunks are fewer than 2 * kFill; so sized, a workspace serves fewer
+  // rows as well
+  return std::max<size_t>((size_t)M * chunks_of(V, bf16, 8), 2 * kFill) * partial_stride(top);
 }
 
 hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t s) {

@@ -52,3 +52,19 @@ def token_logprobs_backward(logits, tokens, lse, entropy, g, h) -> np.ndarray:
         if gm:
             out[m, tokens[m]] += gm
     return out
+
+
+def gated(x: np.ndarray, w13: np.ndarray) -> np.ndarray:
+    """x [M, H], w13 [2I, H], float64."""
+    I = w13.shape[0] // 2
+    g, u = x @ w13[:I].T, x @ w13[I:].T
+    return g / (1.0 + np.exp(-g)) * u
+
+
+def gated_backward(x, w13, d):
+    """(grad_x, grad_w13) for the gradient d [M, I] of gated's output."""
+    I = w13.shape[0] // 2
+    g, u = x @ w13[:I].T, x @ w13[I:].T
+    s = 1.0 / (1.0 + np.exp(-g))
+    both = np.concatenate([d * u * (s + g * s * (1.0 - s)), d * g * s], axis=1)
+    return both @ w13, both.T @ x

@@ -593,6 +593,51 @@ int moe_linear_gated_backward(const uint16_t* x, const uint16_t* w13, const uint
                               int M, int H, int I, uint16_t* grad_x, uint16_t* grad_w13,
                               void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * Low-rank adapters that are loaded side by side (host struct of device
+ * pointers, a and b 16-byte aligned): adapter s adds
+ * scales[s] (x A_s^T) B_s^T to a projection's output.
+ */
+typedef struct moe_adapters {
+  int count;                 /* S adapters, at most 4096            */
+  int rank;                  /* R, a multiple of 8, at most 128; a smaller
+                                adapter's rows are filled with zeros */
+  const uint16_t* a;         /* [S, R, K] bf16                      */
+  const uint16_t* b;         /* [S, N, R] bf16                      */
+  const float* scales;       /* [S] fp32, or NULL (1)               */
+} moe_adapters;
+
+/* Bytes of workspace of moe_linear_adapters for any batch of at most M rows,
+ * any N and any number of adapters (0: unsupported sizes). */
+size_t moe_linear_adapters_workspace_size(int M, int K, int R);
+
+/*
+ * moe_linear_adapters -- the adapters of many requests at once, beside a
+ * shared projection (moe_linear_quantized without `gated`, or any other),
+ * whose output is the addend.
+ *
+ *   s = slots[m]
+ *   y[m, :] = addend[m, :] + scales[s] (x[m] A_s^T) B_s^T      0 <= s < S
+ *   y[m, :] = addend[m, :]                                     any other s
+ *   gated 0: out = bf16(y), [M, N]
+ *   gated 1: out[m, i] = bf16(SiLU(y[m, i]) * y[m, N/2 + i]), [M, N/2] (gate
+ *            rows first, as in W13)
+ *
+ *   x      [M, K] bf16, the projection's input
+ *   slots  [M] int32: each row's adapter, in any order; -1: none
+ *   addend [M, N] bf16 or NULL (0); out itself (gated 0), to add in place
+ *   out    bf16 out, overlapping no input but an addend that is out itself
+ *   workspace  moe_linear_adapters_workspace_size(M, K, R) bytes, 16-byte
+ *          aligned, overlapping no operand
+ * Two launches, three above 64 rows (rows are grouped by adapter there).  K and N multiples
+ * of 8 (gated: N of 16), at most 2^17; M < 2^21.  Sums are fp32; x A^T keeps
+ * at least 16 bits between the two products.  A row's result depends on no
+ * other row.
+ */
+int moe_linear_adapters(const uint16_t* x, const moe_adapters* adapters, const int32_t* slots,
+                        int M, int K, int N, int gated, const uint16_t* addend, uint16_t* out,
+                        void* workspace, size_t ws_bytes, void* stream);
+
 /* Bytes of workspace of moe_token_logprobs for any batch of at most M rows
  * (0: unsupported sizes). */
 size_t moe_token_logprobs_workspace_size(int logits_fp32, int M, int V, int top);

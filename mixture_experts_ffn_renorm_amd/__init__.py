@@ -13,8 +13,9 @@ moe_workspace_size, moe_mx_workspace_size, moe_pick_block_m,
 moe_forward_list_offsets and moe_strerror; and, with a :class:`Routing` rule,
 moe_select, moe_select_backward, moe_route_scored, moe_forward_scored,
 moe_forward_quantized_scored and moe_forward_mxfp8_scored;
-moe_linear_quantized; moe_linear_gated and moe_token_logprobs with their
-gradients moe_linear_gated_backward and moe_token_logprobs_backward.
+moe_linear_quantized and moe_linear_adapters; moe_linear_gated and
+moe_token_logprobs with their gradients moe_linear_gated_backward and
+moe_token_logprobs_backward.
 """
 
 from __future__ import annotations
@@ -90,7 +91,14 @@ class QuantizedMatrix(ctypes.Structure):
                 ("scales", _c_void_p), ("biases", _c_void_p)]
 
 
+class Adapters(ctypes.Structure):
+    """moe_adapters: count, rank and three device pointers."""
+    _fields_ = [("count", _c_int), ("rank", _c_int), ("a", _c_void_p), ("b", _c_void_p),
+                ("scales", _c_void_p)]
+
+
 # the same struct as bytes, which a call takes in a third of the time
+# (moe_adapters has the same layout)
 _pack_matrix = struct.Struct("@iiPPP").pack
 
 
@@ -142,6 +150,9 @@ _SIGNATURES = {
     "moe_linear_gated_backward_workspace_size": (_c_size_t, [_c_int] * 3),
     "moe_linear_gated_backward": (_c_int, [_c_void_p] * 3 + [_c_int] * 3 + [_c_void_p] * 3 +
                                   [_c_size_t, _c_void_p]),
+    "moe_linear_adapters_workspace_size": (_c_size_t, [_c_int] * 3),
+    "moe_linear_adapters": (_c_int, [_c_void_p] * 3 + [_c_int] * 4 + [_c_void_p] * 3 +
+                            [_c_size_t, _c_void_p]),
     "moe_token_logprobs_workspace_size": (_c_size_t, [_c_int] * 4),
     "moe_token_logprobs": (_c_int, [_c_void_p, _c_int, _c_void_p] + [_c_int] * 3 +
                            [_c_void_p] * 6 + [_c_size_t, _c_void_p]),
@@ -1046,6 +1057,73 @@ def moe_linear_gated_backward(x, w13, grad_out, grad_x=None, grad_w13=None, need
     if st:
         _raise("moe_linear_gated_backward", st)
     return tuple(outs)
+
+
+# ---------------------------------------------------------------------------
+# low-rank adapters
+# ---------------------------------------------------------------------------
+
+def moe_linear_adapters_workspace_size(M: int, K: int, R: int) -> int:
+    """Workspace bytes of moe_linear_adapters (0: unsupported sizes)."""
+    if max(M, K, R) >= _INT_END:
+        return 0
+    return int(library().moe_linear_adapters_workspace_size(M, K, R))
+
+
+def linear_adapters_workspace(M: int, K: int, R: int, device=None):
+    """Workspace tensor (uint8) for moe_linear_adapters calls of at most M rows
+    with adapters of rank R."""
+    n = moe_linear_adapters_workspace_size(M, K, R)
+    if n == 0:
+        raise MoeError("moe_linear_adapters_workspace_size", -2)
+    return _torch().empty(n, dtype=_torch().uint8, device=device or "cuda")
+
+
+def moe_linear_adapters(x, adapters: dict, slots, gated: bool = False, addend=None, out=None,
+                        ws=None, stream=None):
+    """Low-rank adapters of many requests beside a shared projection:
+    y = addend + scales[s] (x A_s^T) B_s^T with s = slots[m], per row of x
+    [M, K] bf16.  ``adapters`` holds ``a`` [S, R, K] and ``b`` [S, N, R] (bf16)
+    and ``scales`` [S] fp32 or None (1); ``slots`` [M] int32 gives each row's
+    adapter, in any order, and any number outside [0, S) none.  ``addend``
+    [M, N] bf16 is the shared projection's output, or None (0).  Returns out =
+    y [M, N], or with ``gated`` SiLU(first half) * second half [M, N/2], bf16;
+    ``out`` may be ``addend`` (not gated), and overlaps nothing else.  R is a
+    multiple of 8 up to 128, K and N of 8 (gated: N of 16)."""
+    torch = _torch()
+    M, K = x.shape
+    a, b, scales = adapters["a"], adapters["b"], adapters.get("scales")
+    S, R, _ = a.shape
+    N = b.shape[1]
+    if max(M, K, S, R, N) >= _INT_END:
+        raise MoeError("moe_linear_adapters", -2)
+    dev = x.get_device()
+    if not _current(dev):
+        return _elsewhere(dev, moe_linear_adapters, x, adapters, slots, gated, addend, out, ws,
+                          stream)
+    bf16 = torch.bfloat16
+    shape = (M, N // 2 if gated else N)
+    _need(x, "x", bf16, (M, K), dev)
+    _need(a, "a", bf16, (S, R, K), dev)
+    _need(b, "b", bf16, (S, N, R), dev)
+    if scales is not None:
+        _need(scales, "scales", torch.float32, (S,), dev)
+    _need(slots, "slots", torch.int32, (M,), dev)
+    if addend is not None:
+        _need(addend, "addend", bf16, (M, N), dev)
+    if out is None:
+        out = _empty(shape, bf16, dev, stream)
+    else:
+        _need(out, "out", bf16, shape, dev)
+    need = library().moe_linear_adapters_workspace_size(M, K, R)
+    ws = _workspace_of("moe_linear_adapters", need, ws, dev, stream)
+    w = _pack_matrix(S, R, a.data_ptr(), b.data_ptr(), 0 if scales is None else scales.data_ptr())
+    st = library().moe_linear_adapters(x.data_ptr(), w, slots.data_ptr(), M, K, N,
+                                       1 if gated else 0, _ptr(addend), out.data_ptr(),
+                                       ws.data_ptr(), ws.numel(), _raw_stream(dev, stream))
+    if st:
+        _raise("moe_linear_adapters", st)
+    return out
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,435 @@
+// Low-rank adapters of many requests beside a shared projection:
+//   y[m] = addend[m] + scale[s] (x[m] A_s^T) B_s^T,   s = slots[m]
+//   out = bf16(y), or with `gated` SiLU(first half of y) * second half
+// A_s [R, K], B_s [N, R]; a token whose slot is outside [0, S) has no adapter.
+//
+// Two steps, t = scale (x A^T) and y = addend + t B^T.  Few tokens: each reads
+// its adapter by itself (GEMVs, t in fp32).  More: tokens are grouped by slot
+// first (a counting sort; the groups' order does not reach any sum), 64 to a
+// unit, and both steps run on the matrix cores; t is kept as the sum of two
+// bf16 numbers, so that it loses less than 2^-16 of itself.
+#include <algorithm>
+
+#include "dense.h"
+
+using namespace moe;
+using moe_host::AdapterArgs;
+
+namespace {
+
+constexpr int kUnit = 64;              // tokens of a unit at most
+constexpr int kWindow = 8192;          // tokens that one workgroup groups
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanTokens = kWindow / kPlanThreads;
+constexpr int kMaxSlots = 4096;
+
+struct Unit {
+  int slot;      // S: no adapter
+  int start;     // place of the first token in the order by slot
+  int count;     // tokens; 0: no unit
+  int pad;
+};
+
+__device__ __forceinline__ float bf16_at(const uint16_t* p) {
+  return __uint_as_float((uint32_t)*p << 16);
+}
+
+// ---- few tokens ----
+
+// t[m, r] = scale x[m] . A_s[r]: one wave for kR rows of A_s
+template <int kR>
+__global__ __launch_bounds__(256) void shrink_gemv_kernel(AdapterArgs a, float* __restrict__ t) {
+  const int lane = threadIdx.x & 63;
+  const int groups = a.R / kR;
+  const int w = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  const int m = w / groups, r0 = w % groups * kR;
+  if (m >= a.M) return;
+  const int s = a.slots[m];
+  if (s < 0 || s >= a.S) return;
+  const uint16_t* x = a.x + (size_t)m * a.K;
+  const uint16_t* A = a.a + ((size_t)s * a.R + r0) * a.K;
+  float sum[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) sum[r] = 0.f;
+#pragma unroll 4
+  for (int k = lane * 8; k < a.K; k += 512) {
+    const u32x4 xv = load16(x + k);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const u32x4 av = load16(A + (size_t)r * a.K + k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[r] = __builtin_fmaf(bf16_lo(xv[j]), bf16_lo(av[j]), sum[r]);
+        sum[r] = __builtin_fmaf(bf16_hi(xv[j]), bf16_hi(av[j]), sum[r]);
+      }
+    }
+  }
+  const float scale = a.scales != nullptr ? a.scales[s] : 1.f;
+#pragma unroll
+  for (int r = 0; r < kR; ++r) {
+    const float v = wave_sum(sum[r]);
+    if (lane == 0) t[(size_t)m * a.R + r0 + r] = v * scale;
+  }
+}
+
+// y of one token, one column a thread
+template <bool kGated>
+__global__ __launch_bounds__(256) void expand_gemv_kernel(AdapterArgs a,
+                                                          const float* __restrict__ t) {
+  const int n_out = kGated ? a.N / 2 : a.N;
+  const int m = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= n_out) return;
+  const int s = a.slots[m];
+  float y[2] = {0.f, 0.f};
+  if (s >= 0 && s < a.S) {
+    const float* tm = t + (size_t)m * a.R;
+#pragma unroll
+    for (int h = 0; h < (kGated ? 2 : 1); ++h) {
+      const uint16_t* b = a.b + ((size_t)s * a.N + n + h * n_out) * a.R;
+#pragma unroll 4
+      for (int r = 0; r < a.R; r += 8) {
+        const u32x4 v = load16(b + r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          y[h] = __builtin_fmaf(tm[r + 2 * j], bf16_lo(v[j]), y[h]);
+          y[h] = __builtin_fmaf(tm[r + 2 * j + 1], bf16_hi(v[j]), y[h]);
+        }
+      }
+    }
+  }
+  if (a.addend != nullptr) {
+    const uint16_t* p = a.addend + (size_t)m * a.N + n;
+    y[0] += bf16_at(p);
+    if (kGated) y[1] += bf16_at(p + n_out);
+  }
+  a.out[(size_t)m * n_out + n] = (uint16_t)f32_to_bf16(kGated ? silu_mul(y[0], y[1]) : y[0]);
+}
+
+// ---- tokens grouped by slot ----
+
+__device__ __forceinline__ int wave_scan(int v, int lane) {   // inclusive
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d, kWave);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// Window blockIdx.x of kWindow tokens: order[place] = token, by slot, and the
+// window's units (`cap` records, the last ones empty).
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(AdapterArgs a, int* __restrict__ order,
+                                                            Unit* __restrict__ units, int cap) {
+  __shared__ int s_count[kMaxSlots + 1], s_place[kMaxSlots + 1];
+  __shared__ int s_wave[2][kPlanThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int base = blockIdx.x * kWindow, here = min(kWindow, a.M - base);
+  const int bins = a.S + 1;
+  for (int i = tid; i < bins; i += kPlanThreads) s_count[i] = 0;
+  __syncthreads();
+  int slot[kPlanTokens], rank[kPlanTokens];
+#pragma unroll
+  for (int i = 0; i < kPlanTokens; ++i) {
+    const int at = i * kPlanThreads + tid;
+    slot[i] = -1;
+    if (at < here) {
+      const int s = a.slots[base + at];
+      slot[i] = s < 0 || s >= a.S ? a.S : s;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPlanTokens; ++i) {
+    rank[i] = 0;
+    if (i * kPlanThreads >= here) break;
+    const int first = __builtin_amdgcn_readfirstlane(slot[i]);
+    if (__ballot(slot[i] == first) == ~0ull && first >= 0) {
+      int old = 0;
+      if (lane == 0) old = atomicAdd(&s_count[first], 64);
+      rank[i] = __builtin_amdgcn_readfirstlane(old) + lane;
+    } else if (slot[i] >= 0) {
+      rank[i] = atomicAdd(&s_count[slot[i]], 1);
+    }
+  }
+  __syncthreads();
+  // exclusive sums over the bins of tokens and units; a thread has `per` bins
+  const int per = (bins + kPlanThreads - 1) / kPlanThreads;
+  int tokens = 0, unit = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    const int c = b < bins ? s_count[b] : 0;
+    tokens += c;
+    unit += (c + kUnit - 1) / kUnit;
+  }
+  const int in_t = wave_scan(tokens, lane), in_u = wave_scan(unit, lane);
+  if (lane == 63) {
+    s_wave[0][wave] = in_t;
+    s_wave[1][wave] = in_u;
+  }
+  __syncthreads();
+  int t0 = in_t - tokens, u0 = in_u - unit, total = 0;
+  for (int i = 0; i < kPlanThreads / 64; ++i) {
+    if (i < wave) {
+      t0 += s_wave[0][i];
+      u0 += s_wave[1][i];
+    }
+    total += s_wave[1][i];
+  }
+  units += (size_t)blockIdx.x * cap;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b >= bins) break;
+    const int c = s_count[b];
+    s_place[b] = t0;
+    for (int q = 0; q < c; q += kUnit) units[u0++] = Unit{b, base + t0 + q, min(kUnit, c - q), 0};
+    t0 += c;
+  }
+  for (int i = total + tid; i < cap; i += kPlanThreads) units[i] = Unit{0, 0, 0, 0};
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPlanTokens; ++i)
+    if (slot[i] >= 0) order[base + s_place[slot[i]] + rank[i]] = base + i * kPlanThreads + tid;
+}
+
+// t of 16 tokens of a unit (blockIdx.x: unit, quarter): eight waves, an eighth
+// of K each, summed through LDS in wave order.  t[place] holds R high parts,
+// then R low parts.
+template <int FR>
+__global__ __launch_bounds__(512) void shrink_kernel(AdapterArgs a, const int* __restrict__ order,
+                                                     const Unit* __restrict__ units,
+                                                     uint16_t* __restrict__ t) {
+  __shared__ f32x4 red[8][FR][64];
+  const Unit u = units[blockIdx.x >> 2];
+  const int q = (blockIdx.x & 3) * 16, n = u.count - q;
+  if (n <= 0 || u.slot >= a.S) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int m = order[u.start + q + min(i, n - 1)];
+  const int steps = ceil_div(a.K, 32), per = ceil_div(steps, 8);
+  const int first = wave * per, last = min(steps, first + per);
+  const uint16_t* x = a.x + (size_t)m * a.K + 8 * g;
+  const uint16_t* A[FR];
+#pragma unroll
+  for (int f = 0; f < FR; ++f)
+    A[f] = a.a + ((size_t)u.slot * a.R + min(f * 16 + i, a.R - 1)) * a.K + 8 * g;
+  f32x4 acc[FR];
+#pragma unroll
+  for (int f = 0; f < FR; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int whole = min(last, a.K / 32);
+#pragma unroll 4
+  for (int k = first; k < whole; ++k) {
+    const u32x4 xv = load16(x + k * 32);
+#pragma unroll
+    for (int f = 0; f < FR; ++f) acc[f] = mfma_16x16x32(load16(A[f] + k * 32), xv, acc[f]);
+  }
+  if (first < last && whole < last) {            // K ends inside the step
+    const bool ok = whole * 32 + 8 * g < a.K;
+    const u32x4 xv = load16_or_zero(x + whole * 32, ok);
+#pragma unroll
+    for (int f = 0; f < FR; ++f)
+      acc[f] = mfma_16x16x32(load16_or_zero(A[f] + whole * 32, ok), xv, acc[f]);
+  }
+#pragma unroll
+  for (int f = 0; f < FR; ++f) red[wave][f][lane] = acc[f];
+  __syncthreads();
+  const float scale = a.scales != nullptr ? a.scales[u.slot] : 1.f;
+  for (int e = threadIdx.x; e < FR * 64; e += 512) {
+    const int f = e >> 6, l = e & 63;
+    const int r = f * 16 + 4 * (l >> 4), tok = l & 15;
+    f32x4 v = red[0][f][l];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) v += red[w][f][l];
+    if (tok >= n || r >= a.R) continue;
+    float hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float y = v[j] * scale;
+      hi[j] = __uint_as_float(f32_to_bf16(y) << 16);
+      // not finite: the low part is 0
+      lo[j] = __builtin_fabsf(hi[j]) < INFINITY ? y - hi[j] : 0.f;
+    }
+    uint16_t* p = t + (size_t)(u.start + q + tok) * 2 * a.R + r;
+    *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
+    *reinterpret_cast<u32x2*>(p + a.R) =
+        u32x2{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3])};
+  }
+}
+
+constexpr int kExpandCols = 64;        // output columns of a wave
+constexpr int kExpandWaves = 4;
+
+// y of a unit: a wave takes kExpandCols columns of all its tokens.  The rows
+// of two fragments of B are dealt so that a lane holds 8 consecutive columns.
+template <int FK, bool kGated>
+__global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(
+    AdapterArgs a, const int* __restrict__ order, const Unit* __restrict__ units,
+    const uint16_t* __restrict__ t) {
+  constexpr int kHalves = kGated ? 2 : 1;
+  const Unit u = units[blockIdx.x];
+  if (u.count == 0) return;
+  const bool none = u.slot >= a.S;
+  const int n_out = kGated ? a.N / 2 : a.N;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int n0 = (blockIdx.y * kExpandWaves + wave) * kExpandCols;
+  if (n0 >= n_out || (none && !kGated && a.addend == a.out)) return;
+  const int frags = ceil_div(u.count, 16);
+  int m[4];
+  u32x4 hi[4][FK], lo[4][FK];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int at = u.start + min(16 * j + i, u.count - 1);
+    m[j] = order[at];
+    const uint16_t* p = t + (size_t)at * 2 * a.R;
+#pragma unroll
+    for (int k = 0; k < FK; ++k) {
+      const int r = 32 * k + 8 * g;
+      const bool ok = !none && j < frags && r < a.R;
+      hi[j][k] = load16_or_zero(p + r, ok);
+      lo[j][k] = load16_or_zero(p + a.R + r, ok);
+    }
+  }
+#pragma unroll 1
+  for (int c = n0; c < min(n0 + kExpandCols, n_out); c += 32) {
+    // row i of fragment f: column 8 (i / 4) + 4 f + i % 4
+    u32x4 b[kHalves][2][FK];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int n = min(c + 8 * (i >> 2) + 4 * f + (i & 3), n_out - 1) + h * n_out;
+        const uint16_t* p = a.b + ((size_t)(none ? 0 : u.slot) * a.N + n) * a.R;
+#pragma unroll
+        for (int k = 0; k < FK; ++k) {
+          const int r = 32 * k + 8 * g;
+          b[h][f][k] = load16_or_zero(p + r, !none && r < a.R);
+        }
+      }
+    const int n = c + 8 * g;
+    u32x4 add[4][kHalves];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+        add[j][h] = load16_or_zero(a.addend + (size_t)m[j] * a.N + h * n_out + n,
+                                   a.addend != nullptr && j < frags && n < n_out);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j >= frags) break;
+      f32x4 acc[kHalves][2];
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          acc[h][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+          // the smaller terms first
+#pragma unroll
+          for (int k = 0; k < FK; ++k) acc[h][f] = mfma_16x16x32(b[h][f][k], lo[j][k], acc[h][f]);
+#pragma unroll
+          for (int k = 0; k < FK; ++k) acc[h][f] = mfma_16x16x32(b[h][f][k], hi[j][k], acc[h][f]);
+        }
+      if (16 * j + i >= u.count || n >= n_out) continue;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        auto at = [&](int h) {
+          const uint32_t w = add[j][h][e >> 1];
+          return acc[h][e >> 2][e & 3] + (e & 1 ? bf16_hi(w) : bf16_lo(w));
+        };
+        y[e] = kGated ? silu_mul(at(0), at(kHalves - 1)) : at(0);
+      }
+      *reinterpret_cast<u32x4*>(a.out + (size_t)m[j] * n_out + n) =
+          u32x4{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                pack_bf16x2(y[6], y[7])};
+    }
+  }
+}
+
+using moe_host::ceil_div_host;
+
+// Tokens up to which each reads its adapter by itself.
+constexpr int kGemvTokens = 64;
+
+struct Layout {
+  int windows, cap;        // of the grouping; units of a window
+  size_t order, units, t, total;
+};
+Layout layout_of(int M, int R, int S) {
+  Layout l;
+  l.windows = ceil_div_host(M, kWindow);
+  const int w = std::min(M, kWindow);
+  l.cap = w / kUnit + std::min(S + 1, w);
+  auto align = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  l.t = 0;
+  l.order = align((size_t)M * R * 4);
+  l.units = l.order + align((size_t)M * 4);
+  l.total = l.units + align((size_t)l.windows * l.cap * sizeof(Unit));
+  return l;
+}
+
+template <int FR>
+void launch_shrink(const AdapterArgs& a, const Layout& l, const int* order, const Unit* units,
+                   uint16_t* t, hipStream_t s) {
+  shrink_kernel<FR><<<l.windows * l.cap * 4, 512, 0, s>>>(a, order, units, t);
+}
+template <int FK, bool kGated>
+void launch_expand(const AdapterArgs& a, const Layout& l, const int* order, const Unit* units,
+                   const uint16_t* t, hipStream_t s) {
+  const dim3 grid((unsigned)(l.windows * l.cap),
+                  (unsigned)ceil_div_host(kGated ? a.N / 2 : a.N, kExpandCols * kExpandWaves));
+  expand_kernel<FK, kGated><<<grid, 64 * kExpandWaves, 0, s>>>(a, order, units, t);
+}
+
+}  // namespace
+
+namespace moe_host {
+
+size_t adapters_bytes(int M, int R) {
+  // any number of adapters up to the most
+  return layout_of(M, R, kMaxSlots).total;
+}
+
+hipError_t launch_adapters(const AdapterArgs& a, hipStream_t s) {
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const Layout l = layout_of(a.M, a.R, a.S);
+  if (a.M <= kGemvTokens) {
+    float* t = reinterpret_cast<float*>(ws + l.t);
+    const int n_out = a.gated ? a.N / 2 : a.N;
+    const dim3 grid((unsigned)ceil_div_host(n_out, 256), (unsigned)a.M);
+    shrink_gemv_kernel<2><<<ceil_div_host(a.M * (a.R / 2), 4), 256, 0, s>>>(a, t);
+    if (a.gated)
+      expand_gemv_kernel<true><<<grid, 256, 0, s>>>(a, t);
+    else
+      expand_gemv_kernel<false><<<grid, 256, 0, s>>>(a, t);
+    return hipGetLastError();
+  }
+  int* order = reinterpret_cast<int*>(ws + l.order);
+  Unit* units = reinterpret_cast<Unit*>(ws + l.units);
+  uint16_t* t = reinterpret_cast<uint16_t*>(ws + l.t);
+  plan_kernel<<<l.windows, kPlanThreads, 0, s>>>(a, order, units, l.cap);
+  if (a.R <= 16)
+    launch_shrink<1>(a, l, order, units, t, s);
+  else if (a.R <= 32)
+    launch_shrink<2>(a, l, order, units, t, s);
+  else if (a.R <= 64)
+    launch_shrink<4>(a, l, order, units, t, s);
+  else
+    launch_shrink<8>(a, l, order, units, t, s);
+  if (a.gated) {
+    if (a.R <= 32)
+      launch_expand<1, true>(a, l, order, units, t, s);
+    else if (a.R <= 64)
+      launch_expand<2, true>(a, l, order, units, t, s);
+    else
+      launch_expand<4, true>(a, l, order, units, t, s);
+  } else {
+    if (a.R <= 32)
+      launch_expand<1, false>(a, l, order, units, t, s);
+    else if (a.R <= 64)
+      launch_expand<2, false>(a, l, order, units, t, s);
+    else
+      launch_expand<4, false>(a, l, order, units, t, s);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace moe_host

@@ -58,6 +58,21 @@ struct GatedGradArgs {
 size_t gated_backward_bytes(int M, int H, int I);
 hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s);
 
+// Low-rank adapters: out = f(addend + scale[s] (x A_s^T) B_s^T), s = slots[m].
+struct AdapterArgs {
+  const uint16_t* x;         // [M, K]
+  const uint16_t* a;         // [S, R, K]
+  const uint16_t* b;         // [S, N, R]
+  const float* scales;       // [S] or null
+  const int32_t* slots;      // [M]
+  int M, K, N, R, S, gated;
+  const uint16_t* addend;    // [M, N] or null; may be out (not gated)
+  uint16_t* out;             // [M, N], gated [M, N / 2]
+  void* workspace;           // adapters_bytes
+};
+size_t adapters_bytes(int M, int R);
+hipError_t launch_adapters(const AdapterArgs& a, hipStream_t s);
+
 // bytes (a multiple of 16) of zeros
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t s);
 

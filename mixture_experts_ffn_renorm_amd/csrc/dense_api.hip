@@ -43,6 +43,8 @@ constexpr int kMaxLogitRows = 1 << 21;
 constexpr long long kMaxLogits = 1LL << 35;
 constexpr int kMaxAlternatives = 32;
 constexpr int kMaxRows = 1 << 21;
+constexpr int kMaxRank = 128;
+constexpr int kMaxAdapters = 4096;
 constexpr int kMaxFeatures = 1 << 17;
 
 int check_logits(int logits_fp32, int M, int V) {
@@ -60,9 +62,52 @@ int check_gated(int M, int H, int I) {
   return MOE_OK;
 }
 
+// Sizes of the adapters' products.
+int check_adapters(int M, int K, int R) {
+  if (M < 0 || K <= 0 || R <= 0) return MOE_ERR_INVALID_ARG;
+  if (K % 8 != 0 || R % 8 != 0 || R > kMaxRank || K > kMaxFeatures || M >= kMaxRows)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t moe_linear_adapters_workspace_size(int M, int K, int R) {
+  if (check_adapters(M, K, R) != MOE_OK) return 0;
+  return adapters_bytes(M > 0 ? M : 1, R);
+}
+
+int moe_linear_adapters(const uint16_t* x, const moe_adapters* adapters, const int32_t* slots,
+                        int M, int K, int N, int gated, const uint16_t* addend, uint16_t* out,
+                        void* workspace, size_t ws_bytes, void* stream) {
+  if (adapters == nullptr || N <= 0 || (gated != 0 && gated != 1)) return MOE_ERR_INVALID_ARG;
+  const moe_adapters& w = *adapters;
+  const int st = check_adapters(M, K, w.rank);
+  if (st != MOE_OK) return st;
+  if (w.count <= 0) return MOE_ERR_INVALID_ARG;
+  if (N % (gated ? 16 : 8) != 0 || N > kMaxFeatures || w.count > kMaxAdapters)
+    return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!x || !w.a || !w.b || !slots || !out) return MOE_ERR_INVALID_ARG;
+  if (!a16(x) || !a16(w.a) || !a16(w.b) || !a16(out) || !a16(addend) || !a16(workspace))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = adapters_bytes(M, w.rank);
+  if (workspace == nullptr || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  // addend may be out itself: each output is read where it is written
+  const bool in_place = addend == out && !gated;
+  const size_t S = w.count, R = w.rank;
+  if (clash({{out, (size_t)M * (gated ? N / 2 : N) * 2}, {workspace, need}},
+            {{x, (size_t)M * K * 2}, {w.a, S * R * K * 2}, {w.b, S * R * N * 2},
+             {w.scales, S * 4}, {slots, (size_t)M * 4},
+             {in_place ? nullptr : addend, (size_t)M * N * 2}}))
+    return MOE_ERR_INVALID_ARG;
+  const AdapterArgs a{x, w.a, w.b, w.scales, slots, M, K, N, w.rank, w.count, gated, addend, out,
+                      workspace};
+  MOE_TRY_LAUNCH(launch_adapters(a, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
 
 int moe_linear_gated(const uint16_t* x, const uint16_t* w13, int M, int H, int I, uint16_t* out,
                      void* stream) {

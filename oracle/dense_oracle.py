@@ -68,3 +68,17 @@ def gated_backward(x, w13, d):
     s = 1.0 / (1.0 + np.exp(-g))
     both = np.concatenate([d * u * (s + g * s * (1.0 - s)), d * g * s], axis=1)
     return both @ w13, both.T @ x
+
+
+def adapters(x, a, b, scales, slots, addend=None, is_gated=False):
+    """x [M, K], a [S, R, K], b [S, N, R], scales [S] or None, float64."""
+    S = a.shape[0]
+    y = np.zeros((x.shape[0], b.shape[1])) if addend is None else addend.astype(np.float64)
+    y = y.copy()
+    for m, s in enumerate(slots):
+        if 0 <= s < S:
+            y[m] += (1.0 if scales is None else float(scales[s])) * (b[s] @ (a[s] @ x[m]))
+    if is_gated:
+        n = y.shape[1] // 2
+        y = y[:, :n] / (1.0 + np.exp(-y[:, :n])) * y[:, n:]
+    return y

@@ -20,7 +20,7 @@ struct LogprobArgs {
   float* top_logprobs;       // [M, top]
   void* partial;             // logprob_partial_bytes
 };
-size_t logprob_partial_bytes(int M, int V, int top, int bf16);
+size_t logprob_partial_bytes(int top);
 hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t s);
 
 struct LogprobGradArgs {

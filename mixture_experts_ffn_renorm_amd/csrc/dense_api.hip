@@ -155,8 +155,7 @@ int moe_linear_gated_backward(const uint16_t* x, const uint16_t* w13, const uint
 size_t moe_token_logprobs_workspace_size(int logits_fp32, int M, int V, int top) {
   if (check_logits(logits_fp32, M, V) != MOE_OK || top < 0 || top > kMaxAlternatives || top > V)
     return 0;
-  const size_t n = logprob_partial_bytes(M, V, top, !logits_fp32);
-  return n > 16 ? n : 16;
+  return logprob_partial_bytes(top);
 }
 
 int moe_token_logprobs(const void* logits, int logits_fp32, const int32_t* tokens, int M, int V,
@@ -170,7 +169,7 @@ int moe_token_logprobs(const void* logits, int logits_fp32, const int32_t* token
   if (!logits || !tokens || !logprobs || !entropy || !lse || (top > 0 && (!top_ids || !top_logprobs)))
     return MOE_ERR_INVALID_ARG;
   if (!a16(logits) || !a16(workspace)) return MOE_ERR_INVALID_ARG;
-  const size_t need = logprob_partial_bytes(M, V, top, !logits_fp32);
+  const size_t need = logprob_partial_bytes(top);
   if (workspace == nullptr || ws_bytes < need) return MOE_ERR_WORKSPACE;
   const size_t row = (size_t)M * 4, alt = row * top;
   if (clash({{logprobs, row}, {entropy, row}, {lse, row}, {top > 0 ? top_ids : nullptr, alt},

@@ -5,10 +5,27 @@
 //   the `top` largest logits, in descending order, ties to the lower id
 // and the gradient of the first two with respect to the logits.
 //
-// Differences l - m are formed before anything is multiplied, so that a row
-// of the type's lowest value (a mask) is as exact as any other; sums are fp32,
-// of one register's logits first, then of lanes, waves and chunks in a fixed
-// order (bitwise repeatable).
+// One pass over the logits.  A thread keeps a running anchor (its largest
+// logit so far) and forms each exponent as one FMA, y = l log2 e - m2 with
+// m2 = fp32(m log2 e); what m2 is off by is taken back from the sums at the
+// end.  Sums are fp32: of 16 or 32 logits first, then of a thread's such
+// groups, of lanes, waves and chunks, in a fixed order (bitwise repeatable).
+// Where a chunk's largest logit lies beyond +-kFar (a mask throughout,
+// infinities) that would be too much; its sums are formed again from the
+// differences l - m.
+//
+// Alternatives: a wave collects the logits that reach a threshold in LDS.  The
+// threshold starts as the top-th largest of the lanes' first maxima (at least
+// `top` logits reach it) and rises to the top-th largest so far whenever the
+// list is cut back; a logit is looked at singly only in a 16-byte block whose
+// maximum reaches the threshold.  Lists are cut by a bitwise search for a key
+// that exactly `top` entries reach (wave ballots), equal keys by their ids.
+//
+// 2048 rows of 131072 bf16 logits: 108 us without alternatives (5.0 TB/s, what
+// a large copy reaches), 136 us with 5, 166 us with 20; one row 5.4, 14 and 20
+// us, two launches and the searches' chains.  Without a prefetch a wave takes
+// 64 registers and a SIMD holds 8 of them, which hide the loads: 136 us against
+// 143 (4 waves at the least), and 179 with the next group's loads in flight.
 #include <algorithm>
 
 #include "dense.h"
@@ -19,13 +36,25 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kThreads = 512;
+constexpr float kFar = 16777216.f;  // 2^24: fp32(m log2 e) is off by less than 2
+constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kMaxChunks = 64;      // the join keeps one chunk's list per lane
-constexpr int kFill = 512;          // workgroups that fill the chip
-constexpr int kMaxCand = 512;       // candidates of a chunk that are ranked in LDS
+constexpr int kLoads = 4;           // 16-byte blocks of a thread's group
+constexpr int kGroup = kThreads * kLoads;
+constexpr int kMaxTop = 32;
+constexpr int kMinWaves = 8;        // waves of a SIMD: 64 registers a wave
+constexpr int kMaxChunks = 64;
+constexpr int kFill = 2048;         // workgroups that fill the chip: no more chunks than that
+constexpr int kKeep = 64;           // a longer list is cut back before it takes more
+constexpr int kList = kKeep + 64;
+constexpr int kFewLanes = 6;        // that hold a hit: their logits are dealt out one lane after another
 
 typedef unsigned long long u64;
+
+constexpr uint32_t kLeastKey = 0x007fffffu;   // the order key of -inf
+
+// (ids have kIdBits bits: the low words differ in no others)
+constexpr int kIdBits = 19;
 
 // One logit's place in the order: larger logits first, then lower ids.  NaN
 // comes after -inf, 0 after everything (no logit).
@@ -37,15 +66,6 @@ __device__ __forceinline__ int id_of(u64 o) { return (int)~(uint32_t)o; }
 __device__ __forceinline__ float logit_of(u64 o) {
   const uint32_t k = (uint32_t)(o >> 32);
   return k == 1u ? __builtin_nanf("") : topk_detail::key_logit(k);
-}
-
-__device__ __forceinline__ u64 wave_max64(u64 v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const u64 o = __shfl_xor(v, d, kWave);
-    v = o > v ? o : v;
-  }
-  return v;
 }
 
 // The 16-byte blocks that a row of V elements of a dense [M, V] tensor
@@ -99,237 +119,419 @@ __device__ __forceinline__ void drop(u32x4& w, int j) {
     w[j >> 1] = j & 1 ? (w[j >> 1] & 0xFFFFu) | 0xFF800000u : (w[j >> 1] & 0xFFFF0000u) | 0xFF80u;
 }
 
+// A key that exactly n of the wave's keys reach, or, where equal keys leave
+// none, the largest that at least n reach: T, whose bits kFrom .. kTo are 0,
+// and those bits.  `reach`: how many keys reach T, then how many reach the
+// result.
+template <int kFrom, int kTo, int NB>
+__device__ __forceinline__ uint32_t nth_key(const uint32_t (&key)[NB], int n, uint32_t T,
+                                            int& reach) {
+  for (int bit = kFrom; bit >= kTo && reach != n; --bit) {
+    const uint32_t t = T | (1u << bit);
+    const int c = topk_detail::count_ge(key, t);
+    if (c >= n) {
+      T = t;
+      reach = c;
+    }
+  }
+  return T;
+}
+
+__device__ __forceinline__ void lds_order() {   // of one wave's LDS accesses
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Keeps the n largest of the wave's entries (0: none), in no order, in `to`;
+// returns how many there are.  `least`: a key that they all reach and, if
+// `strict`, that later entries (of higher ids) have to pass to replace one;
+// at most -inf's key if fewer than n are kept.
+template <bool kBf16, int NB>
+__device__ __forceinline__ int cut(const u64 (&o)[NB], u64* to, int n, uint32_t& least,
+                                   bool& strict) {
+  const int lane = threadIdx.x & 63;
+  uint32_t key[NB], low[NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    key[i] = (uint32_t)(o[i] >> 32);
+    low[i] = (uint32_t)o[i];
+  }
+  // of bf16 logits the key's upper half decides; the lower one is all 0, or
+  // all 1 below 0
+  int reach = topk_detail::count_ge(key, 1u);
+  uint32_t T = nth_key<31, kBf16 ? 16 : 0>(key, n, 0u, reach);
+  if (kBf16 && reach > n && !(T & 0x80000000u)) T |= 0xFFFFu;
+  uint32_t low_least = 0u;
+  strict = reach > n;
+  if (strict) {
+    // of the entries that equal T the lower ids, which are the larger low words
+    const int above = topk_detail::count_ge(key, T + 1u);
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      if (key[i] != T) low[i] = 0u;
+    low_least = nth_key<kIdBits - 1, 0>(low, n - above, ~0u << kIdBits, reach = NB * 64);
+  }
+  least = max(T, kLeastKey);
+  const unsigned long long below = (1ull << lane) - 1ull;
+  int at = 0;
+  lds_order();
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const bool keep = key[i] >= max(T, 1u) && (!strict || key[i] != T || low[i] >= low_least);
+    const unsigned long long m = __ballot(keep);
+    if (keep) to[at + __popcll(m & below)] = o[i];
+    at += __popcll(m);
+  }
+  lds_order();
+  return at;
+}
+
 // What a chunk of a row leaves for the row's join.
 struct Partial {
   float m;       // largest logit (NaN aside)
   float z, s;    // sums of e = 2^y and y e, y = (l - m) log2 e (m = -inf: of l)
-  float pad;
+  int count;     // alternatives that follow, in no order
 };
 __host__ __device__ inline size_t partial_stride(int top) {
   return sizeof(Partial) + (size_t)((top + 1) & ~1) * 8;
 }
 
-// ---- one chunk of a row: kThreads * kLoads blocks, held in registers ----
-template <bool kBf16, int kLoads, bool kTop>
-__global__ __launch_bounds__(kThreads) void logprob_chunk_kernel(moe_host::LogprobArgs a,
-                                                                 int chunks) {
+// A row's results, by one wave: its largest logit, sums, and the `count`
+// alternatives in LDS, in no order.
+template <bool kBf16>
+__device__ __forceinline__ void finish(const moe_host::LogprobArgs& a, int m, float M, float z,
+                                       float s, const u64* list, int count) {
+  const int lane = threadIdx.x & 63;
+  const uint16_t* l16 = static_cast<const uint16_t*>(a.logits) + (size_t)m * a.V;
+  const float* l32 = static_cast<const float*>(a.logits) + (size_t)m * a.V;
+  auto logit = [&](int v) {
+    return kBf16 ? __uint_as_float((uint32_t)l16[v] << 16) : l32[v];
+  };
+  // no logit above -inf: nothing is likely, nothing uncertain
+  const bool none = z == 0.f;
+  const float lz = logf(z);
+  auto logprob = [&](float l) { return none ? -INFINITY : l - M - lz; };
+  if (lane == 0) {
+    const int t = a.tokens[m];
+    a.logprobs[m] = t >= 0 && t < a.V ? logprob(logit(t)) : 0.f;
+    a.entropy[m] = none ? 0.f : lz - kLn2 * (s / z);
+    a.lse[m] = none ? -INFINITY : M + lz;
+  }
+  if (a.top == 0) return;
+  const size_t to = (size_t)m * a.top;
+  if (lane < count) {
+    const u64 o = list[lane];
+    int r = 0;
+    for (int i = 0; i < count; ++i) r += list[i] > o;
+    a.top_ids[to + r] = id_of(o);
+    a.top_logprobs[to + r] = logprob(logit_of(o));
+  }
+  // fewer than `top` logits are numbers: NaN follows, by id
+  const unsigned long long below = (1ull << lane) - 1ull;
+  for (int v0 = 0; v0 < a.V && count < a.top; v0 += 64) {
+    const float l = v0 + lane < a.V ? logit(v0 + lane) : 0.f;
+    const unsigned long long nan = __ballot(l != l);
+    const int at = count + __popcll(nan & below);
+    if (l != l && at < a.top) {
+      a.top_ids[to + at] = v0 + lane;
+      a.top_logprobs[to + at] = __builtin_nanf("");
+    }
+    count += __popcll(nan);
+  }
+}
+
+// ---- one chunk of a row ----
+template <bool kBf16, bool kTop>
+__global__ __launch_bounds__(kThreads, kMinWaves) void logprob_kernel(moe_host::LogprobArgs a, int chunks,
+                                                           int chunk_blocks) {
+#pragma clang fp contract(off)      // an anchor's product is the rounded one wherever it is used
   constexpr int kPer = Row<kBf16>::kPer;
-  __shared__ float s_m[kWaves], s_z[kWaves], s_s[kWaves], s_t[kWaves];
-  __shared__ u64 s_cand[kMaxCand];
-  __shared__ u64 s_best[kWaves];
-  __shared__ int s_count;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ float s_m[kWaves], s_a[kWaves], s_z[kWaves], s_s[kWaves];
+  __shared__ int s_count[kWaves];
+  __shared__ u64 s_list[kTop ? kWaves : 1][kTop ? kList : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = blockIdx.x / chunks, c = blockIdx.x % chunks;
   const Row<kBf16> row(a.logits, a.M, a.V, m);
-  const int b0 = c * kThreads * kLoads;
+  const int b0 = c * chunk_blocks, b1 = min(row.blocks, b0 + chunk_blocks);
 
-  u32x4 w[kLoads];
+  // A wave's group g: 64 kLoads consecutive blocks.  `inner`: all of them are
+  // there, whole, and not the tensor's last.
+  auto start = [&](int g) { return b0 + (g * kWaves + wave) * (64 * kLoads); };
+  auto inner = [&](int g) {
+    const int b = start(g);
+    return b + 64 * kLoads <= b1 && b + 64 * kLoads < row.blocks && (b > 0 || row.lead == 0);
+  };
+  auto load = [&](int g, u32x4 (&w)[kLoads]) {
+    const int b = start(g) + lane;
+    if (inner(g)) {
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int b = b0 + i * kThreads + tid;
-    w[i] = u32x4{0u, 0u, 0u, 0u};
-    if (b < row.blocks) w[i] = row.load(b);
-  }
-  float mx = -INFINITY;
+      for (int i = 0; i < kLoads; ++i) w[i] = load16(row.base + (size_t)(b + 64 * i) * 16);
+    } else {
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int b = b0 + i * kThreads + tid;
-    if (!row.whole(b)) {
+      for (int i = 0; i < kLoads; ++i) {
+        w[i] = u32x4{0u, 0u, 0u, 0u};
+        if (b + 64 * i < b1) w[i] = row.load(b + 64 * i);
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int e = row.first(b) + j;
-        if (e < 0 || e >= a.V) drop<kBf16>(w[i], j);
+        for (int j = 0; j < kPer; ++j) {
+          const int e = row.first(b + 64 * i) + j;
+          if (e < 0 || e >= a.V || b + 64 * i >= b1) drop<kBf16>(w[i], j);
+        }
       }
     }
+  };
+  const int groups = ceil_div(b1 - b0, kGroup);
+  float mx = -INFINITY, from = -kFar, m2 = -kFar * kLog2e, z = 0.f, s = 0.f;
+  float T = -INFINITY;
+  int count = 0;
+  u64* list = s_list[kTop ? wave : 0];
+  const unsigned long long below = (1ull << lane) - 1ull;
+  bool strict = false;
+  auto cut_back = [&] {
+    uint32_t least;
+    u64 o[kList / 64];
+    lds_order();
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) mx = fmaxf(mx, element<kBf16>(w[i], j));
-  }
-  const float wmx = wave_max(mx);
-  if (lane == 0) s_m[wave] = wmx;
-  if (kTop) {
-    // the top-th largest of the wave's lane maxima bounds the row's from below
-    const uint32_t key = topk_detail::order_key(mx);
-    const uint32_t k1[1] = {key};
-    uint32_t T = 0u;
+    for (int i = 0; i < kList / 64; ++i) o[i] = 64 * i + lane < count ? list[64 * i + lane] : 0ull;
+    count = cut<kBf16>(o, list, a.top, least, strict);
+    if (count == a.top) T = topk_detail::key_logit(least);
+  };
+  auto push = [&](bool hit, float l, int e) {
+    const unsigned long long hits = __ballot(hit);
+    if (hits == 0ull) return;
+    if (count > kKeep) cut_back();
+    if (hit) list[count + __popcll(hits & below)] = order_of(l, e);
+    count += __popcll(hits);
+  };
+#pragma unroll 1
+  for (int g = 0; g < groups; ++g) {
+    u32x4 w[kLoads];
+    load(g, w);
+    float bm[kLoads];
 #pragma unroll
-    for (int bit = 31; bit >= (kBf16 ? 16 : 0); --bit) {
-      const uint32_t t = T | (1u << bit);
-      if (topk_detail::count_ge(k1, t) >= a.top) T = t;
+    for (int i = 0; i < kLoads; ++i) {
+      bm[i] = -INFINITY;                               // NaN aside
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) bm[i] = fmaxf(bm[i], element<kBf16>(w[i], j));
     }
-    // bf16: the low 16 key bits are all 0 (positive) or all 1 (negative)
-    if (kBf16 && !(T & 0x80000000u)) T |= 0xFFFFu;
-    if (lane == 0) s_t[wave] = T >= 0x007fffffu ? topk_detail::key_logit(T) : -INFINITY;
-    if (tid == 0) s_count = 0;
+    // (widened again below: 32 fp32 registers fewer)
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) asm("" : "+v"(w[i]));
+    const float gm = fmaxf(fmaxf(bm[0], bm[1]), fmaxf(bm[2], bm[3]));
+    mx = fmaxf(mx, gm);
+    from = fmaxf(from, gm);
+    const float to = from * kLog2e, d = m2 - to, f = __builtin_amdgcn_exp2f(d);
+    m2 = to;
+    float gz = 0.f, gs = 0.f;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const float y = __builtin_fmaf(element<kBf16>(w[i], j), kLog2e, -m2);
+        const float e = __builtin_amdgcn_exp2f(y);
+        gz += e;
+        gs = __builtin_fmaf(fmaxf(y, -200.f), e, gs);   // -inf * 0 is 0 here
+      }
+    s = __builtin_fmaf(f, __builtin_fmaf(d, z, s), gs);
+    z = __builtin_fmaf(f, z, gz);
+    if (kTop) {
+      if (g == 0) {
+        const uint32_t key[1] = {topk_detail::order_key(gm)};
+        int reach = 64;
+        const uint32_t k = nth_key<31, kBf16 ? 16 : 0>(key, a.top, 0u, reach);
+        T = topk_detail::key_logit(max(k, kLeastKey));
+      }
+      if (__ballot(gm >= T) != 0ull) {
+        const bool whole = inner(g);
+#pragma unroll 1
+        for (int i = 0; i < kLoads; ++i) {
+          const float top = i == 0 ? bm[0] : i == 1 ? bm[1] : i == 2 ? bm[2] : bm[3];
+          unsigned long long lanes = __ballot(top >= T);
+          if (lanes == 0ull) continue;
+          const u32x4 v = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+          const int b = start(g) + 64 * i, e = row.first(b + lane);
+          if (whole && __popcll(lanes) <= kFewLanes) {
+            // one lane's logits at a time, dealt to the first lanes
+            const int q = kBf16 ? lane >> 1 : lane;
+            for (; lanes != 0ull; lanes &= lanes - 1ull) {
+              const int L = __builtin_ctzll(lanes);
+              uint32_t x = (uint32_t)__builtin_amdgcn_readlane((int)v[0], L);
+#pragma unroll
+              for (int k = 1; k < 4; ++k) {
+                const uint32_t y = (uint32_t)__builtin_amdgcn_readlane((int)v[k], L);
+                x = q == k ? y : x;
+              }
+              const float l =
+                  kBf16 ? (lane & 1 ? bf16_hi(x) : bf16_lo(x)) : __uint_as_float(x);
+              push(lane < kPer && l >= T, l, row.first(b + L) + lane);
+            }
+          } else {
+#pragma unroll 1
+            for (int j = 0; j < kPer; ++j) {
+              const int q = kBf16 ? j >> 1 : j;
+              const uint32_t x = q == 0 ? v[0] : q == 1 ? v[1] : q == 2 ? v[2] : v[3];
+              const float l = kBf16 ? (j & 1 ? bf16_hi(x) : bf16_lo(x)) : __uint_as_float(x);
+              push(l >= T && (whole || (b + lane < b1 && e + j >= 0 && e + j < a.V)), l, e + j);
+            }
+          }
+          // the logits of later blocks have higher ids: an equal one does not count
+          if (strict) {
+            T = topk_detail::key_logit(topk_detail::order_key(T) + 1u);
+            strict = false;
+          }
+        }
+      }
+    }
+  }
+  if (kTop) {
+    lds_order();
+    if (count > a.top) cut_back();
+    if (lane == 0) s_count[wave] = count;
+  }
+
+  const float wm = wave_max(mx), wa = wave_max(from);
+  if (lane == 0) {
+    s_m[wave] = wm;
+    s_a[wave] = wa;
   }
   __syncthreads();
-  float M = s_m[0];
+  float M = s_m[0], A = s_a[0];
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) M = fmaxf(M, s_m[i]);
-  const float from = M == -INFINITY ? 0.f : M;
-
-  float z = 0.f, s = 0.f;
+  for (int i = 1; i < kWaves; ++i) {
+    M = fmaxf(M, s_m[i]);
+    A = fmaxf(A, s_a[i]);
+  }
+  if (__builtin_fabsf(M) <= kFar || M == -INFINITY) {
+    const float M2 = A * kLog2e, d = m2 - M2, f = __builtin_amdgcn_exp2f(d);
+    s = f * __builtin_fmaf(d, z, s);
+    z = f * z;
+  } else {
+    z = s = 0.f;
+#pragma unroll 1
+    for (int g = 0; g < groups; ++g) {
+      u32x4 w[kLoads];
+      load(g, w);
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i)
+      for (int i = 0; i < kLoads; ++i)
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const float y = (element<kBf16>(w[i], j) - from) * kLog2e;
-      const float e = __builtin_amdgcn_exp2f(y);
-      z += e;
-      s = __builtin_fmaf(fmaxf(y, -200.f), e, s);   // -inf * 0 is 0 here
+        for (int j = 0; j < kPer; ++j) {
+          const float y = (element<kBf16>(w[i], j) - M) * kLog2e;
+          const float e = __builtin_amdgcn_exp2f(y);
+          z += e;
+          s = __builtin_fmaf(fmaxf(y, -200.f), e, s);
+        }
     }
+    A = M;
+  }
   z = wave_sum(z);
   s = wave_sum(s);
   if (lane == 0) {
     s_z[wave] = z;
     s_s[wave] = s;
   }
-
-  uint8_t* part = static_cast<uint8_t*>(a.partial) + (size_t)blockIdx.x * partial_stride(a.top);
-  u64* list = reinterpret_cast<u64*>(part + sizeof(Partial));
+  __syncthreads();
+  if (wave != 0) return;
+  z = s_z[0];
+  s = s_s[0];
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) {
+    z += s_z[i];
+    s += s_s[i];
+  }
+  if (A != M || __builtin_fabsf(M) <= kFar) {
+    // to the anchor itself, from fp32(A log2 e)
+    const float off = __builtin_fmaf(A, kLog2e, -(A * kLog2e));
+    const float f = __builtin_amdgcn_exp2f(-off);
+    s = f * __builtin_fmaf(-off, z, s);
+    z = f * z;
+  }
+  int kept = 0;
   if (kTop) {
-    float T = s_t[0];
+    // the waves' lists, each at most `top` long
+    u64 o[kWaves * kMaxTop / 64];
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) T = fmaxf(T, s_t[i]);
-    if (mx >= T && T > -INFINITY) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const float v = element<kBf16>(w[i], j);
-          if (v >= T) {
-            const int at = atomicAdd(&s_count, 1);
-            if (at < kMaxCand)
-              s_cand[at] = order_of(v, row.first(b0 + i * kThreads + tid) + j);
-          }
-        }
+    for (int i = 0; i < kWaves * kMaxTop / 64; ++i) {
+      const int q = i * 64 + lane, w = q / kMaxTop, at = q % kMaxTop;
+      o[i] = at < s_count[w] ? s_list[kTop ? w : 0][kTop ? at : 0] : 0ull;
     }
-    __syncthreads();
-    const int n = s_count;
-    if (T > -INFINITY && n >= a.top && n <= kMaxCand) {
-      // ranks among the candidates (their order in the list does not matter)
-      for (int q = tid; q < n; q += kThreads) {
-        const u64 o = s_cand[q];
-        int r = 0;
-        for (int i = 0; i < n; ++i) r += s_cand[i] > o;
-        if (r < a.top) list[r] = o;
-      }
-    } else {
-      // many equal logits, or few at all: the next largest, one after another
-      u64 last = ~0ull;
-      for (int k = 0; k < a.top; ++k) {
-        u64 best = 0;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            const int e = row.first(b0 + i * kThreads + tid) + j;
-            const u64 o = e >= 0 && e < a.V ? order_of(element<kBf16>(w[i], j), e) : 0ull;
-            if (o < last && o > best) best = o;
-          }
-        best = wave_max64(best);
-        if (lane == 0) s_best[wave] = best;
-        __syncthreads();
-        best = s_best[0];
-#pragma unroll
-        for (int i = 1; i < kWaves; ++i) best = s_best[i] > best ? s_best[i] : best;
-        __syncthreads();
-        if (tid == 0) list[k] = best;
-        last = best;
-      }
-    }
-  } else {
-    __syncthreads();
+    uint32_t least;
+    kept = cut<kBf16>(o, list, a.top, least, strict);
   }
-  if (tid == 0) {
-    float zs = s_z[0], ss = s_s[0];
-    for (int i = 1; i < kWaves; ++i) {
-      zs += s_z[i];
-      ss += s_s[i];
-    }
-    *reinterpret_cast<Partial*>(part) = Partial{M, zs, ss, 0.f};
+  if (chunks == 1) {
+    finish<kBf16>(a, m, M, z, s, list, kept);
+    return;
   }
+  uint8_t* part = static_cast<uint8_t*>(a.partial) + (size_t)blockIdx.x * partial_stride(a.top);
+  if (lane == 0) *reinterpret_cast<Partial*>(part) = Partial{M, z, s, kept};
+  if (kTop && lane < kept) reinterpret_cast<u64*>(part + sizeof(Partial))[lane] = list[lane];
 }
 
-// ---- a row's chunks joined: one wave a row, lane c holding chunk c ----
+// ---- a row's chunks joined: one wave a row, lane c holding chunk c's sums ----
+template <bool kBf16, int NB>
 __global__ __launch_bounds__(64) void logprob_join_kernel(moe_host::LogprobArgs a, int chunks) {
+  __shared__ u64 s_list[kMaxTop];
   const int m = blockIdx.x, lane = threadIdx.x;
   const size_t stride = partial_stride(a.top);
-  const uint8_t* part = static_cast<const uint8_t*>(a.partial) + ((size_t)m * chunks + lane) * stride;
-  Partial p{-INFINITY, 0.f, 0.f, 0.f};
-  if (lane < chunks) p = *reinterpret_cast<const Partial*>(part);
+  const uint8_t* parts = static_cast<const uint8_t*>(a.partial) + (size_t)m * chunks * stride;
+  Partial p{-INFINITY, 0.f, 0.f, 0};
+  if (lane < chunks) p = *reinterpret_cast<const Partial*>(parts + lane * stride);
+  int kept = 0;
+  if (NB > 0) {
+    u64 o[NB > 0 ? NB : 1];
+    const int all = chunks * a.top;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int q = i * 64 + lane, c = min(q / a.top, chunks - 1), at = q % a.top;
+      const u64 v = reinterpret_cast<const u64*>(parts + c * stride + sizeof(Partial))[at];
+      const int n = __shfl(p.count, c, kWave);         // by all lanes
+      o[i] = q < all && at < n ? v : 0ull;
+    }
+    uint32_t least;
+    bool strict;
+    kept = cut<kBf16>(o, s_list, a.top, least, strict);
+  }
   const float M = wave_max(p.m);
-  // a chunk without a logit above -inf adds 0 (or its NaN) as it is
+  // a chunk without a logit above -inf adds 0 (or its NaN) as it is, one far
+  // below the row's largest logit nothing
   const float d = p.m == -INFINITY ? 0.f : (p.m - M) * kLog2e;
   const float f = __builtin_amdgcn_exp2f(d);
-  // a chunk far below the row's largest logit adds nothing
   const float z = wave_sum(p.z * f);
   const float s = wave_sum(f > 0.f ? f * __builtin_fmaf(d, p.z, p.s) : 0.f * p.z);
-  // no logit above -inf: nothing is likely, nothing uncertain
-  const bool none = z == 0.f;
-  const float lz = logf(z);
-  auto logprob = [&](float l) {
-    if (none) return -INFINITY;
-    return l - M - lz;
-  };
-  if (lane == 0) {
-    const int t = a.tokens[m];
-    float lp = 0.f;
-    if (t >= 0 && t < a.V) {
-      const size_t at = (size_t)m * a.V + t;
-      const float l = a.bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.logits)[at]
-                                               << 16)
-                             : static_cast<const float*>(a.logits)[at];
-      lp = logprob(l);
-    }
-    a.logprobs[m] = lp;
-    a.entropy[m] = none ? 0.f : lz - kLn2 * (s / z);
-    a.lse[m] = none ? -INFINITY : M + lz;
-  }
-  // the lists' heads, one a lane; the largest is the next alternative
-  const u64* list = reinterpret_cast<const u64*>(part + sizeof(Partial));
-  u64 head = lane < chunks && a.top > 0 ? list[0] : 0ull;
-  int at = 0;
-  for (int k = 0; k < a.top; ++k) {
-    const u64 best = wave_max64(head);
-    if (lane == 0) {
-      a.top_ids[(size_t)m * a.top + k] = id_of(best);
-      a.top_logprobs[(size_t)m * a.top + k] = logprob(logit_of(best));
-    }
-    if (head == best && lane < chunks) {
-      ++at;
-      head = at < a.top ? list[at] : 0ull;
-    }
-  }
+  finish<kBf16>(a, m, M, z, s, s_list, kept);
 }
 
-// Blocks of 16 bytes that a row touches at most, and chunks of `loads` blocks
-// a thread.
+// Blocks of 16 bytes that a row touches at most, and the length of a chunk:
+// whole groups of a workgroup's loads, as many chunks as fill the chip.
 int row_blocks(int V, int bf16) {
   const int per = bf16 ? 8 : 4;
   return (V + 2 * (per - 1)) / per;
 }
-int chunks_of(int V, int bf16, int loads) {
-  return moe_host::ceil_div_host(row_blocks(V, bf16), kThreads * loads);
+int chunk_blocks_of(int M, int V, int bf16) {
+  const int groups = moe_host::ceil_div_host(row_blocks(V, bf16), kGroup);
+  const int want = std::min(kMaxChunks, std::max(1, kFill / std::max(M, 1)));
+  return moe_host::ceil_div_host(groups, want) * kGroup;
 }
-// Whole registers of logits a thread where the rows fill the chip, else
-// smaller chunks, so that more CUs read.
-int loads_of(int M, int V, int bf16) {
-  int loads = 8;
-  while (loads > 1 && (long long)M * chunks_of(V, bf16, loads) < kFill &&
-         chunks_of(V, bf16, loads / 2) <= kMaxChunks)
-    loads /= 2;
-  return loads;
+int chunks_of(int M, int V, int bf16) {
+  return moe_host::ceil_div_host(row_blocks(V, bf16), chunk_blocks_of(M, V, bf16));
 }
 
-template <bool kBf16, bool kTop>
-void launch_chunks(const moe_host::LogprobArgs& a, int loads, int chunks, hipStream_t s) {
-  const dim3 grid((unsigned)(a.M * chunks));
-  switch (loads) {
-    case 1: logprob_chunk_kernel<kBf16, 1, kTop><<<grid, kThreads, 0, s>>>(a, chunks); break;
-    case 2: logprob_chunk_kernel<kBf16, 2, kTop><<<grid, kThreads, 0, s>>>(a, chunks); break;
-    case 4: logprob_chunk_kernel<kBf16, 4, kTop><<<grid, kThreads, 0, s>>>(a, chunks); break;
-    default: logprob_chunk_kernel<kBf16, 8, kTop><<<grid, kThreads, 0, s>>>(a, chunks); break;
-  }
+template <bool kBf16>
+void launch_rows(const moe_host::LogprobArgs& a, hipStream_t s) {
+  const int length = chunk_blocks_of(a.M, a.V, a.bf16), chunks = chunks_of(a.M, a.V, a.bf16);
+  const unsigned grid = (unsigned)a.M * chunks;
+  if (a.top > 0)
+    logprob_kernel<kBf16, true><<<grid, kThreads, 0, s>>>(a, chunks, length);
+  else
+    logprob_kernel<kBf16, false><<<grid, kThreads, 0, s>>>(a, chunks, length);
+  if (chunks == 1) return;
+  const int lists = chunks * a.top;
+  if (lists == 0)
+    logprob_join_kernel<kBf16, 0><<<a.M, 64, 0, s>>>(a, chunks);
+  else if (lists <= 256)
+    logprob_join_kernel<kBf16, 4><<<a.M, 64, 0, s>>>(a, chunks);
+  else if (lists <= 768)
+    logprob_join_kernel<kBf16, 12><<<a.M, 64, 0, s>>>(a, chunks);
+  else
+    logprob_join_kernel<kBf16, kMaxChunks * kMaxTop / 64><<<a.M, 64, 0, s>>>(a, chunks);
 }
 
 // ---- gradient ----
@@ -398,21 +600,13 @@ __global__ __launch_bounds__(256) void logprob_backward_kernel(moe_host::Logprob
 
 namespace moe_host {
 
-size_t logprob_partial_bytes(int M, int V, int top, int bf16) {
-  // halved chunks are fewer than 2 * kFill; so sized, a workspace serves fewer
-  // rows as well
-  return std::max<size_t>((size_t)M * chunks_of(V, bf16, 8), 2 * kFill) * partial_stride(top);
-}
+size_t logprob_partial_bytes(int top) { return (size_t)kFill * partial_stride(top); }
 
 hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t s) {
-  const int loads = loads_of(a.M, a.V, a.bf16), chunks = chunks_of(a.V, a.bf16, loads);
   if (a.bf16)
-    a.top > 0 ? launch_chunks<true, true>(a, loads, chunks, s)
-              : launch_chunks<true, false>(a, loads, chunks, s);
+    launch_rows<true>(a, s);
   else
-    a.top > 0 ? launch_chunks<false, true>(a, loads, chunks, s)
-              : launch_chunks<false, false>(a, loads, chunks, s);
-  logprob_join_kernel<<<a.M, 64, 0, s>>>(a, chunks);
+    launch_rows<false>(a, s);
   return hipGetLastError();
 }
 

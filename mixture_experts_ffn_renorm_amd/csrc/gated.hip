@@ -16,7 +16,6 @@ using namespace moe;
 namespace {
 
 constexpr int kBK = 32;            // elements of the summed axis per stage
-constexpr int kStages = 4;         // stages in LDS
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -137,7 +136,7 @@ __device__ __forceinline__ void gated_grad(float g, float u, float d, float& dg,
   dg = d * u * (s * (1.0f + g * (1.0f - s)));
 }
 
-template <int BM, int BN, int WM, int WN, Op kOp>
+template <int BM, int BN, int WM, int WN, int kStages, Op kOp>
 __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
   constexpr int W = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr bool kGated = kOp == kAct || kOp == kGradAct;
@@ -179,11 +178,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // Stage kt of K, while the stages kt + 1 and kt + 2 are on their way:
-  // fragments to registers, the copies of stage kt + 3 sent into the LDS of
-  // stage kt - 1, which every wave has read; then the products.  Eight waves
-  // are two halves, half a stage apart, so that of the two waves of a SIMD one
-  // multiplies while the other reads.
+  // Stage kt of K, while the stages behind it are on their way: fragments to
+  // registers, the copies of stage kt + kStages - 1 sent into the LDS of stage
+  // kt - 1, which every wave has read (past the end: of zeros, so that every
+  // wait counts the same); then the products.  Eight waves are two halves, half
+  // a stage apart, so that of the two waves of a SIMD one multiplies while the
+  // other reads.
   constexpr bool kHalves = W == 8;
   constexpr int kCopies = Loader<BM, W, kMAcross>::kInstr + Loader<BN, W, kNAcross>::kInstr;
   const int nk = ceil_div(K, kBK);
@@ -221,7 +221,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
     if (kHalves) barrier_nofence();
   }
   if (kHalves && wave < W / 2) barrier_nofence();
-  wait_vmem<0>();                      // the copies past the end, of zeros
+  wait_vmem<0>();                      // the copies past the end
 
   // a lane holds 4 consecutive n of one m
   const int ml = m0 + wm * TM + (lane & 15), nq = 4 * (lane >> 4);
@@ -269,6 +269,129 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
   }
 }
 
+// ---- few rows: the weights are read once, as fast as memory gives them ----
+
+constexpr int kGemvRows = 4;           // rows of the GEMVs
+constexpr int kFewRows = 64;           // rows of the streaming products
+constexpr int kGemvFeatures = 2;       // features of a wave
+
+// One to four rows: a wave reads the gate and up rows of kGemvFeatures
+// features, 1 KB of each at a time.
+template <int T>
+__global__ __launch_bounds__(512) void gated_gemv_kernel(moe_host::GatedArgs a) {
+  constexpr int F = kGemvFeatures;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int f0 = (blockIdx.x * 8 + wave) * F;
+  if (f0 >= a.I) return;
+  const uint16_t* w[2 * F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const int i = min(f0 + f, a.I - 1);
+    w[f] = a.w13 + (size_t)i * a.H;
+    w[F + f] = a.w13 + (size_t)(a.I + i) * a.H;
+  }
+  float sum[2 * F][T];
+#pragma unroll
+  for (int f = 0; f < 2 * F; ++f)
+#pragma unroll
+    for (int t = 0; t < T; ++t) sum[f][t] = 0.f;
+  auto step = [&](int k) {
+    u32x4 x[T], v[2 * F];
+#pragma unroll
+    for (int f = 0; f < 2 * F; ++f) v[f] = load16(w[f] + k);
+#pragma unroll
+    for (int t = 0; t < T; ++t) x[t] = load16(a.x + (size_t)t * a.H + k);
+#pragma unroll
+    for (int f = 0; f < 2 * F; ++f)
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sum[f][t] = __builtin_fmaf(bf16_lo(x[t][j]), bf16_lo(v[f][j]), sum[f][t]);
+          sum[f][t] = __builtin_fmaf(bf16_hi(x[t][j]), bf16_hi(v[f][j]), sum[f][t]);
+        }
+  };
+  int k = 0;
+#pragma unroll 4
+  for (; k + 512 <= a.H; k += 512) step(k + lane * 8);
+  if (k + lane * 8 < a.H) step(k + lane * 8);
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const float g = wave_sum(sum[f][t]), u = wave_sum(sum[F + f][t]);
+      if (lane == 0 && f0 + f < a.I)
+        a.out[(size_t)t * a.I + f0 + f] = (uint16_t)f32_to_bf16(silu_mul(g, u));
+    }
+}
+
+// Up to 16 FM rows: a workgroup takes 16 FF features, its eight waves an
+// eighth of K each, fragments straight from memory (a wave's 64-byte pieces of
+// a weight row follow one another); the waves' sums meet in LDS, in wave order.
+// More than 16 rows take 32 features, since x comes from L2 once for every
+// workgroup (2048 x 5632, 64 rows: 21.4 us against 27.6 with 16; 32: 17.1 / 20.4).
+template <int FM, int FF>
+__global__ __launch_bounds__(512) void gated_rows_kernel(moe_host::GatedArgs a) {
+  __shared__ f32x4 red[8][2 * FF * FM][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int f0 = blockIdx.x * 16 * FF;
+  const uint16_t *w[2 * FF], *x[FM];             // gates, then ups
+#pragma unroll
+  for (int f = 0; f < FF; ++f) {
+    w[f] = a.w13 + (size_t)min(f0 + 16 * f + i, a.I - 1) * a.H + 8 * g;
+    w[FF + f] = w[f] + (size_t)a.I * a.H;
+  }
+#pragma unroll
+  for (int j = 0; j < FM; ++j) x[j] = a.x + (size_t)min(16 * j + i, a.M - 1) * a.H + 8 * g;
+  const int steps = ceil_div(a.H, 32), per = ceil_div(steps, 8);
+  const int first = wave * per, last = min(steps, first + per), whole = min(last, a.H / 32);
+  f32x4 acc[2 * FF][FM];
+#pragma unroll
+  for (int f = 0; f < 2 * FF; ++f)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = first; k < whole; ++k) {
+    u32x4 v[2 * FF];
+#pragma unroll
+    for (int f = 0; f < 2 * FF; ++f) v[f] = load16(w[f] + k * 32);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const u32x4 xv = load16(x[j] + k * 32);
+#pragma unroll
+      for (int f = 0; f < 2 * FF; ++f) acc[f][j] = mfma_16x16x32(v[f], xv, acc[f][j]);
+    }
+  }
+  if (first < last && whole < last) {            // H ends inside the step
+    const bool ok = whole * 32 + 8 * g < a.H;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const u32x4 xv = load16_or_zero(x[j] + whole * 32, ok);
+#pragma unroll
+      for (int f = 0; f < 2 * FF; ++f)
+        acc[f][j] = mfma_16x16x32(load16_or_zero(w[f] + whole * 32, ok), xv, acc[f][j]);
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < 2 * FF; ++f)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) red[wave][f * FM + j][lane] = acc[f][j];
+  __syncthreads();
+  if (wave >= FF * FM) return;
+  const int j = wave % FM, m = 16 * j + i, n = f0 + wave / FM * 16 + 4 * g;
+  f32x4 sg = red[0][wave][lane], su = red[0][FF * FM + wave][lane];
+#pragma unroll
+  for (int q = 1; q < 8; ++q) {
+    sg += red[q][wave][lane];
+    su += red[q][FF * FM + wave][lane];
+  }
+  if (m < a.M && n < a.I)
+    *reinterpret_cast<u32x2*>(a.out + (size_t)m * a.I + n) =
+        u32x2{pack_bf16x2(silu_mul(sg[0], su[0]), silu_mul(sg[1], su[1])),
+              pack_bf16x2(silu_mul(sg[2], su[2]), silu_mul(sg[3], su[3]))};
+}
+
 // out = bf16(sum of the splits, in their order); n a multiple of 8
 __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ partial, int splits,
                                                    size_t n, uint16_t* __restrict__ out) {
@@ -295,14 +418,21 @@ using moe_host::ceil_div_host;
 
 constexpr int kMaxSplits = 16;
 constexpr int kSplitTiles = 1024;
+constexpr int kSmallSplitTiles = 256;   // 512 and 1024: 5 and 12 % slower at 509 x 2048 x 1408
 
-// Tile size and ranges of K of one product.
+// Tile size and ranges of K of one product.  Tiles of 256 x 256 where half the
+// chip has one (128 x 128 re-reads twice as much from L2 and LDS), 64 x 128 with
+// a ring twice as deep where 128 x 128 would leave half the chip without
+// (2048 x 5632, 128 rows: 23.3 us against 27.0; 509 rows' gradient at 1408
+// features 53 / 60), and a product whose sum is all it stores is cut along K
+// until every CU has a tile.
 struct Plan {
-  bool big;                  // 256 x 256 tiles, else 128 x 128
+  bool big;                  // 256 x 256 tiles, else bm x 128
+  int bm;
   int splits, k_per;
 };
 Plan plan_of(int rows, int n_rows, int K, bool can_split) {
-  Plan p{true, 1, 0};
+  Plan p{true, 128, 1, 0};
   const int cu = 256;
   const long long big = (long long)ceil_div_host(rows, 256) * ceil_div_host(n_rows, 256);
   p.big = big >= cu / 2;
@@ -311,11 +441,12 @@ Plan plan_of(int rows, int n_rows, int K, bool can_split) {
   const int stages = ceil_div_host(K, kBK);
   if (can_split && tiles < cu) {
     // whole stages, at least 8 to a range
-    const long long most = std::min(stages / 8, kMaxSplits), room = kSplitTiles / (p.big ? 4 : 1);
+    const long long most = std::min(stages / 8, kMaxSplits), room = p.big ? kSplitTiles / 4 : kSmallSplitTiles;
     p.splits = (int)std::max<long long>(1, std::min(room / tiles, most));
   }
   p.k_per = ceil_div_host(stages, p.splits) * kBK;
   p.splits = ceil_div_host(K, p.k_per);
+  if (!can_split && !p.big && tiles <= cu / 2) p.bm = 64;
   return p;
 }
 
@@ -323,13 +454,15 @@ template <Op kOp>
 hipError_t launch_tiles(TileArgs a, int n_rows, const Plan& p, hipStream_t s) {
   a.splits = p.splits;
   a.k_per = p.k_per;
-  a.tiles_m = ceil_div_host(a.rows, p.big ? 256 : 128);
+  a.tiles_m = ceil_div_host(a.rows, p.big ? 256 : p.bm);
   a.tiles_n = ceil_div_host(n_rows, p.big ? 256 : 128);
   const unsigned grid = (unsigned)ceil_div_host(a.tiles_m * a.tiles_n * a.splits, 8) * 8;
   if (p.big)
-    tile_kernel<256, 256, 2, 4, kOp><<<grid, 512, 0, s>>>(a);
+    tile_kernel<256, 256, 2, 4, 4, kOp><<<grid, 512, 0, s>>>(a);
+  else if (p.bm == 64)
+    tile_kernel<64, 128, 2, 2, 8, kOp><<<grid, 256, 0, s>>>(a);
   else
-    tile_kernel<128, 128, 2, 2, kOp><<<grid, 256, 0, s>>>(a);
+    tile_kernel<128, 128, 2, 2, 4, kOp><<<grid, 256, 0, s>>>(a);
   if (p.splits > 1) {
     const size_t n = (size_t)a.rows * a.cols;
     const unsigned g = (unsigned)std::min<size_t>((n / 8 + 255) / 256, 4096);
@@ -351,6 +484,25 @@ size_t partial_bytes(int rows, int cols) {
 namespace moe_host {
 
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s) {
+  if (a.M <= kGemvRows) {
+    const int grid = ceil_div_host(a.I, 8 * kGemvFeatures);
+    switch (a.M) {
+      case 1: gated_gemv_kernel<1><<<grid, 512, 0, s>>>(a); break;
+      case 2: gated_gemv_kernel<2><<<grid, 512, 0, s>>>(a); break;
+      case 3: gated_gemv_kernel<3><<<grid, 512, 0, s>>>(a); break;
+      default: gated_gemv_kernel<4><<<grid, 512, 0, s>>>(a); break;
+    }
+    return hipGetLastError();
+  }
+  if (a.M <= kFewRows) {
+    if (a.M <= 16)
+      gated_rows_kernel<1, 1><<<ceil_div_host(a.I, 16), 512, 0, s>>>(a);
+    else if (a.M <= 32)
+      gated_rows_kernel<2, 2><<<ceil_div_host(a.I, 32), 512, 0, s>>>(a);
+    else
+      gated_rows_kernel<4, 2><<<ceil_div_host(a.I, 32), 512, 0, s>>>(a);
+    return hipGetLastError();
+  }
   TileArgs t{};
   t.m_side = a.x;
   t.n_side = a.w13;

@@ -629,9 +629,9 @@ size_t moe_linear_adapters_workspace_size(int M, int K, int R);
  *   out    bf16 out, overlapping no input but an addend that is out itself
  *   workspace  moe_linear_adapters_workspace_size(M, K, R) bytes, 16-byte
  *          aligned, overlapping no operand
- * Two launches, three above 64 rows (rows are grouped by adapter there).  K and N multiples
- * of 8 (gated: N of 16), at most 2^17; M < 2^21.  Sums are fp32; x A^T keeps
- * at least 16 bits between the two products.  A row's result depends on no
+ * Two launches, three above 128 rows (rows are grouped by adapter there).  K
+ * and N multiples of 8 (gated: N of 16), at most 2^17; M < 2^21.  Sums are
+ * fp32; x A^T keeps at least 16 bits between the two products.  A row's result depends on no
  * other row.
  */
 int moe_linear_adapters(const uint16_t* x, const moe_adapters* adapters, const int32_t* slots,
@@ -645,7 +645,7 @@ size_t moe_token_logprobs_workspace_size(int logits_fp32, int M, int V, int top)
 /*
  * moe_token_logprobs -- what is read from an output head's logits: the log
  * probability of one given token per row, the entropy, and the most likely
- * alternatives (two launches).
+ * alternatives (one or two launches).
  *
  *   p = softmax(l)                      over the V logits of a row
  *   logprobs[m] = log p[tokens[m]]      0 where tokens[m] is outside [0, V)

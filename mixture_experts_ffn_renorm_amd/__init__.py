@@ -964,13 +964,16 @@ def moe_linear_quantized(x, weight: dict, gated: bool = False, row_scale=None, a
 # a gated block in bf16 and its gradient
 # ---------------------------------------------------------------------------
 
-def _workspace_of(call: str, nbytes: int, ws, device: int, stream):
-    """The workspace of a call that needs nbytes (0: sizes it refuses)."""
-    if nbytes == 0:
-        raise MoeError(call, -2)
+def _workspace_of(call: str, size, args, ws, device: int, stream):
+    """The workspace of a call: ``ws``, whose size the C call checks, or a new
+    one of size(*args) bytes (0: sizes that the call refuses)."""
+    torch = _torch()
     if ws is None:
-        return _empty((nbytes,), _torch().uint8, device, stream)
-    _need(ws, "ws", _torch().uint8, (ws.numel(),), device)
+        nbytes = size(*args)
+        if nbytes == 0:
+            raise MoeError(call, -2)
+        return _empty((nbytes,), torch.uint8, device, stream)
+    _need(ws, "ws", torch.uint8, (ws.numel(),), device)
     return ws
 
 
@@ -1049,8 +1052,9 @@ def moe_linear_gated_backward(x, w13, grad_out, grad_x=None, grad_w13=None, need
         else:
             _need(t, name, bf16, shape, dev)
         outs.append(t)
-    need = library().moe_linear_gated_backward_workspace_size(M, H, two_i // 2)
-    ws = _workspace_of("moe_linear_gated_backward", need, ws, dev, stream)
+    ws = _workspace_of("moe_linear_gated_backward",
+                       library().moe_linear_gated_backward_workspace_size, (M, H, two_i // 2), ws,
+                       dev, stream)
     st = library().moe_linear_gated_backward(
         x.data_ptr(), w13.data_ptr(), grad_out.data_ptr(), M, H, two_i // 2, *map(_ptr, outs),
         ws.data_ptr(), ws.numel(), _raw_stream(dev, stream))
@@ -1115,8 +1119,8 @@ def moe_linear_adapters(x, adapters: dict, slots, gated: bool = False, addend=No
         out = _empty(shape, bf16, dev, stream)
     else:
         _need(out, "out", bf16, shape, dev)
-    need = library().moe_linear_adapters_workspace_size(M, K, R)
-    ws = _workspace_of("moe_linear_adapters", need, ws, dev, stream)
+    ws = _workspace_of("moe_linear_adapters", library().moe_linear_adapters_workspace_size,
+                       (M, K, R), ws, dev, stream)
     w = _pack_matrix(S, R, a.data_ptr(), b.data_ptr(), 0 if scales is None else scales.data_ptr())
     st = library().moe_linear_adapters(x.data_ptr(), w, slots.data_ptr(), M, K, N,
                                        1 if gated else 0, _ptr(addend), out.data_ptr(),
@@ -1180,8 +1184,8 @@ def moe_token_logprobs(logits, tokens, top: int = 0, logprobs=None, entropy=None
                           top_ids, top_logprobs, ws, stream)
     _need(logits, "logits", logits.dtype, (M, V), dev)
     _need(tokens, "tokens", torch.int32, (M,), dev)
-    need = library().moe_token_logprobs_workspace_size(fp32, M, V, top)
-    ws = _workspace_of("moe_token_logprobs", need, ws, dev, stream)
+    ws = _workspace_of("moe_token_logprobs", library().moe_token_logprobs_workspace_size,
+                       (fp32, M, V, top), ws, dev, stream)
     f32 = torch.float32
     outs = []
     for name, t, dtype, shape in (("logprobs", logprobs, f32, (M,)), ("entropy", entropy, f32, (M,)),

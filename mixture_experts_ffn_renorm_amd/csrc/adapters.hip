@@ -215,11 +215,21 @@ __global__ __launch_bounds__(512) void shrink_kernel(AdapterArgs a, const int* _
 #pragma unroll
   for (int f = 0; f < FR; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int whole = min(last, a.K / 32);
-#pragma unroll 4
-  for (int k = first; k < whole; ++k) {
-    const u32x4 xv = load16(x + k * 32);
+  // kBatch steps at a time, all their loads in flight at once
+  constexpr int kBatch = FR <= 4 ? 4 : 2;
+  for (int k = first; k < whole; k += kBatch) {
+    u32x4 xv[kBatch], av[kBatch][FR];
 #pragma unroll
-    for (int f = 0; f < FR; ++f) acc[f] = mfma_16x16x32(load16(A[f] + k * 32), xv, acc[f]);
+    for (int b = 0; b < kBatch; ++b) {
+      const bool ok = k + b < whole;
+      xv[b] = load16_or_zero(x + (k + b) * 32, ok);
+#pragma unroll
+      for (int f = 0; f < FR; ++f) av[b][f] = load16_or_zero(A[f] + (k + b) * 32, ok);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int f = 0; f < FR; ++f) acc[f] = mfma_16x16x32(av[b][f], xv[b], acc[f]);
   }
   if (first < last && whole < last) {            // K ends inside the step
     const bool ok = whole * 32 + 8 * g < a.K;
@@ -254,90 +264,114 @@ __global__ __launch_bounds__(512) void shrink_kernel(AdapterArgs a, const int* _
   }
 }
 
-constexpr int kExpandCols = 64;        // output columns of a wave
 constexpr int kExpandWaves = 4;
 
-// y of a unit: a wave takes kExpandCols columns of all its tokens.  The rows
-// of two fragments of B are dealt so that a lane holds 8 consecutive columns.
+// y of a unit: each of four waves has 16 of its tokens and walks over `steps`
+// times 16 F columns (not gated: 128-byte lines).  The step's four fragments of
+// B are read once, one by each wave, and shared through LDS (every wave for
+// itself, B comes from L2 four times and bounds the kernel: 4096 tokens x 8192,
+// rank 64); the next step's loads are in flight meanwhile.  The rows of the F
+// fragments of B are dealt so that a lane holds 4 F consecutive columns.
 template <int FK, bool kGated>
 __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(
     AdapterArgs a, const int* __restrict__ order, const Unit* __restrict__ units,
-    const uint16_t* __restrict__ t) {
-  constexpr int kHalves = kGated ? 2 : 1;
-  const Unit u = units[blockIdx.x];
-  if (u.count == 0) return;
+    const uint16_t* __restrict__ t, int total, int steps) {
+  constexpr int kHalves = kGated ? 2 : 1, F = kGated ? 2 : 4, kQ = F / 2;
+  static_assert(kHalves * F == kExpandWaves, "a fragment a wave");
+  __shared__ u32x4 s_b[2][kExpandWaves][FK][64];
+  const int at_unit = blockIdx.y + blockIdx.z * gridDim.y;
+  if (at_unit >= total) return;
+  const Unit u = units[at_unit];
   const bool none = u.slot >= a.S;
   const int n_out = kGated ? a.N / 2 : a.N;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const int n0 = (blockIdx.y * kExpandWaves + wave) * kExpandCols;
-  if (n0 >= n_out || (none && !kGated && a.addend == a.out)) return;
-  const int frags = ceil_div(u.count, 16);
-  int m[4];
-  u32x4 hi[4][FK], lo[4][FK];
+  const int c0 = blockIdx.x * steps * 16 * F, c1 = min(c0 + steps * 16 * F, n_out);
+  const bool added = a.addend != nullptr;
+  if (u.count == 0 || c0 >= c1 || (none && !kGated && a.addend == a.out)) return;
+  // a wave past the unit's last token works for the others alone
+  const int count = u.count - 16 * wave;
+  const int place = u.start + min(16 * wave + i, u.count - 1), m = order[place];
+  const uint16_t* addend = added ? a.addend + (size_t)m * a.N : nullptr;
+  uint16_t* out = a.out + (size_t)m * n_out;
+  const uint8_t* B = reinterpret_cast<const uint8_t*>(a.b + (size_t)(none ? 0 : u.slot) * a.N * a.R);
+  constexpr u32x4 kZero = {0u, 0u, 0u, 0u};
+  struct Loads {
+    u32x4 add[kHalves][kQ], b[FK];
+  };
+  auto load = [&](int c, Loads& l) {
+    if (added && count > 0) {
+      // lanes past the last column read what is there and store nothing
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int at = u.start + min(16 * j + i, u.count - 1);
-    m[j] = order[at];
-    const uint16_t* p = t + (size_t)at * 2 * a.R;
+      for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-    for (int k = 0; k < FK; ++k) {
-      const int r = 32 * k + 8 * g;
-      const bool ok = !none && j < frags && r < a.R;
-      hi[j][k] = load16_or_zero(p + r, ok);
-      lo[j][k] = load16_or_zero(p + a.R + r, ok);
+        for (int q = 0; q < kQ; ++q)
+          l.add[h][q] = load16(addend + h * n_out + min(c + 4 * F * g + 8 * q, n_out - 8));
     }
+    if (!none) {
+      // row i of fragment wave % F, of the half wave / F
+      const int row = min(c + 4 * F * (i >> 2) + 4 * (wave % F) + (i & 3), n_out - 1) +
+                      wave / F * n_out;
+      const uint32_t at = (uint32_t)__umul24(row, 2 * a.R) + 16 * g;
+#pragma unroll
+      for (int k = 0; k < FK; ++k) l.b[k] = load16_or_zero(B + (at + 64 * k), 32 * k + 8 * g < a.R);
+    }
+  };
+  Loads next;
+#pragma unroll
+  for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) next.add[h][q] = kZero;
+#pragma unroll
+  for (int k = 0; k < FK; ++k) next.b[k] = kZero;
+  load(c0, next);
+  u32x4 hi[FK], lo[FK];
+#pragma unroll
+  for (int k = 0; k < FK; ++k) {
+    const uint16_t* p = t + (size_t)place * 2 * a.R + 32 * k + 8 * g;
+    const bool ok = !none && 32 * k + 8 * g < a.R;
+    hi[k] = load16_or_zero(p, ok);
+    lo[k] = load16_or_zero(p + a.R, ok);
   }
+  int buf = 0;
 #pragma unroll 1
-  for (int c = n0; c < min(n0 + kExpandCols, n_out); c += 32) {
-    // row i of fragment f: column 8 (i / 4) + 4 f + i % 4
-    u32x4 b[kHalves][2][FK];
+  for (int c = c0; c < c1; c += 16 * F, buf ^= 1) {
+#pragma unroll
+    for (int k = 0; k < FK; ++k) s_b[buf][wave][k][lane] = next.b[k];
+    const Loads now = next;
+    wait_lgkm0();
+    barrier_nofence();
+    if (c + 16 * F < c1) load(c + 16 * F, next);
+    if (count <= 0) continue;
+    f32x4 acc[kHalves][F];
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int n = min(c + 8 * (i >> 2) + 4 * f + (i & 3), n_out - 1) + h * n_out;
-        const uint16_t* p = a.b + ((size_t)(none ? 0 : u.slot) * a.N + n) * a.R;
+      for (int f = 0; f < F; ++f) {
+        u32x4 b[FK];
 #pragma unroll
-        for (int k = 0; k < FK; ++k) {
-          const int r = 32 * k + 8 * g;
-          b[h][f][k] = load16_or_zero(p + r, !none && r < a.R);
-        }
+        for (int k = 0; k < FK; ++k) b[k] = s_b[buf][h * F + f][k][lane];
+        acc[h][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // the smaller terms first
+#pragma unroll
+        for (int k = 0; k < FK; ++k) acc[h][f] = mfma_16x16x32(b[k], lo[k], acc[h][f]);
+#pragma unroll
+        for (int k = 0; k < FK; ++k) acc[h][f] = mfma_16x16x32(b[k], hi[k], acc[h][f]);
       }
-    const int n = c + 8 * g;
-    u32x4 add[4][kHalves];
+    const int n = c + 4 * F * g;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int h = 0; h < kHalves; ++h)
-        add[j][h] = load16_or_zero(a.addend + (size_t)m[j] * a.N + h * n_out + n,
-                                   a.addend != nullptr && j < frags && n < n_out);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j >= frags) break;
-      f32x4 acc[kHalves][2];
-#pragma unroll
-      for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          acc[h][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-          // the smaller terms first
-#pragma unroll
-          for (int k = 0; k < FK; ++k) acc[h][f] = mfma_16x16x32(b[h][f][k], lo[j][k], acc[h][f]);
-#pragma unroll
-          for (int k = 0; k < FK; ++k) acc[h][f] = mfma_16x16x32(b[h][f][k], hi[j][k], acc[h][f]);
-        }
-      if (16 * j + i >= u.count || n >= n_out) continue;
+    for (int q = 0; q < kQ; ++q) {
+      if (i >= count || n + 8 * q >= n_out) continue;
       float y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         auto at = [&](int h) {
-          const uint32_t w = add[j][h][e >> 1];
-          return acc[h][e >> 2][e & 3] + (e & 1 ? bf16_hi(w) : bf16_lo(w));
+          const uint32_t w = now.add[h][q][e >> 1];
+          return acc[h][2 * q + (e >> 2)][e & 3] + (e & 1 ? bf16_hi(w) : bf16_lo(w));
         };
         y[e] = kGated ? silu_mul(at(0), at(kHalves - 1)) : at(0);
       }
-      *reinterpret_cast<u32x4*>(a.out + (size_t)m[j] * n_out + n) =
+      *reinterpret_cast<u32x4*>(out + n + 8 * q) =
           u32x4{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                 pack_bf16x2(y[6], y[7])};
     }
@@ -346,8 +380,14 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(
 
 using moe_host::ceil_div_host;
 
-// Tokens up to which each reads its adapter by itself.
-constexpr int kGemvTokens = 64;
+// Units enough to fill the chip with workgroups of 4 steps (8 and 16 steps: 43
+// and 46 us against 41 for 4096 tokens, 8192 columns, rank 64).
+constexpr int kManyTokens = 1024;
+
+// Tokens up to which each reads its adapter by itself: 128 tokens, 48 adapters of
+// rank 16, 2048 -> 11264 columns gated 12.6 us against 17.8 by units; 256 tokens
+// of rank 64 43 us against 31.
+constexpr int kGemvTokens = 128;
 
 struct Layout {
   int windows, cap;        // of the grouping; units of a window
@@ -374,9 +414,14 @@ void launch_shrink(const AdapterArgs& a, const Layout& l, const int* order, cons
 template <int FK, bool kGated>
 void launch_expand(const AdapterArgs& a, const Layout& l, const int* order, const Unit* units,
                    const uint16_t* t, hipStream_t s) {
-  const dim3 grid((unsigned)(l.windows * l.cap),
-                  (unsigned)ceil_div_host(kGated ? a.N / 2 : a.N, kExpandCols * kExpandWaves));
-  expand_kernel<FK, kGated><<<grid, 64 * kExpandWaves, 0, s>>>(a, order, units, t);
+  // the columns of one unit next to each other: the rows' lines, and with 8 XCDs
+  // the same columns of B, meet in one L2
+  const int units_all = l.windows * l.cap, high = std::min(units_all, 32768);
+  const int steps = a.M >= kManyTokens ? 4 : 1;
+  const dim3 grid((unsigned)ceil_div_host(kGated ? a.N / 2 : a.N, 16 * (kGated ? 2 : 4) * steps),
+                  (unsigned)high, (unsigned)ceil_div_host(units_all, high));
+  expand_kernel<FK, kGated><<<grid, 64 * kExpandWaves, 0, s>>>(a, order, units, t, units_all,
+                                                               steps);
 }
 
 }  // namespace

@@ -105,7 +105,7 @@ def check(M, S, R, K, N, order="random", seed=0, scaled=True, added=True, gated=
     return out
 
 
-MS = [1, 2, 5, 16, 17, 31, 64, 65, 66, 100, 128, 129, 300, 1000]
+MS = [1, 2, 5, 16, 17, 31, 64, 65, 66, 100, 128, 129, 130, 300, 1000, 1030]
 
 
 @pytest.mark.parametrize("order", ["random", "runs"])
@@ -121,13 +121,13 @@ def test_ranks(R, M):
     check(M, 4, R, 96, 96, seed=R, gated=True)
 
 
-@pytest.mark.parametrize("M", [1, 30, 130])
+@pytest.mark.parametrize("M", [1, 30, 130, 135])
 @pytest.mark.parametrize("K", [8, 16, 24, 32, 40, 64, 248, 256, 264, 504, 520, 1408, 2048, 8192])
 def test_inner_sizes(K, M):
     check(M, 3, 16, K, 40, seed=K)
 
 
-@pytest.mark.parametrize("M", [1, 30, 130])
+@pytest.mark.parametrize("M", [1, 30, 130, 135])
 @pytest.mark.parametrize("N", [8, 16, 24, 56, 64, 72, 248, 256, 264, 520, 2048, 11264])
 def test_output_sizes(N, M):
     check(M, 3, 16, 64, N, seed=N)
@@ -135,7 +135,7 @@ def test_output_sizes(N, M):
         check(M, 3, 16, 64, N, seed=N, gated=True)
 
 
-@pytest.mark.parametrize("M", [3, 64, 65, 260])
+@pytest.mark.parametrize("M", [3, 64, 65, 260, 1100])
 @pytest.mark.parametrize("scaled,added,gated,in_place", [
     (False, True, False, False), (True, False, False, False), (True, True, False, True),
     (False, False, False, False), (True, True, True, False), (True, False, True, False)])
@@ -144,7 +144,7 @@ def test_epilogues(M, scaled, added, gated, in_place):
     check(M, 6, 24, 72, 80, "runs", 4, scaled, added, gated, in_place)
 
 
-@pytest.mark.parametrize("M", [2, 64, 70, 500])
+@pytest.mark.parametrize("M", [2, 64, 70, 140, 500])
 def test_slots(M):
     """No adapter at all, all one, each its own, numbers far outside."""
     S = 500
@@ -172,7 +172,7 @@ def test_layer_sizes(M, order):
     check(M, 8, 64, 2048, 2048, order, seed=1)
 
 
-@pytest.mark.parametrize("M", [3, 80])
+@pytest.mark.parametrize("M", [3, 180])
 def test_a_row_that_is_not_finite_stays_alone(M):
     import torch
     moe = _moe()

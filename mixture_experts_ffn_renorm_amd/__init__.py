@@ -1186,19 +1186,23 @@ def moe_token_logprobs(logits, tokens, top: int = 0, logprobs=None, entropy=None
     _need(tokens, "tokens", torch.int32, (M,), dev)
     ws = _workspace_of("moe_token_logprobs", library().moe_token_logprobs_workspace_size,
                        (fp32, M, V, top), ws, dev, stream)
-    f32 = torch.float32
-    outs = []
-    for name, t, dtype, shape in (("logprobs", logprobs, f32, (M,)), ("entropy", entropy, f32, (M,)),
-                                  ("lse", lse, f32, (M,)),
-                                  ("top_ids", top_ids, torch.int32, (M, top)),
-                                  ("top_logprobs", top_logprobs, f32, (M, top))):
-        if top == 0 and len(shape) == 2:
-            t = None
-        elif t is None:
-            t = _empty(shape, dtype, dev, stream)
-        else:
-            _need(t, name, dtype, shape, dev)
-        outs.append(t)
+    f32, i32 = torch.float32, torch.int32
+    outs = [logprobs, entropy, lse, top_ids if top else None, top_logprobs if top else None]
+    for k, name in enumerate(("logprobs", "entropy", "lse")):
+        if outs[k] is not None:
+            _need(outs[k], name, f32, (M,), dev)
+    for k, name, dtype in ((3, "top_ids", i32), (4, "top_logprobs", f32)):
+        if outs[k] is not None:
+            _need(outs[k], name, dtype, (M, top), dev)
+        elif top:
+            outs[k] = _empty((M, top), dtype, dev, stream)
+    if logprobs is None and entropy is None and lse is None:
+        # one allocation; rows of whole 16 bytes, as every operand's start
+        outs[:3] = _empty((3, (M + 3) & ~3), f32, dev, stream)[:, :M].unbind(0)
+    else:
+        for k in range(3):
+            if outs[k] is None:
+                outs[k] = _empty((M,), f32, dev, stream)
     st = library().moe_token_logprobs(logits.data_ptr(), fp32, tokens.data_ptr(), M, V, top,
                                       *map(_ptr, outs), ws.data_ptr(), ws.numel(),
                                       _raw_stream(dev, stream))

@@ -112,7 +112,7 @@ def algorithmic(shape, M, touched):
 
 # sources of kernels that no layer of this benchmark launches
 OPERATOR_SOURCES = ("adapters.hip", "dense.h", "dense_api.hip", "gated.hip", "logprobs.hip",
-                    "mfma_tile.h", "qlinear.hip", "select.hip")
+                    "qlinear.hip", "select.hip")
 
 
 def kernel_source_hash():

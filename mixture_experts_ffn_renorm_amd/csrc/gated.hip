@@ -325,71 +325,111 @@ __global__ __launch_bounds__(512) void gated_gemv_kernel(moe_host::GatedArgs a) 
     }
 }
 
-// Up to 16 FM rows: a workgroup takes 16 FF features, its eight waves an
-// eighth of K each, fragments straight from memory (a wave's 64-byte pieces of
-// a weight row follow one another); the waves' sums meet in LDS, in wave order.
-// More than 16 rows take 32 features, since x comes from L2 once for every
-// workgroup (2048 x 5632, 64 rows: 21.4 us against 27.6 with 16; 32: 17.1 / 20.4).
+// Up to 16 FM rows: a workgroup takes 16 FF features, its four waves every
+// fourth 128 elements of K each.  A wave copies its weight rows in runs of 256
+// bytes into LDS of its own (no barriers), two pieces of K ahead, and reads them
+// back as fragments; x comes from L2 straight into registers.  The waves' sums
+// meet in LDS, in wave order.  (2048 x 5632: 16 rows 13.5 us, 32 15.3, 64 19.2;
+// fragments straight from memory, 16 rows of 64 bytes an instruction: 16.7, 17.1
+// and 21.4.)  More than 16 rows take 32 features, since x comes from L2 once for
+// every workgroup: 64 rows 24.8 with 16.
+constexpr int kRowsWaves = 4;
+constexpr int kRowsK = 128;            // elements of K of a piece
+
 template <int FM, int FF>
-__global__ __launch_bounds__(512) void gated_rows_kernel(moe_host::GatedArgs a) {
-  __shared__ f32x4 red[8][2 * FF * FM][64];
+__global__ __launch_bounds__(64 * kRowsWaves, 1) void gated_rows_kernel(moe_host::GatedArgs a) {
+  constexpr int kRows = 32 * FF;                 // gate rows, then up rows
+  constexpr int kPiece = kRows * kRowsK * 2, kCopies = kRows / 4, kSteps = kRowsK / 32;
+  constexpr int kSums = kRowsWaves * 2 * FF * FM * 1024;
+  constexpr int kLds = kRowsWaves * 2 * kPiece;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds > kSums ? kLds : kSums];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
   const int f0 = blockIdx.x * 16 * FF;
-  const uint16_t *w[2 * FF], *x[FM];             // gates, then ups
+  // copy q takes rows 4 q .. 4 q + 3; 16-byte piece c of row r lies at c ^ (r & 15)
+  const uint16_t* src[kCopies];
+  int at_k[kCopies];
 #pragma unroll
-  for (int f = 0; f < FF; ++f) {
-    w[f] = a.w13 + (size_t)min(f0 + 16 * f + i, a.I - 1) * a.H + 8 * g;
-    w[FF + f] = w[f] + (size_t)a.I * a.H;
+  for (int q = 0; q < kCopies; ++q) {
+    const int r = 4 * q + g, f = min(f0 + r % (16 * FF), a.I - 1);
+    at_k[q] = 8 * (i ^ (r & 15));
+    src[q] = a.w13 + (size_t)(r < 16 * FF ? f : a.I + f) * a.H + at_k[q];
   }
+  const uint16_t* x[FM];
 #pragma unroll
   for (int j = 0; j < FM; ++j) x[j] = a.x + (size_t)min(16 * j + i, a.M - 1) * a.H + 8 * g;
-  const int steps = ceil_div(a.H, 32), per = ceil_div(steps, 8);
-  const int first = wave * per, last = min(steps, first + per), whole = min(last, a.H / 32);
+  uint8_t* mine = lds + wave * 2 * kPiece;
+  const uint32_t mine_at = (uint32_t)(uintptr_t)(lds_void_t*)mine;
+  const int pieces = ceil_div(a.H, kRowsK * kRowsWaves);
+  // piece p of this wave; past the end of K zeros
+  auto issue = [&](int p, u32x4 (&xv)[kSteps][FM]) {
+    const int k0 = (p * kRowsWaves + wave) * kRowsK;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+        xv[s][j] = load16_or_zero(x[j] + k0 + 32 * s, k0 + 32 * s + 8 * g < a.H);
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q)
+      copy16(k0 + at_k[q] < a.H ? (const void*)(src[q] + k0) : (const void*)kZeroPage,
+             mine_at + (p & 1) * kPiece + q * 1024);
+  };
   f32x4 acc[2 * FF][FM];
 #pragma unroll
   for (int f = 0; f < 2 * FF; ++f)
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int k = first; k < whole; ++k) {
-    u32x4 v[2 * FF];
+  auto multiply = [&](int p, const u32x4 (&xv)[kSteps][FM]) {
+    // at most the next piece's copies are still on their way
+    wait_vmem<kCopies>();
+    asm volatile("" ::: "memory");
+    const uint8_t* at = mine + (p & 1) * kPiece + i * 256;
 #pragma unroll
-    for (int f = 0; f < 2 * FF; ++f) v[f] = load16(w[f] + k * 32);
+    for (int s = 0; s < kSteps; ++s) {
+      u32x4 v[2 * FF];
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const u32x4 xv = load16(x[j] + k * 32);
+      for (int f = 0; f < 2 * FF; ++f) v[f] = load16(at + f * 4096 + (((4 * s + g) ^ i) << 4));
 #pragma unroll
-      for (int f = 0; f < 2 * FF; ++f) acc[f][j] = mfma_16x16x32(v[f], xv, acc[f][j]);
+      for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int f = 0; f < 2 * FF; ++f) acc[f][j] = mfma_16x16x32(v[f], xv[s][j], acc[f][j]);
     }
+    wait_lgkm0();                                // the piece's LDS is free
+    asm volatile("" ::: "memory");
+  };
+  u32x4 x0[kSteps][FM], x1[kSteps][FM];
+  issue(0, x0);
+  issue(1, x1);
+#pragma unroll 1
+  for (int p = 0; p < pieces; p += 2) {
+    multiply(p, x0);
+    issue(p + 2, x0);
+    multiply(p + 1, x1);
+    issue(p + 3, x1);
   }
-  if (first < last && whole < last) {            // H ends inside the step
-    const bool ok = whole * 32 + 8 * g < a.H;
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const u32x4 xv = load16_or_zero(x[j] + whole * 32, ok);
-#pragma unroll
-      for (int f = 0; f < 2 * FF; ++f)
-        acc[f][j] = mfma_16x16x32(load16_or_zero(w[f] + whole * 32, ok), xv, acc[f][j]);
-    }
-  }
+  wait_vmem<0>();                                // the copies past the end
+  __syncthreads();
+  f32x4* red = reinterpret_cast<f32x4*>(lds);    // [wave][2 FF][FM][64]
 #pragma unroll
   for (int f = 0; f < 2 * FF; ++f)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) red[wave][f * FM + j][lane] = acc[f][j];
+    for (int j = 0; j < FM; ++j)
+      red[((wave * 2 * FF + f) * FM + j) * 64 + lane] = acc[f][j];
   __syncthreads();
-  if (wave >= FF * FM) return;
-  const int j = wave % FM, m = 16 * j + i, n = f0 + wave / FM * 16 + 4 * g;
-  f32x4 sg = red[0][wave][lane], su = red[0][FF * FM + wave][lane];
 #pragma unroll
-  for (int q = 1; q < 8; ++q) {
-    sg += red[q][wave][lane];
-    su += red[q][FF * FM + wave][lane];
+  for (int e = wave; e < FF * FM; e += kRowsWaves) {
+    const int f = e / FM, j = e % FM, m = 16 * j + i, n = f0 + f * 16 + 4 * g;
+    f32x4 sg = red[(f * FM + j) * 64 + lane], su = red[((FF + f) * FM + j) * 64 + lane];
+#pragma unroll
+    for (int q = 1; q < kRowsWaves; ++q) {
+      sg += red[((q * 2 * FF + f) * FM + j) * 64 + lane];
+      su += red[((q * 2 * FF + FF + f) * FM + j) * 64 + lane];
+    }
+    if (m < a.M && n < a.I)
+      *reinterpret_cast<u32x2*>(a.out + (size_t)m * a.I + n) =
+          u32x2{pack_bf16x2(silu_mul(sg[0], su[0]), silu_mul(sg[1], su[1])),
+                pack_bf16x2(silu_mul(sg[2], su[2]), silu_mul(sg[3], su[3]))};
   }
-  if (m < a.M && n < a.I)
-    *reinterpret_cast<u32x2*>(a.out + (size_t)m * a.I + n) =
-        u32x2{pack_bf16x2(silu_mul(sg[0], su[0]), silu_mul(sg[1], su[1])),
-              pack_bf16x2(silu_mul(sg[2], su[2]), silu_mul(sg[3], su[3]))};
 }
 
 // out = bf16(sum of the splits, in their order); n a multiple of 8
@@ -496,11 +536,11 @@ hipError_t launch_gated(const GatedArgs& a, hipStream_t s) {
   }
   if (a.M <= kFewRows) {
     if (a.M <= 16)
-      gated_rows_kernel<1, 1><<<ceil_div_host(a.I, 16), 512, 0, s>>>(a);
+      gated_rows_kernel<1, 1><<<ceil_div_host(a.I, 16), 64 * kRowsWaves, 0, s>>>(a);
     else if (a.M <= 32)
-      gated_rows_kernel<2, 2><<<ceil_div_host(a.I, 32), 512, 0, s>>>(a);
+      gated_rows_kernel<2, 2><<<ceil_div_host(a.I, 32), 64 * kRowsWaves, 0, s>>>(a);
     else
-      gated_rows_kernel<4, 2><<<ceil_div_host(a.I, 32), 512, 0, s>>>(a);
+      gated_rows_kernel<4, 2><<<ceil_div_host(a.I, 32), 64 * kRowsWaves, 0, s>>>(a);
     return hipGetLastError();
   }
   TileArgs t{};

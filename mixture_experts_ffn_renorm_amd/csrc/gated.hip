@@ -456,6 +456,7 @@ __global__ __launch_bounds__(256) void zero_kernel(u32x4* p, size_t n) {
 
 using moe_host::ceil_div_host;
 
+constexpr int kTileCus = 256;          // CUs that tiles are counted for
 constexpr int kMaxSplits = 16;
 constexpr int kSplitTiles = 1024;
 constexpr int kSmallSplitTiles = 256;   // 512 and 1024: 5 and 12 % slower at 509 x 2048 x 1408
@@ -473,7 +474,7 @@ struct Plan {
 };
 Plan plan_of(int rows, int n_rows, int K, bool can_split) {
   Plan p{true, 128, 1, 0};
-  const int cu = 256;
+  const int cu = kTileCus;
   const long long big = (long long)ceil_div_host(rows, 256) * ceil_div_host(n_rows, 256);
   p.big = big >= cu / 2;
   const long long tiles =
@@ -491,11 +492,28 @@ Plan plan_of(int rows, int n_rows, int K, bool can_split) {
 }
 
 template <Op kOp>
-hipError_t launch_tiles(TileArgs a, int n_rows, const Plan& p, hipStream_t s) {
+hipError_t launch_tiles(TileArgs a, int n_rows, bool can_split, hipStream_t s) {
+  const Plan p = plan_of(a.rows, n_rows, a.K, can_split);
   a.splits = p.splits;
   a.k_per = p.k_per;
   a.tiles_m = ceil_div_host(a.rows, p.big ? 256 : p.bm);
   a.tiles_n = ceil_div_host(n_rows, p.big ? 256 : 128);
+  TileArgs rest = a;
+  const int last = a.tiles_m * a.tiles_n % kTileCus;
+  const int whole = a.tiles_m * a.tiles_n / kTileCus * kTileCus / a.tiles_n;   // rows of tiles
+  if (p.big && p.splits == 1 && whole > 0 && last > 0 && last <= kTileCus / 2) {
+    // a last round that leaves half the chip idle: its rows are a product of
+    // their own, of smaller tiles (4096 x 2048 x 5632, grad_w13: 352 tiles)
+    a.tiles_m = whole;
+    a.rows = whole * 256;
+    const size_t down = (size_t)a.rows;
+    rest.rows -= a.rows;
+    rest.m_side += kOp == kGradW ? down : down * rest.m_ld;
+    rest.out += down * rest.out_ld;
+    if (rest.grad_out != nullptr) rest.grad_out += down * rest.cols;
+  } else {
+    rest.rows = 0;
+  }
   const unsigned grid = (unsigned)ceil_div_host(a.tiles_m * a.tiles_n * a.splits, 8) * 8;
   if (p.big)
     tile_kernel<256, 256, 2, 4, 4, kOp><<<grid, 512, 0, s>>>(a);
@@ -508,7 +526,8 @@ hipError_t launch_tiles(TileArgs a, int n_rows, const Plan& p, hipStream_t s) {
     const unsigned g = (unsigned)std::min<size_t>((n / 8 + 255) / 256, 4096);
     join_kernel<<<g, 256, 0, s>>>(a.partial, p.splits, n, a.out);
   }
-  return hipGetLastError();
+  const hipError_t err = hipGetLastError();
+  return err != hipSuccess || rest.rows == 0 ? err : launch_tiles<kOp>(rest, n_rows, can_split, s);
 }
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -550,7 +569,7 @@ hipError_t launch_gated(const GatedArgs& a, hipStream_t s) {
   t.rows = a.M;
   t.cols = t.out_ld = a.I;
   t.out = a.out;
-  return launch_tiles<kAct>(t, 2 * a.I, plan_of(a.M, 2 * a.I, a.H, false), s);
+  return launch_tiles<kAct>(t, 2 * a.I, false, s);
 }
 
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t s) {
@@ -579,7 +598,7 @@ hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s) {
   t.grad_out = a.grad_out;
   t.out = d;
   t.out_ld = 2 * a.I;
-  hipError_t err = launch_tiles<kGradAct>(t, 2 * a.I, plan_of(a.M, 2 * a.I, a.H, false), s);
+  hipError_t err = launch_tiles<kGradAct>(t, 2 * a.I, false, s);
   if (err == hipSuccess && a.grad_x != nullptr) {
     TileArgs g{};
     g.m_side = d;
@@ -589,7 +608,7 @@ hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s) {
     g.rows = a.M;
     g.out = a.grad_x;
     g.partial = partial;
-    err = launch_tiles<kGradX>(g, a.H, plan_of(a.M, a.H, 2 * a.I, true), s);
+    err = launch_tiles<kGradX>(g, a.H, true, s);
   }
   if (err == hipSuccess && a.grad_w13 != nullptr) {
     TileArgs g{};
@@ -600,7 +619,7 @@ hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s) {
     g.K = a.M;
     g.out = a.grad_w13;
     g.partial = partial;
-    err = launch_tiles<kGradW>(g, a.H, plan_of(2 * a.I, a.H, a.M, true), s);
+    err = launch_tiles<kGradW>(g, a.H, true, s);
   }
   return err;
 }

@@ -91,7 +91,7 @@ def test_output_sizes(I, M):
 
 
 @pytest.mark.parametrize("M,H,I", [(1, 2048, 5632), (64, 2048, 5632), (509, 2048, 1408),
-                                   (2100, 256, 1500), (4100, 64, 520)])
+                                   (2100, 256, 1500), (4100, 64, 520), (2100, 64, 4096)])
 def test_layer_sizes(M, H, I):
     # (I multiple of 8)
     check(M, H, I // 8 * 8, 3)
@@ -195,7 +195,8 @@ def test_one_gradient_alone(M, need):
     check_grad(M, 264, 136, 4, need=need)
 
 
-@pytest.mark.parametrize("M,H,I", [(509, 2048, 1408), (2100, 256, 1504), (4099, 512, 264)])
+@pytest.mark.parametrize("M,H,I", [(509, 2048, 1408), (2100, 256, 1504), (4099, 512, 264),
+                                   (40, 2048, 5632), (2100, 64, 4096)])
 def test_gradient_layer_sizes(M, H, I):
     check_grad(M, H, I, 9)
 

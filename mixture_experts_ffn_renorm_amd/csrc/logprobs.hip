@@ -15,17 +15,18 @@
 // differences l - m.
 //
 // Alternatives: a wave collects the logits that reach a threshold in LDS.  The
-// threshold starts as the top-th largest of the lanes' first maxima (at least
-// `top` logits reach it) and rises to the top-th largest so far whenever the
-// list is cut back; a logit is looked at singly only in a 16-byte block whose
+// threshold is the top-th largest of the lanes' maxima so far (at least `top`
+// logits reach it), taken again after 1, 2, 4 ... groups, at first the best of
+// the four waves', and rises to the top-th largest so far whenever the list is
+// cut back; a logit is looked at singly only in a 16-byte block whose
 // maximum reaches the threshold.  Lists are cut by a bitwise search for a key
 // that exactly `top` entries reach (wave ballots), equal keys by their ids.
 //
-// 2048 rows of 131072 bf16 logits: 108 us without alternatives (5.0 TB/s, what
-// a large copy reaches), 136 us with 5, 166 us with 20; one row 5.4, 14 and 20
-// us, two launches and the searches' chains.  Without a prefetch a wave takes
-// 64 registers and a SIMD holds 8 of them, which hide the loads: 136 us against
-// 143 (4 waves at the least), and 179 with the next group's loads in flight.
+// 2048 rows of 131072 bf16 logits: 105 us without alternatives (5.1 TB/s, what
+// a large copy reaches), 112 us with 5, 153 us with 20; one row 5.7, 12 and 19
+// us, two launches and the searches' chains.  A threshold taken from the first
+// group alone: 136 and 166 us.  Without a prefetch a wave takes 64 registers and
+// a SIMD holds 8 of them, which hide the loads (4 waves at the least: 5 % more).
 #include <algorithm>
 
 #include "dense.h"
@@ -247,6 +248,7 @@ __global__ __launch_bounds__(kThreads, kMinWaves) void logprob_kernel(moe_host::
 #pragma clang fp contract(off)      // an anchor's product is the rounded one wherever it is used
   constexpr int kPer = Row<kBf16>::kPer;
   __shared__ float s_m[kWaves], s_a[kWaves], s_z[kWaves], s_s[kWaves];
+  __shared__ float s_t[kTop ? kWaves : 1];
   __shared__ int s_count[kWaves];
   __shared__ u64 s_list[kTop ? kWaves : 1][kTop ? kList : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -295,10 +297,12 @@ __global__ __launch_bounds__(kThreads, kMinWaves) void logprob_kernel(moe_host::
     count = cut<kBf16>(o, list, a.top, least, strict);
     if (count == a.top) T = topk_detail::key_logit(least);
   };
+  // cut lists raise the threshold: soon where few alternatives are wanted
+  const int keep = min(kKeep, 2 * a.top + 32);
   auto push = [&](bool hit, float l, int e) {
     const unsigned long long hits = __ballot(hit);
     if (hits == 0ull) return;
-    if (count > kKeep) cut_back();
+    if (count > keep) cut_back();
     if (hit) list[count + __popcll(hits & below)] = order_of(l, e);
     count += __popcll(hits);
   };
@@ -334,11 +338,17 @@ __global__ __launch_bounds__(kThreads, kMinWaves) void logprob_kernel(moe_host::
     s = __builtin_fmaf(f, __builtin_fmaf(d, z, s), gs);
     z = __builtin_fmaf(f, z, gz);
     if (kTop) {
-      if (g == 0) {
-        const uint32_t key[1] = {topk_detail::order_key(gm)};
+      if ((g & (g + 1)) == 0) {          // 0, 1, 3, 7, ...
+        const uint32_t key[1] = {topk_detail::order_key(mx)};
         int reach = 64;
         const uint32_t k = nth_key<31, kBf16 ? 16 : 0>(key, a.top, 0u, reach);
-        T = topk_detail::key_logit(max(k, kLeastKey));
+        T = fmaxf(T, topk_detail::key_logit(max(k, kLeastKey)));
+        if (g == 0) {                    // the best of the waves' serves them all
+          if (lane == 0) s_t[wave] = T;
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < kWaves; ++i) T = fmaxf(T, s_t[i]);
+        }
       }
       if (__ballot(gm >= T) != 0ull) {
         const bool whole = inner(g);
@@ -383,8 +393,8 @@ __global__ __launch_bounds__(kThreads, kMinWaves) void logprob_kernel(moe_host::
     }
   }
   if (kTop) {
+    if (count > kKeep) cut_back();
     lds_order();
-    if (count > a.top) cut_back();
     if (lane == 0) s_count[wave] = count;
   }
 
@@ -446,15 +456,28 @@ __global__ __launch_bounds__(kThreads, kMinWaves) void logprob_kernel(moe_host::
   }
   int kept = 0;
   if (kTop) {
-    // the waves' lists, each at most `top` long
-    u64 o[kWaves * kMaxTop / 64];
+    // the waves' lists, each at most kKeep long, one after another
+    int total = 0, from_wave = 0, from_at = lane;
 #pragma unroll
-    for (int i = 0; i < kWaves * kMaxTop / 64; ++i) {
-      const int q = i * 64 + lane, w = q / kMaxTop, at = q % kMaxTop;
-      o[i] = at < s_count[w] ? s_list[kTop ? w : 0][kTop ? at : 0] : 0ull;
+    for (int w = 0; w < kWaves; ++w) {
+      const int n = s_count[w];
+      if (lane >= total + n && w + 1 < kWaves) {
+        from_wave = w + 1;
+        from_at = lane - total - n;
+      }
+      total += n;
     }
     uint32_t least;
-    kept = cut<kBf16>(o, list, a.top, least, strict);
+    if (total <= 64) {
+      const u64 o[1] = {lane < total ? s_list[kTop ? from_wave : 0][kTop ? from_at : 0] : 0ull};
+      kept = cut<kBf16>(o, list, a.top, least, strict);
+    } else {
+      u64 o[kWaves];
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+        o[w] = lane < s_count[w] ? s_list[kTop ? w : 0][kTop ? lane : 0] : 0ull;
+      kept = cut<kBf16>(o, list, a.top, least, strict);
+    }
   }
   if (chunks == 1) {
     finish<kBf16>(a, m, M, z, s, list, kept);

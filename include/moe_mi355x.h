@@ -562,8 +562,8 @@ int moe_linear_quantized(const uint16_t* x, const moe_quantized_matrix* w, int M
  *   x [M, H], w13 [2I, H] (gate rows first, as one expert's W13), out [M, I],
  *   bf16; out overlaps no operand
  * One or two launches, no workspace.  H and I multiples of 8, at most 2^17;
- * M < 2^21.  A row of x that is not finite gives results that are not finite in its own
- * row of out and in no other.
+ * M < 2^21.  A row of x that is not finite gives results that are not finite
+ * in its own row of out and in no other.
  */
 int moe_linear_gated(const uint16_t* x, const uint16_t* w13, int M, int H, int I, uint16_t* out,
                      void* stream);

@@ -526,7 +526,7 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(moe_host::LogprobArgs 
 // whole groups of a workgroup's loads, as many chunks as fill the chip.
 int row_blocks(int V, int bf16) {
   const int per = bf16 ? 8 : 4;
-  return (V + 2 * (per - 1)) / per;
+  return V % per == 0 ? V / per : (V + 2 * (per - 1)) / per;
 }
 int chunk_blocks_of(int M, int V, int bf16) {
   const int groups = moe_host::ceil_div_host(row_blocks(V, bf16), kGroup);

@@ -196,7 +196,7 @@ def test_one_gradient_alone(M, need):
 
 
 @pytest.mark.parametrize("M,H,I", [(509, 2048, 1408), (2100, 256, 1504), (4099, 512, 264),
-                                   (40, 2048, 5632), (2100, 64, 4096)])
+                                   (40, 2048, 5632), (2100, 64, 4096), (2100, 8192, 8)])
 def test_gradient_layer_sizes(M, H, I):
     check_grad(M, H, I, 9)
 

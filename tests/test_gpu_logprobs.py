@@ -132,6 +132,14 @@ def test_ties_go_to_the_lower_id(V, dtype):
     check(l, dtype, 32)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [300, 20011, 131072])
+def test_rows_in_order(V, dtype):
+    """Every logit passes the threshold of those before it, or none does."""
+    up = np.linspace(-6, 6, V, dtype=np.float32)
+    check(np.stack([up, up[::-1], -np.abs(up), np.abs(up)]), dtype, 20)
+
+
 LOWEST = {"bfloat16": -3.3895313892515355e38, "float32": np.finfo(np.float32).min}
 
 

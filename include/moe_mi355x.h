@@ -629,10 +629,10 @@ size_t moe_linear_adapters_workspace_size(int M, int K, int R);
  *   out    bf16 out, overlapping no input but an addend that is out itself
  *   workspace  moe_linear_adapters_workspace_size(M, K, R) bytes, 16-byte
  *          aligned, overlapping no operand
- * Two launches, three above 128 rows (rows are grouped by adapter there).  K
- * and N multiples of 8 (gated: N of 16), at most 2^17; M < 2^21.  Sums are
- * fp32; x A^T keeps at least 16 bits between the two products.  A row's result depends on no
- * other row.
+ * One or two launches, three above 128 rows (rows are grouped by adapter
+ * there).  K and N multiples of 8 (gated: N of 16), at most 2^17; M < 2^21.
+ * Sums are fp32; x A^T keeps at least 16 bits between the two products.  A
+ * row's result depends on no other row.
  */
 int moe_linear_adapters(const uint16_t* x, const moe_adapters* adapters, const int32_t* slots,
                         int M, int K, int N, int gated, const uint16_t* addend, uint16_t* out,

@@ -22,6 +22,7 @@ constexpr int kWindow = 8192;          // tokens that one workgroup groups
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanTokens = kWindow / kPlanThreads;
 constexpr int kMaxSlots = 4096;
+constexpr int kMaxRank = 128;
 
 struct Unit {
   int slot;      // S: no adapter
@@ -103,6 +104,78 @@ __global__ __launch_bounds__(256) void expand_gemv_kernel(AdapterArgs a,
     if (kGated) y[1] += bf16_at(p + n_out);
   }
   a.out[(size_t)m * n_out + n] = (uint16_t)f32_to_bf16(kGated ? silu_mul(y[0], y[1]) : y[0]);
+}
+
+// Both steps in one launch, with the same sums: each workgroup of 256 columns forms t by itself, B's
+// first rows on their way meanwhile.
+template <bool kGated>
+__global__ __launch_bounds__(256) void adapters_gemv_kernel(AdapterArgs a) {
+  constexpr int kHalves = kGated ? 2 : 1, kAhead = 4;
+  __shared__ __attribute__((aligned(16))) float s_t[kMaxRank];
+  const int n_out = kGated ? a.N / 2 : a.N;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
+  const int s = a.slots[m];
+  float y[kHalves];
+#pragma unroll
+  for (int h = 0; h < kHalves; ++h) y[h] = 0.f;
+  if (s >= 0 && s < a.S) {
+    const uint16_t* b[kHalves];
+    u32x4 first[kHalves][kAhead];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      b[h] = a.b + ((size_t)s * a.N + min(n, n_out - 1) + h * n_out) * a.R;
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) first[h][q] = load16_or_zero(b[h] + 8 * q, 8 * q < a.R);
+    }
+    const uint16_t* x = a.x + (size_t)m * a.K;
+    const float scale = a.scales != nullptr ? a.scales[s] : 1.f;
+    for (int r0 = wave * 4; r0 < a.R; r0 += 16) {
+      const uint16_t* A = a.a + ((size_t)s * a.R + r0) * a.K;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int k = lane * 8; k < a.K; k += 512) {
+        const u32x4 xv = load16(x + k);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const u32x4 av = load16(A + (size_t)r * a.K + k);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sum[r] = __builtin_fmaf(bf16_lo(xv[j]), bf16_lo(av[j]), sum[r]);
+            sum[r] = __builtin_fmaf(bf16_hi(xv[j]), bf16_hi(av[j]), sum[r]);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float v = wave_sum(sum[r]);
+        if (lane == 0) s_t[r0 + r] = v * scale;
+      }
+    }
+    __syncthreads();
+    auto add = [&](int h, const u32x4& v, int r) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[h] = __builtin_fmaf(s_t[r + 2 * j], bf16_lo(v[j]), y[h]);
+        y[h] = __builtin_fmaf(s_t[r + 2 * j + 1], bf16_hi(v[j]), y[h]);
+      }
+    };
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+        if (8 * q < a.R) add(h, first[h][q], 8 * q);
+      for (int r = 8 * kAhead; r < a.R; r += 8) add(h, load16(b[h] + r), r);
+    }
+  }
+  if (n >= n_out) return;
+  if (a.addend != nullptr) {
+    const uint16_t* p = a.addend + (size_t)m * a.N + n;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) y[h] += bf16_at(p + h * n_out);
+  }
+  a.out[(size_t)m * n_out + n] =
+      (uint16_t)f32_to_bf16(kGated ? silu_mul(y[0], y[kHalves - 1]) : y[0]);
 }
 
 // ---- tokens grouped by slot ----
@@ -391,6 +464,12 @@ constexpr int kManyTokens = 1024;
 // of rank 64 43 us against 31.
 constexpr int kGemvTokens = 128;
 
+// One launch where an adapter's A has at most kOneLaunchA bytes (a wave then
+// reads its rows at once) and all workgroups' reading of it kOneLaunchAll: rank
+// 16, 2048 -> 2048 columns, 1 to 64 tokens 8.7 us a call against 11.4, 5.2 to
+// 5.6 on the GPU either way; rank 64 13.4 against 5.4.
+constexpr long long kOneLaunchA = 64 << 10, kOneLaunchAll = 64 << 20;
+
 struct Layout {
   int windows, cap;        // of the grouping; units of a window
   size_t order, units, t, total;
@@ -446,6 +525,14 @@ hipError_t launch_adapters(const AdapterArgs& a, hipStream_t s) {
     float* t = reinterpret_cast<float*>(ws + l.t);
     const int n_out = a.gated ? a.N / 2 : a.N;
     const dim3 grid((unsigned)ceil_div_host(n_out, 256), (unsigned)a.M);
+    const long long bytes = (long long)a.R * a.K * 2;
+    if (bytes <= kOneLaunchA && bytes * grid.x * a.M <= kOneLaunchAll) {
+      if (a.gated)
+        adapters_gemv_kernel<true><<<grid, 256, 0, s>>>(a);
+      else
+        adapters_gemv_kernel<false><<<grid, 256, 0, s>>>(a);
+      return hipGetLastError();
+    }
     shrink_gemv_kernel<2><<<ceil_div_host(a.M * (a.R / 2), 4), 256, 0, s>>>(a, t);
     if (a.gated)
       expand_gemv_kernel<true><<<grid, 256, 0, s>>>(a, t);

@@ -167,6 +167,15 @@ def test_many_rows(order):
     check(20000, 30, 16, 24, 24, order, seed=2)
 
 
+@pytest.mark.parametrize("M", [1, 7])
+@pytest.mark.parametrize("R,K,N", [(16, 2048, 2048), (16, 2056, 2048), (128, 256, 528), (128, 264, 528),
+                                   (40, 800, 272), (8, 4096, 4112)])
+def test_one_and_two_launches(R, K, N, M):
+    """At the border of the one-launch form, and just past it."""
+    for gated in (False, True):
+        check(M, 3, R, K, N, seed=R, gated=gated)
+
+
 @pytest.mark.parametrize("M,order", [(64, "random"), (1000, "runs"), (700, "random")])
 def test_layer_sizes(M, order):
     check(M, 8, 64, 2048, 2048, order, seed=1)

@@ -164,8 +164,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
   ln.init(a.n_side, a.n_ld, k0,
           [&](int r) {
             if (!kGated) return min(n0 + r, a.cols - 1);
-            // a wave's TN rows: TN/2 gates, then their ups
-            const int q = r % TN, f = min(n0 + r / TN * (TN / 2) + q % (TN / 2), a.cols - 1);
+            // a wave's TN rows: TN/2 gates, then their ups; row i of fragment h of a
+            // half is feature 8 (i / 4) + 4 h + i % 4, so that a lane holds 8
+            // consecutive ones
+            const int q = r % TN, h = q % (TN / 2) / 16, i = q % 16;
+            const int f = min(n0 + r / TN * (TN / 2) + 8 * (i >> 2) + 4 * h + (i & 3), a.cols - 1);
             return q < TN / 2 ? f : a.cols + f;
           },
           n0, a.cols, wave, lane);
@@ -223,35 +226,41 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
   if (kHalves && wave < W / 2) barrier_nofence();
   wait_vmem<0>();                      // the copies past the end
 
-  // a lane holds 4 consecutive n of one m
+  // a lane holds 4 consecutive n of one m, gated 8 features
   const int ml = m0 + wm * TM + (lane & 15), nq = 4 * (lane >> 4);
 #pragma unroll
   for (int j = 0; j < FM; ++j) {
     const int m = ml + j * 16;
     if (m >= a.rows) continue;
     if (kGated) {
+      static_assert(!kGated || FN == 4, "two fragments of gates, two of ups");
+      const int n = n0 + wn * (TN / 2) + 2 * nq;
+      if (n >= a.cols) continue;
+      const size_t at = (size_t)m * a.out_ld + n;
+      if (kOp == kAct) {
+        u32x4 o;
 #pragma unroll
-      for (int i = 0; i < FN / 2; ++i) {
-        const int n = n0 + wn * (TN / 2) + i * 16 + nq;
-        if (n >= a.cols) continue;
-        const f32x4 g = acc[i][j], u = acc[i + FN / 2][j];
-        if (kOp == kAct) {
-          u32x2 o;
-          o[0] = pack_bf16x2(silu_mul(g[0], u[0]), silu_mul(g[1], u[1]));
-          o[1] = pack_bf16x2(silu_mul(g[2], u[2]), silu_mul(g[3], u[3]));
-          *reinterpret_cast<u32x2*>(a.out + (size_t)m * a.out_ld + n) = o;
-        } else {
-          const u32x2 d = *reinterpret_cast<const u32x2*>(a.grad_out + (size_t)m * a.cols + n);
-          float dg[4], du[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            gated_grad(g[r], u[r], r & 1 ? bf16_hi(d[r >> 1]) : bf16_lo(d[r >> 1]), dg[r], du[r]);
-          uint16_t* o = a.out + (size_t)m * a.out_ld + n;
-          *reinterpret_cast<u32x2*>(o) =
-              u32x2{pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3])};
-          *reinterpret_cast<u32x2*>(o + a.cols) =
-              u32x2{pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3])};
+        for (int r = 0; r < 4; ++r) {
+          const f32x4 g = acc[r >> 1][j], u = acc[2 + (r >> 1)][j];
+          const int e = 2 * (r & 1);
+          o[r] = pack_bf16x2(silu_mul(g[e], u[e]), silu_mul(g[e + 1], u[e + 1]));
         }
+        *reinterpret_cast<u32x4*>(a.out + at) = o;
+      } else {
+        const u32x4 d = load16(a.grad_out + (size_t)m * a.cols + n);
+        u32x4 og, ou;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const f32x4 g = acc[r >> 1][j], u = acc[2 + (r >> 1)][j];
+          const int e = 2 * (r & 1);
+          float dg[2], du[2];
+          gated_grad(g[e], u[e], bf16_lo(d[r]), dg[0], du[0]);
+          gated_grad(g[e + 1], u[e + 1], bf16_hi(d[r]), dg[1], du[1]);
+          og[r] = pack_bf16x2(dg[0], dg[1]);
+          ou[r] = pack_bf16x2(du[0], du[1]);
+        }
+        *reinterpret_cast<u32x4*>(a.out + at) = og;
+        *reinterpret_cast<u32x4*>(a.out + at + a.cols) = ou;
       }
     } else {
 #pragma unroll

@@ -39,10 +39,10 @@ def bounds(l):
     them.  So z is off by (3 A + 162) U relatively, A = sum p |x|, and with
     one more product per term s = sum p x by sum p |x| (6 |x| + 165) U.
     """
-    l = l.astype(np.float64)
+    l = np.where(np.isnan(l).any(axis=1, keepdims=True), 0.0, l.astype(np.float64))   # NaN rows: any
     m = l.max(axis=1, keepdims=True)
     m = np.where(np.isfinite(m), m, 0.0)
-    x = np.maximum(l - m, -800.0)
+    x = np.clip(l - m, -800.0, 0.0)
     p = np.exp(x)
     z = p.sum(axis=1)
     z = np.where(z > 0, z, 1.0)

@@ -19,11 +19,12 @@
 // logits reach it), taken again after 1, 2, 4 ... groups, at first the best of
 // the four waves', and rises to the top-th largest so far whenever the list is
 // cut back; a logit is looked at singly only in a 16-byte block whose
-// maximum reaches the threshold.  Lists are cut by a bitwise search for a key
-// that exactly `top` entries reach (wave ballots), equal keys by their ids.
+// maximum reaches the threshold.  Lists that grow are cut by a bitwise search for
+// a key that exactly `top` entries reach (wave ballots), equal keys by their ids;
+// the last 64 entries or fewer are ranked against each other.
 //
-// 2048 rows of 131072 bf16 logits: 105 us without alternatives (5.1 TB/s, what
-// a large copy reaches), 112 us with 5, 153 us with 20; one row 5.7, 12 and 19
+// 2048 rows of 131072 bf16 logits: 106 us without alternatives (5.1 TB/s, what
+// a large copy reaches), 116 us with 5, 154 us with 20; one row 5.4, 11 and 18
 // us, two launches and the searches' chains.  A threshold taken from the first
 // group alone: 136 and 166 us.  Without a prefetch a wave takes 64 registers and
 // a SIMD holds 8 of them, which hide the loads (4 waves at the least: 5 % more).
@@ -146,8 +147,9 @@ __device__ __forceinline__ void lds_order() {   // of one wave's LDS accesses
 // Keeps the n largest of the wave's entries (0: none), in no order, in `to`;
 // returns how many there are.  `least`: a key that they all reach and, if
 // `strict`, that later entries (of higher ids) have to pass to replace one;
-// at most -inf's key if fewer than n are kept.
-template <bool kBf16, int NB>
+// at most -inf's key if fewer than n are kept.  kLoose: up to 64 entries that
+// reach the n-th largest key are all kept.
+template <bool kBf16, bool kLoose, int NB>
 __device__ __forceinline__ int cut(const u64 (&o)[NB], u64* to, int n, uint32_t& least,
                                    bool& strict) {
   const int lane = threadIdx.x & 63;
@@ -161,10 +163,10 @@ __device__ __forceinline__ int cut(const u64 (&o)[NB], u64* to, int n, uint32_t&
   // all 1 below 0
   int reach = topk_detail::count_ge(key, 1u);
   uint32_t T = nth_key<31, kBf16 ? 16 : 0>(key, n, 0u, reach);
-  if (kBf16 && reach > n && !(T & 0x80000000u)) T |= 0xFFFFu;
   uint32_t low_least = 0u;
-  strict = reach > n;
+  strict = reach > n && !(kLoose && reach <= 64);
   if (strict) {
+    if (kBf16 && !(T & 0x80000000u)) T |= 0xFFFFu;
     // of the entries that equal T the lower ids, which are the larger low words
     const int above = topk_detail::count_ge(key, T + 1u);
 #pragma unroll
@@ -187,34 +189,56 @@ __device__ __forceinline__ int cut(const u64 (&o)[NB], u64* to, int n, uint32_t&
   return at;
 }
 
-// What a chunk of a row leaves for the row's join.
+// The place of an entry among `count` different ones in LDS: 0 for the largest.
+__device__ __forceinline__ int rank_of(const u64* list, int count, u64 o) {
+  int r = 0;
+#pragma unroll 8
+  for (int i = 0; i < count; ++i) r += list[i] > o;
+  return r;
+}
+
+// What a chunk of a row leaves for the row's join, kFill of them at most; then
+// the lists, `top` entries a chunk (0: none).
 struct Partial {
   float m;       // largest logit (NaN aside)
   float z, s;    // sums of e = 2^y and y e, y = (l - m) log2 e (m = -inf: of l)
-  int count;     // alternatives that follow, in no order
+  float pad;
 };
-__host__ __device__ inline size_t partial_stride(int top) {
-  return sizeof(Partial) + (size_t)((top + 1) & ~1) * 8;
+__host__ __device__ inline u64* lists_of(void* partial) {
+  return reinterpret_cast<u64*>(static_cast<uint8_t*>(partial) + kFill * sizeof(Partial));
 }
 
-// A row's results, by one wave: its largest logit, sums, and the `count`
-// alternatives in LDS, in no order.
+// A logit of a row, and that of its token.
 template <bool kBf16>
-__device__ __forceinline__ void finish(const moe_host::LogprobArgs& a, int m, float M, float z,
-                                       float s, const u64* list, int count) {
+__device__ __forceinline__ float logit_at(const moe_host::LogprobArgs& a, int m, int v) {
+  const size_t at = (size_t)m * a.V + v;
+  return kBf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.logits)[at] << 16)
+               : static_cast<const float*>(a.logits)[at];
+}
+struct Asked {
+  bool is;       // the token is one of the row's
+  float l;
+};
+template <bool kBf16>
+__device__ __forceinline__ Asked asked_of(const moe_host::LogprobArgs& a, int m) {
+  const int t = a.tokens[m];
+  Asked k{t >= 0 && t < a.V, 0.f};
+  if (k.is) k.l = logit_at<kBf16>(a, m, t);
+  return k;
+}
+
+// A row's results, by one wave: its largest logit, sums, and `count` entries in
+// LDS (at most 64, in no order) that hold its alternatives.
+template <bool kBf16>
+__device__ __forceinline__ void finish(const moe_host::LogprobArgs& a, int m, const Asked& asked,
+                                       float M, float z, float s, const u64* list, int count) {
   const int lane = threadIdx.x & 63;
-  const uint16_t* l16 = static_cast<const uint16_t*>(a.logits) + (size_t)m * a.V;
-  const float* l32 = static_cast<const float*>(a.logits) + (size_t)m * a.V;
-  auto logit = [&](int v) {
-    return kBf16 ? __uint_as_float((uint32_t)l16[v] << 16) : l32[v];
-  };
   // no logit above -inf: nothing is likely, nothing uncertain
   const bool none = z == 0.f;
   const float lz = logf(z);
   auto logprob = [&](float l) { return none ? -INFINITY : l - M - lz; };
   if (lane == 0) {
-    const int t = a.tokens[m];
-    a.logprobs[m] = t >= 0 && t < a.V ? logprob(logit(t)) : 0.f;
+    a.logprobs[m] = asked.is ? logprob(asked.l) : 0.f;
     a.entropy[m] = none ? 0.f : lz - kLn2 * (s / z);
     a.lse[m] = none ? -INFINITY : M + lz;
   }
@@ -222,15 +246,16 @@ __device__ __forceinline__ void finish(const moe_host::LogprobArgs& a, int m, fl
   const size_t to = (size_t)m * a.top;
   if (lane < count) {
     const u64 o = list[lane];
-    int r = 0;
-    for (int i = 0; i < count; ++i) r += list[i] > o;
-    a.top_ids[to + r] = id_of(o);
-    a.top_logprobs[to + r] = logprob(logit_of(o));
+    const int r = rank_of(list, count, o);
+    if (r < a.top) {
+      a.top_ids[to + r] = id_of(o);
+      a.top_logprobs[to + r] = logprob(logit_of(o));
+    }
   }
   // fewer than `top` logits are numbers: NaN follows, by id
   const unsigned long long below = (1ull << lane) - 1ull;
   for (int v0 = 0; v0 < a.V && count < a.top; v0 += 64) {
-    const float l = v0 + lane < a.V ? logit(v0 + lane) : 0.f;
+    const float l = v0 + lane < a.V ? logit_at<kBf16>(a, m, v0 + lane) : 0.f;
     const unsigned long long nan = __ballot(l != l);
     const int at = count + __popcll(nan & below);
     if (l != l && at < a.top) {
@@ -281,6 +306,8 @@ __global__ __launch_bounds__(kThreads, kMinWaves) void logprob_kernel(moe_host::
       }
     }
   };
+  Asked asked{false, 0.f};
+  if (chunks == 1 && wave == 0) asked = asked_of<kBf16>(a, m);
   const int groups = ceil_div(b1 - b0, kGroup);
   float mx = -INFINITY, from = -kFar, m2 = -kFar * kLog2e, z = 0.f, s = 0.f;
   float T = -INFINITY;
@@ -294,7 +321,7 @@ __global__ __launch_bounds__(kThreads, kMinWaves) void logprob_kernel(moe_host::
     lds_order();
 #pragma unroll
     for (int i = 0; i < kList / 64; ++i) o[i] = 64 * i + lane < count ? list[64 * i + lane] : 0ull;
-    count = cut<kBf16>(o, list, a.top, least, strict);
+    count = cut<kBf16, false>(o, list, a.top, least, strict);
     if (count == a.top) T = topk_detail::key_logit(least);
   };
   // cut lists raise the threshold: soon where few alternatives are wanted
@@ -467,50 +494,56 @@ __global__ __launch_bounds__(kThreads, kMinWaves) void logprob_kernel(moe_host::
       }
       total += n;
     }
-    uint32_t least;
     if (total <= 64) {
-      const u64 o[1] = {lane < total ? s_list[kTop ? from_wave : 0][kTop ? from_at : 0] : 0ull};
-      kept = cut<kBf16>(o, list, a.top, least, strict);
+      const u64 o = lane < total ? s_list[kTop ? from_wave : 0][kTop ? from_at : 0] : 0ull;
+      lds_order();
+      if (lane < total) list[lane] = o;
+      lds_order();
+      kept = total;
     } else {
       u64 o[kWaves];
+      uint32_t least;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w)
         o[w] = lane < s_count[w] ? s_list[kTop ? w : 0][kTop ? lane : 0] : 0ull;
-      kept = cut<kBf16>(o, list, a.top, least, strict);
+      kept = cut<kBf16, true>(o, list, a.top, least, strict);
     }
   }
   if (chunks == 1) {
-    finish<kBf16>(a, m, M, z, s, list, kept);
+    finish<kBf16>(a, m, asked, M, z, s, list, kept);
     return;
   }
-  uint8_t* part = static_cast<uint8_t*>(a.partial) + (size_t)blockIdx.x * partial_stride(a.top);
-  if (lane == 0) *reinterpret_cast<Partial*>(part) = Partial{M, z, s, kept};
-  if (kTop && lane < kept) reinterpret_cast<u64*>(part + sizeof(Partial))[lane] = list[lane];
+  if (lane == 0) static_cast<Partial*>(a.partial)[blockIdx.x] = Partial{M, z, s, 0.f};
+  if (kTop) {
+    u64* to = lists_of(a.partial) + (size_t)blockIdx.x * a.top;
+    if (lane < kept) {
+      const u64 o = list[lane];
+      const int r = rank_of(list, kept, o);
+      if (r < a.top) to[r] = o;
+    } else if (lane < a.top) {
+      to[lane] = 0ull;
+    }
+  }
 }
 
 // ---- a row's chunks joined: one wave a row, lane c holding chunk c's sums ----
 template <bool kBf16, int NB>
 __global__ __launch_bounds__(64) void logprob_join_kernel(moe_host::LogprobArgs a, int chunks) {
-  __shared__ u64 s_list[kMaxTop];
+  __shared__ u64 s_list[64];
   const int m = blockIdx.x, lane = threadIdx.x;
-  const size_t stride = partial_stride(a.top);
-  const uint8_t* parts = static_cast<const uint8_t*>(a.partial) + (size_t)m * chunks * stride;
-  Partial p{-INFINITY, 0.f, 0.f, 0};
-  if (lane < chunks) p = *reinterpret_cast<const Partial*>(parts + lane * stride);
+  const Asked asked = asked_of<kBf16>(a, m);
+  Partial p{-INFINITY, 0.f, 0.f, 0.f};
+  if (lane < chunks) p = static_cast<const Partial*>(a.partial)[(size_t)m * chunks + lane];
   int kept = 0;
   if (NB > 0) {
     u64 o[NB > 0 ? NB : 1];
     const int all = chunks * a.top;
+    const u64* lists = lists_of(a.partial) + (size_t)m * all;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int q = i * 64 + lane, c = min(q / a.top, chunks - 1), at = q % a.top;
-      const u64 v = reinterpret_cast<const u64*>(parts + c * stride + sizeof(Partial))[at];
-      const int n = __shfl(p.count, c, kWave);         // by all lanes
-      o[i] = q < all && at < n ? v : 0ull;
-    }
+    for (int i = 0; i < NB; ++i) o[i] = i * 64 + lane < all ? lists[i * 64 + lane] : 0ull;
     uint32_t least;
     bool strict;
-    kept = cut<kBf16>(o, s_list, a.top, least, strict);
+    kept = cut<kBf16, true>(o, s_list, a.top, least, strict);
   }
   const float M = wave_max(p.m);
   // a chunk without a logit above -inf adds 0 (or its NaN) as it is, one far
@@ -519,7 +552,7 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(moe_host::LogprobArgs 
   const float f = __builtin_amdgcn_exp2f(d);
   const float z = wave_sum(p.z * f);
   const float s = wave_sum(f > 0.f ? f * __builtin_fmaf(d, p.z, p.s) : 0.f * p.z);
-  finish<kBf16>(a, m, M, z, s, s_list, kept);
+  finish<kBf16>(a, m, asked, M, z, s, s_list, kept);
 }
 
 // Blocks of 16 bytes that a row touches at most, and the length of a chunk:
@@ -623,7 +656,9 @@ __global__ __launch_bounds__(256) void logprob_backward_kernel(moe_host::Logprob
 
 namespace moe_host {
 
-size_t logprob_partial_bytes(int top) { return (size_t)kFill * partial_stride(top); }
+size_t logprob_partial_bytes(int top) {
+  return (size_t)kFill * (sizeof(Partial) + (size_t)top * sizeof(u64));
+}
 
 hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t s) {
   if (a.bf16)

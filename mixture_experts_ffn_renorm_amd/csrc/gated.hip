@@ -8,14 +8,13 @@
 // as the matrix cores take them; every sum is fp32.
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "dense.h"
 
 using namespace moe;
 
 namespace {
-
-constexpr int kBK = 32;            // elements of the summed axis per stage
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -40,12 +39,14 @@ struct TileArgs {
   float* partial;            // splits > 1: [splits, rows, cols]
 };
 
-// Swizzles of the LDS tiles, in 16-byte pieces.  Rows of 32 k (64 bytes):
-// piece c of row r lies at c ^ (r / 2 % 4), so that eight rows of one beat of
-// a 16-byte read lie in different banks.  Rows of R columns: the pairs of
-// pieces are exchanged by the bits of k in which the lanes of a transposing
-// read differ.
-__device__ __forceinline__ int along_swizzle(int r) { return (r >> 1) & 3; }
+// Swizzles of the LDS tiles, in 16-byte pieces.  Rows of kK k: piece c of row r
+// lies at c ^ (r / 2 % pieces), so that the rows of one beat of a 16-byte read
+// lie in different banks.  Rows of R columns: the pairs of pieces are exchanged
+// by the bits of k in which the lanes of a transposing read differ.
+template <int kK>
+__device__ __forceinline__ int along_swizzle(int r) {
+  return (r >> 1) & (kK / 8 - 1);
+}
 __device__ __forceinline__ int across_swizzle(int k) { return ((k & 3) | ((k >> 1) & 4)) << 1; }
 
 // load_lds16 whose completion the kernel waits for itself (wait_vmem): the
@@ -60,10 +61,10 @@ __device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
                : "memory");
 }
 
-// The loads of one operand's stages: R rows by kBK k, by W waves.
-template <int R, int W, bool kAcross>
+// The loads of one operand's stages: R rows by kK k, by W waves.
+template <int R, int kK, int W, bool kAcross>
 struct Loader {
-  static constexpr int kInstr = R * kBK * 2 / 1024 / W;   // 1 KB each
+  static constexpr int kInstr = R * kK * 2 / 1024 / W;   // 1 KB each
   const uint8_t* src[kInstr];
   int k[kInstr];             // k of the lane's piece within a stage
   size_t step;
@@ -82,12 +83,14 @@ struct Loader {
         const int col = min(c0 + c * 8, ncols - 8);
         src[i] = reinterpret_cast<const uint8_t*>(p + (size_t)(k0 + k[i]) * ld + col);
       } else {
-        const int r = q * 16 + (lane >> 2), c = (lane & 3) ^ along_swizzle(r);
+        constexpr int kPieces = kK / 8;                   // per row
+        const int r = q * (64 / kPieces) + lane / kPieces;
+        const int c = (lane % kPieces) ^ along_swizzle<kK>(r);
         k[i] = c * 8;
         src[i] = reinterpret_cast<const uint8_t*>(p + (size_t)row(r) * ld + k0 + k[i]);
       }
     }
-    step = kAcross ? (size_t)kBK * ld * 2 : kBK * 2;
+    step = kAcross ? (size_t)kK * ld * 2 : kK * 2;
   }
   // The next stage into LDS; `left` elements of k are there from its first on
   // (none or fewer: zeros).
@@ -102,7 +105,7 @@ struct Loader {
 };
 
 // Fragments (16 rows by 32 k) of one operand's LDS tile.
-template <int R, bool kAcross>
+template <int R, int kK, bool kAcross>
 struct Reader {
   int base, col, swz;        // bytes
   __device__ __forceinline__ Reader(int row0, int lane) {
@@ -113,19 +116,21 @@ struct Reader {
       col = row0 * 2 + ((i & 2) << 3);
       swz = across_swizzle(k) * 16;
     } else {
-      base = (row0 + i) * 64 + ((g ^ along_swizzle(i)) << 4);
-      col = swz = 0;
+      base = (row0 + i) * kK * 2;
+      col = g * 16;
+      swz = along_swizzle<kK>(i) * 16;
     }
   }
-  __device__ __forceinline__ u32x4 read(const uint8_t* lds, int f) const {
+  // fragment f of rows, of the 32 k at 32 s
+  __device__ __forceinline__ u32x4 read(const uint8_t* lds, int f, int s) const {
     if (kAcross) {
-      const uint8_t* p = lds + base + ((col + f * 32) ^ swz);
+      const uint8_t* p = lds + base + s * 64 * R + ((col + f * 32) ^ swz);
       const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
       const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * R * 2));
       const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
       return u32x4{x[0], x[1], y[0], y[1]};
     }
-    return load16(lds + base + f * 1024);
+    return load16(lds + base + ((col + s * 64) ^ swz) + f * (32 * kK));
   }
 };
 
@@ -136,12 +141,18 @@ __device__ __forceinline__ void gated_grad(float g, float u, float d, float& dg,
   dg = d * u * (s * (1.0f + g * (1.0f - s)));
 }
 
-template <int BM, int BN, int WM, int WN, int kStages, Op kOp>
+// f(0), f(1), ... as constants
+template <class F, int... i>
+__device__ __forceinline__ void each(std::integer_sequence<int, i...>, const F& f) {
+  (f(std::integral_constant<int, i>{}), ...);
+}
+
+template <int BM, int BN, int kK, int WM, int WN, int kStages, Op kOp>
 __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
   constexpr int W = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr bool kGated = kOp == kAct || kOp == kGradAct;
   constexpr bool kMAcross = kOp == kGradW, kNAcross = kOp == kGradX || kOp == kGradW;
-  constexpr int kMBytes = BM * kBK * 2, kStage = (BM + BN) * kBK * 2;
+  constexpr int kMBytes = BM * kK * 2, kStage = (BM + BN) * kK * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * kStage];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -157,8 +168,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
   const int n0 = tn * (kGated ? BN / 2 : BN);
   const int k0 = split * a.k_per, K = min(a.K - k0, a.k_per);
 
-  Loader<BM, W, kMAcross> lm;
-  Loader<BN, W, kNAcross> ln;
+  Loader<BM, kK, W, kMAcross> lm;
+  Loader<BN, kK, W, kNAcross> ln;
   lm.init(a.m_side, a.m_ld, k0, [&](int r) { return min(m0 + r, a.rows - 1); }, m0, a.rows, wave,
           lane);
   ln.init(a.n_side, a.n_ld, k0,
@@ -172,8 +183,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
             return q < TN / 2 ? f : a.cols + f;
           },
           n0, a.cols, wave, lane);
-  const Reader<BM, kMAcross> rm(wm * TM, lane);
-  const Reader<BN, kNAcross> rn(wn * TN, lane);
+  const Reader<BM, kK, kMAcross> rm(wm * TM, lane);
+  const Reader<BN, kK, kNAcross> rn(wn * TN, lane);
 
   f32x4 acc[FN][FM];
 #pragma unroll
@@ -183,48 +194,63 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
 
   // Stage kt of K, while the stages behind it are on their way: fragments to
   // registers, the copies of stage kt + kStages - 1 sent into the LDS of stage
-  // kt - 1, which every wave has read (past the end: of zeros, so that every
-  // wait counts the same); then the products.  Eight waves are two halves, half
-  // a stage apart, so that of the two waves of a SIMD one multiplies while the
-  // other reads.
+  // kt - 1, which every wave has read; then the products.  The last stages have
+  // no copies to send and wait for fewer (copies of zeros past the end, so that
+  // every stage is alike: 128 rows x 2048 x 5632 1.4 us, 4096 rows 3).  Eight
+  // waves are two halves, half a stage apart, so that of the two waves of a SIMD
+  // one multiplies while the other reads.
   constexpr bool kHalves = W == 8;
-  constexpr int kCopies = Loader<BM, W, kMAcross>::kInstr + Loader<BN, W, kNAcross>::kInstr;
-  const int nk = ceil_div(K, kBK);
+  constexpr int kSteps = kK / 32, kRead = kHalves ? 1 : kSteps;   // steps of a stage; read at once
+  constexpr int kCopies = Loader<BM, kK, W, kMAcross>::kInstr + Loader<BN, kK, W, kNAcross>::kInstr;
+  const int nk = max(ceil_div(K, kK), kStages - 1);
   const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds;
   auto issue = [&](int kt) {
     const uint32_t to = lds_at + (uint32_t)(kt % kStages) * kStage;
-    lm.issue(to, wave, K - kt * kBK);
-    ln.issue(to + kMBytes, wave, K - kt * kBK);
+    lm.issue(to, wave, K - kt * kK);
+    ln.issue(to + kMBytes, wave, K - kt * kK);
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue(i);
   wait_vmem<(kStages - 2) * kCopies>();
   barrier_nofence();
   if (kHalves && wave >= W / 2) barrier_nofence();
-#pragma unroll 1
-  for (int kt = 0; kt < nk; ++kt) {
+  auto step = [&](int kt, auto more, auto left) {
     const uint8_t* at = lds + (kt % kStages) * kStage;
-    u32x4 fn[FN], fm[FM];
 #pragma unroll
-    for (int i = 0; i < FN; ++i) fn[i] = rn.read(at + kMBytes, i);
+    for (int s0 = 0; s0 < kSteps; s0 += kRead) {
+      u32x4 fn[kRead][FN], fm[kRead][FM];
 #pragma unroll
-    for (int j = 0; j < FM; ++j) fm[j] = rm.read(at, j);
-    issue(kt + kStages - 1);
-    wait_lgkm0();
-    wait_vmem<(kStages - 2) * kCopies>();          // stage kt + 1 is there
-    barrier_nofence();
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_setprio(1);
+      for (int q = 0; q < kRead; ++q) {
 #pragma unroll
-    for (int i = 0; i < FN; ++i)
+        for (int i = 0; i < FN; ++i) fn[q][i] = rn.read(at + kMBytes, i, s0 + q);
 #pragma unroll
-      for (int j = 0; j < FM; ++j) acc[i][j] = mfma_16x16x32(fn[i], fm[j], acc[i][j]);
-    __builtin_amdgcn_s_setprio(0);
-    __builtin_amdgcn_sched_barrier(0);
-    if (kHalves) barrier_nofence();
-  }
+        for (int j = 0; j < FM; ++j) fm[q][j] = rm.read(at, j, s0 + q);
+      }
+      if (more && s0 == 0) issue(kt + kStages - 1);
+      wait_lgkm0();
+      if (s0 + kRead == kSteps) wait_vmem<left * kCopies>();   // stage kt + 1 is there
+      barrier_nofence();
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int q = 0; q < kRead; ++q)
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int j = 0; j < FM; ++j) acc[i][j] = mfma_16x16x32(fn[q][i], fm[q][j], acc[i][j]);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (kHalves) barrier_nofence();
+    }
+  };
+#pragma unroll 1
+  for (int kt = 0; kt < nk - (kStages - 1); ++kt)
+    step(kt, std::true_type{}, std::integral_constant<int, kStages - 2>{});
+  each(std::make_integer_sequence<int, kStages - 1>{}, [&](auto i) {
+    step(nk - (kStages - 1) + i, std::false_type{},
+         std::integral_constant<int, (kStages - 3 - i > 0 ? kStages - 3 - i : 0)>{});
+  });
   if (kHalves && wave < W / 2) barrier_nofence();
-  wait_vmem<0>();                      // the copies past the end
 
   // a lane holds 4 consecutive n of one m, gated 8 features
   const int ml = m0 + wm * TM + (lane & 15), nq = 4 * (lane >> 4);
@@ -472,10 +498,13 @@ constexpr int kSmallSplitTiles = 256;   // 512 and 1024: 5 and 12 % slower at 50
 
 // Tile size and ranges of K of one product.  Tiles of 256 x 256 where half the
 // chip has one (128 x 128 re-reads twice as much from L2 and LDS), 64 x 128 with
-// a ring twice as deep where 128 x 128 would leave half the chip without
-// (2048 x 5632, 128 rows: 23.3 us against 27.0; 509 rows' gradient at 1408
-// features 53 / 60), and a product whose sum is all it stores is cut along K
-// until every CU has a tile.
+// stages of 64 k where 128 x 128 would leave half the chip without (2048 x 5632,
+// 128 rows: 18 us against 27), and a product whose sum is all it stores is cut
+// along K until every CU has a tile.  Stages of 64 k are whole 128-byte lines of
+// the rows and half the barriers, but at 128 KB a CU the rings hold two or four
+// of them: 64 x 128 tiles 18 us for 23 (eight stages of 32), 128 x 128 tiles
+// slower (1000 rows x 1408 features 33 us for 23, four stages 25), 256 x 256 as
+// well (4096 rows 175 for 168).
 struct Plan {
   bool big;                  // 256 x 256 tiles, else bm x 128
   int bm;
@@ -488,13 +517,13 @@ Plan plan_of(int rows, int n_rows, int K, bool can_split) {
   p.big = big >= cu / 2;
   const long long tiles =
       p.big ? big : (long long)ceil_div_host(rows, 128) * ceil_div_host(n_rows, 128);
-  const int stages = ceil_div_host(K, kBK);
+  const int stages = ceil_div_host(K, 32);
   if (can_split && tiles < cu) {
     // whole stages, at least 8 to a range
     const long long most = std::min(stages / 8, kMaxSplits), room = p.big ? kSplitTiles / 4 : kSmallSplitTiles;
     p.splits = (int)std::max<long long>(1, std::min(room / tiles, most));
   }
-  p.k_per = ceil_div_host(stages, p.splits) * kBK;
+  p.k_per = ceil_div_host(stages, p.splits) * 32;
   p.splits = ceil_div_host(K, p.k_per);
   if (!can_split && !p.big && tiles <= cu / 2) p.bm = 64;
   return p;
@@ -525,11 +554,11 @@ hipError_t launch_tiles(TileArgs a, int n_rows, bool can_split, hipStream_t s) {
   }
   const unsigned grid = (unsigned)ceil_div_host(a.tiles_m * a.tiles_n * a.splits, 8) * 8;
   if (p.big)
-    tile_kernel<256, 256, 2, 4, 4, kOp><<<grid, 512, 0, s>>>(a);
+    tile_kernel<256, 256, 32, 2, 4, 4, kOp><<<grid, 512, 0, s>>>(a);
   else if (p.bm == 64)
-    tile_kernel<64, 128, 2, 2, 8, kOp><<<grid, 256, 0, s>>>(a);
+    tile_kernel<64, 128, 64, 2, 2, 4, kOp><<<grid, 256, 0, s>>>(a);
   else
-    tile_kernel<128, 128, 2, 2, 4, kOp><<<grid, 256, 0, s>>>(a);
+    tile_kernel<128, 128, 32, 2, 2, 4, kOp><<<grid, 256, 0, s>>>(a);
   if (p.splits > 1) {
     const size_t n = (size_t)a.rows * a.cols;
     const unsigned g = (unsigned)std::min<size_t>((n / 8 + 255) / 256, 4096);

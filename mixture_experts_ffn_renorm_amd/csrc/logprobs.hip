@@ -610,8 +610,8 @@ __global__ __launch_bounds__(256) void logprob_backward_kernel(moe_host::Logprob
   const float lse = a.lse[m];
   const bool none = lse < kNone;
   const float g = t >= 0 && t < a.V && !none ? a.grad_logprobs[m] : 0.f;
-  const float h = a.grad_entropy != nullptr ? a.grad_entropy[m] : 0.f;
-  const float H = a.grad_entropy != nullptr ? a.entropy[m] : 0.f;
+  const float h = a.grad_entropy != nullptr && !none ? a.grad_entropy[m] : 0.f;
+  const float H = a.grad_entropy != nullptr && !none ? a.entropy[m] : 0.f;
   u32x4 w[kGradLoads];
 #pragma unroll
   for (int i = 0; i < kGradLoads; ++i) {

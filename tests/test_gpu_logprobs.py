@@ -300,6 +300,24 @@ def test_gradient_under_masks(low, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("low", ["inf", "lowest"])
+def test_gradient_of_a_masked_row_is_zero_for_any_that_comes_in(low, dtype):
+    import torch
+    moe = _moe()
+    l = draw(3, 1003, 17)
+    l[1, :] = -np.inf if low == "inf" else LOWEST[dtype]
+    d, l = device(l, dtype)
+    tok = torch.tensor([3, 4, 5], dtype=torch.int32, device="cuda")
+    _, ent, lse, _, _ = moe.moe_token_logprobs(d, tok)
+    g = torch.ones(3, device="cuda")
+    want = moe.moe_token_logprobs_backward(d, tok, lse, ent, g, g)
+    for bad in (np.nan, np.inf):
+        b = torch.tensor([1.0, bad, 1.0], device="cuda")
+        got = moe.moe_token_logprobs_backward(d, tok, lse, ent, b, b)
+        assert not got[1].any() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_gradient_of_rows_that_are_not_finite_stays_alone(dtype):
     l = draw(4, 333, 14)
     l[1, 7] = np.nan

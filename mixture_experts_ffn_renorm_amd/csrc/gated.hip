@@ -147,15 +147,17 @@ __device__ __forceinline__ void each(std::integer_sequence<int, i...>, const F& 
   (f(std::integral_constant<int, i>{}), ...);
 }
 
-template <int BM, int BN, int kK, int WM, int WN, int kStages, Op kOp>
-__global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
-  constexpr int W = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+// Tiles of BM x BN in stages of kK k, a ring of kStages; WM x WN waves, KS times:
+// each such group takes its share of every stage's k.
+template <int BM, int BN, int kK, int WM, int WN, int KS, int kStages, Op kOp>
+__global__ __launch_bounds__(64 * WM * WN * KS, KS == 1 ? 2 : 1) void tile_kernel(TileArgs a) {
+  constexpr int W = WM * WN * KS, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr bool kGated = kOp == kAct || kOp == kGradAct;
   constexpr bool kMAcross = kOp == kGradW, kNAcross = kOp == kGradX || kOp == kGradW;
   constexpr int kMBytes = BM * kK * 2, kStage = (BM + BN) * kK * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * kStage];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WN, wn = wave % WN;
+  const int wk = wave / (WM * WN), wm = wave / WN % WM, wn = wave % WN;
 
   // tiles of one XCD are neighbours: columns of up to 8 tiles of m
   int t = xcd_contiguous_tile(blockIdx.x, a.tiles_m * a.tiles_n * a.splits);
@@ -200,7 +202,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
   // waves are two halves, half a stage apart, so that of the two waves of a SIMD
   // one multiplies while the other reads.
   constexpr bool kHalves = W == 8;
-  constexpr int kSteps = kK / 32, kRead = kHalves ? 1 : kSteps;   // steps of a stage; read at once
+  constexpr int kSteps = kK / 32 / KS, kRead = kHalves ? 1 : kSteps;   // a wave's of a stage
   constexpr int kCopies = Loader<BM, kK, W, kMAcross>::kInstr + Loader<BN, kK, W, kNAcross>::kInstr;
   const int nk = max(ceil_div(K, kK), kStages - 1);
   const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds;
@@ -222,9 +224,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
 #pragma unroll
       for (int q = 0; q < kRead; ++q) {
 #pragma unroll
-        for (int i = 0; i < FN; ++i) fn[q][i] = rn.read(at + kMBytes, i, s0 + q);
+        for (int i = 0; i < FN; ++i) fn[q][i] = rn.read(at + kMBytes, i, wk * kSteps + s0 + q);
 #pragma unroll
-        for (int j = 0; j < FM; ++j) fm[q][j] = rm.read(at, j, s0 + q);
+        for (int j = 0; j < FM; ++j) fm[q][j] = rm.read(at, j, wk * kSteps + s0 + q);
       }
       if (more && s0 == 0) issue(kt + kStages - 1);
       wait_lgkm0();
@@ -252,10 +254,30 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(TileArgs a) {
   });
   if (kHalves && wave < W / 2) barrier_nofence();
 
-  // a lane holds 4 consecutive n of one m, gated 8 features
-  const int ml = m0 + wm * TM + (lane & 15), nq = 4 * (lane >> 4);
+  // the groups' sums meet in LDS, in order, and each group finishes its rows
+  constexpr int FE = FM / KS;
+  if (KS > 1) {
+    static_assert(KS == 1 || (W * FN * FM * 1024 <= sizeof(lds) && FM % KS == 0), "the sums");
+    f32x4* red = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
-  for (int j = 0; j < FM; ++j) {
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) red[((wave * FN + i) * FM + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FE; ++j) {
+        const f32x4* p = red + (((wave % (WM * WN)) * FN + i) * FM + wk * FE + j) * 64 + lane;
+        acc[i][j] = p[0];
+#pragma unroll
+        for (int q = 1; q < KS; ++q) acc[i][j] += p[q * (WM * WN * FN * FM * 64)];
+      }
+  }
+  // a lane holds 4 consecutive n of one m, gated 8 features
+  const int ml = m0 + wm * TM + wk * FE * 16 + (lane & 15), nq = 4 * (lane >> 4);
+#pragma unroll
+  for (int j = 0; j < FE; ++j) {
     const int m = ml + j * 16;
     if (m >= a.rows) continue;
     if (kGated) {
@@ -501,10 +523,13 @@ constexpr int kSmallSplitTiles = 256;   // 512 and 1024: 5 and 12 % slower at 50
 // stages of 64 k where 128 x 128 would leave half the chip without (2048 x 5632,
 // 128 rows: 18 us against 27), and a product whose sum is all it stores is cut
 // along K until every CU has a tile.  Stages of 64 k are whole 128-byte lines of
-// the rows and half the barriers, but at 128 KB a CU the rings hold two or four
-// of them: 64 x 128 tiles 18 us for 23 (eight stages of 32), 128 x 128 tiles
+// the rows and half the barriers, but at 128 KB a CU the rings hold two to
+// four of them: 64 x 128 tiles 18 us for 23 (eight stages of 32), 128 x 128 tiles
 // slower (1000 rows x 1408 features 33 us for 23, four stages 25), 256 x 256 as
-// well (4096 rows 175 for 168).
+// well (4096 rows 175 for 168).  The waves of 64 x 128 are 64 x 64, two to each
+// half of a stage's k: a third less of LDS is read than by 32 x 64 (509 rows x
+// 1408 features 15.0 us for 16.3, 300 x 1024 of 4096 25.6 for 28.6;
+// three stages 16.1 and 27.6).
 struct Plan {
   bool big;                  // 256 x 256 tiles, else bm x 128
   int bm;
@@ -553,12 +578,14 @@ hipError_t launch_tiles(TileArgs a, int n_rows, bool can_split, hipStream_t s) {
     rest.rows = 0;
   }
   const unsigned grid = (unsigned)ceil_div_host(a.tiles_m * a.tiles_n * a.splits, 8) * 8;
-  if (p.big)
-    tile_kernel<256, 256, 32, 2, 4, 4, kOp><<<grid, 512, 0, s>>>(a);
-  else if (p.bm == 64)
-    tile_kernel<64, 128, 64, 2, 2, 4, kOp><<<grid, 256, 0, s>>>(a);
-  else
-    tile_kernel<128, 128, 32, 2, 2, 4, kOp><<<grid, 256, 0, s>>>(a);
+  if (p.big) {
+    tile_kernel<256, 256, 32, 2, 4, 1, 4, kOp><<<grid, 512, 0, s>>>(a);
+  } else if (p.bm == 64) {
+    if constexpr (kOp == kAct || kOp == kGradAct)
+      tile_kernel<64, 128, 64, 1, 2, 2, 4, kOp><<<grid, 256, 0, s>>>(a);
+  } else {
+    tile_kernel<128, 128, 32, 2, 2, 1, 4, kOp><<<grid, 256, 0, s>>>(a);
+  }
   if (p.splits > 1) {
     const size_t n = (size_t)a.rows * a.cols;
     const unsigned g = (unsigned)std::min<size_t>((n / 8 + 255) / 256, 4096);

@@ -40,12 +40,12 @@ struct TileArgs {
 };
 
 // Swizzles of the LDS tiles, in 16-byte pieces.  Rows of kK k: piece c of row r
-// lies at c ^ (r / 2 % pieces), so that the rows of one beat of a 16-byte read
-// lie in different banks.  Rows of R columns: the pairs of pieces are exchanged
+// lies at c ^ (r / 2 % pieces), c ^ (r % 16) where a row is 256 bytes, so that the
+// rows of one beat of a 16-byte read lie in different banks.  Rows of R columns: the pairs of pieces are exchanged
 // by the bits of k in which the lanes of a transposing read differ.
 template <int kK>
 __device__ __forceinline__ int along_swizzle(int r) {
-  return (r >> 1) & (kK / 8 - 1);
+  return kK < 128 ? (r >> 1) & (kK / 8 - 1) : r & 15;
 }
 __device__ __forceinline__ int across_swizzle(int k) { return ((k & 3) | ((k >> 1) & 4)) << 1; }
 
@@ -150,7 +150,7 @@ __device__ __forceinline__ void each(std::integer_sequence<int, i...>, const F& 
 // Tiles of BM x BN in stages of kK k, a ring of kStages; WM x WN waves, KS times:
 // each such group takes its share of every stage's k.
 template <int BM, int BN, int kK, int WM, int WN, int KS, int kStages, Op kOp>
-__global__ __launch_bounds__(64 * WM * WN * KS, KS == 1 ? 2 : 1) void tile_kernel(TileArgs a) {
+__global__ __launch_bounds__(64 * WM * WN * KS, BM < 128 && WN == 1 ? 1 : 2) void tile_kernel(TileArgs a) {
   constexpr int W = WM * WN * KS, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr bool kGated = kOp == kAct || kOp == kGradAct;
   constexpr bool kMAcross = kOp == kGradW, kNAcross = kOp == kGradX || kOp == kGradW;
@@ -201,7 +201,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, KS == 1 ? 2 : 1) void tile_kerne
   // every stage is alike: 128 rows x 2048 x 5632 1.4 us, 4096 rows 3).  Eight
   // waves are two halves, half a stage apart, so that of the two waves of a SIMD
   // one multiplies while the other reads.
-  constexpr bool kHalves = W == 8;
+  constexpr bool kHalves = W == 8 && KS == 1;
   constexpr int kSteps = kK / 32 / KS, kRead = kHalves ? 1 : kSteps;   // a wave's of a stage
   constexpr int kCopies = Loader<BM, kK, W, kMAcross>::kInstr + Loader<BN, kK, W, kNAcross>::kInstr;
   const int nk = max(ceil_div(K, kK), kStages - 1);
@@ -255,15 +255,16 @@ __global__ __launch_bounds__(64 * WM * WN * KS, KS == 1 ? 2 : 1) void tile_kerne
   if (kHalves && wave < W / 2) barrier_nofence();
 
   // the groups' sums meet in LDS, in order, and each group finishes its rows
-  constexpr int FE = FM / KS;
+  constexpr int FE = FM > KS ? FM / KS : 1;
   if (KS > 1) {
-    static_assert(KS == 1 || (W * FN * FM * 1024 <= sizeof(lds) && FM % KS == 0), "the sums");
+    static_assert(KS == 1 || (W * FN * FM * 1024 <= sizeof(lds)), "the sums");
     f32x4* red = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
       for (int j = 0; j < FM; ++j) red[((wave * FN + i) * FM + j) * 64 + lane] = acc[i][j];
     __syncthreads();
+    if (wk * FE >= FM) return;
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -326,46 +327,39 @@ __global__ __launch_bounds__(64 * WM * WN * KS, KS == 1 ? 2 : 1) void tile_kerne
   }
 }
 
-// ---- few rows: the weights are read once, as fast as memory gives them ----
+// ---- one to four rows: a GEMV, a wave reads the gate and up row of one feature ----
+//
+// Four waves a workgroup, so that 5632 features are 5.5 of them on every CU
+// (2048 x 5632, one row 9.7 us; eight waves of two features 11.6: 1.4 workgroups
+// a CU).  Four rows 11.9 us, by tiles 10.9; 4096 x 1024 7.9 and 10.5.
+constexpr int kGemvRows = 4;
+constexpr int kGemvWaves = 4;
 
-constexpr int kGemvRows = 4;           // rows of the GEMVs
-constexpr int kFewRows = 64;           // rows of the streaming products
-constexpr int kGemvFeatures = 2;       // features of a wave
-
-// One to four rows: a wave reads the gate and up rows of kGemvFeatures
-// features, 1 KB of each at a time.
 template <int T>
-__global__ __launch_bounds__(512) void gated_gemv_kernel(moe_host::GatedArgs a) {
-  constexpr int F = kGemvFeatures;
+__global__ __launch_bounds__(64 * kGemvWaves) void gated_gemv_kernel(moe_host::GatedArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int f0 = (blockIdx.x * 8 + wave) * F;
-  if (f0 >= a.I) return;
-  const uint16_t* w[2 * F];
+  const int f = blockIdx.x * kGemvWaves + wave;
+  if (f >= a.I) return;
+  const uint16_t* w[2] = {a.w13 + (size_t)f * a.H, a.w13 + (size_t)(a.I + f) * a.H};
+  float sum[2][T];
 #pragma unroll
-  for (int f = 0; f < F; ++f) {
-    const int i = min(f0 + f, a.I - 1);
-    w[f] = a.w13 + (size_t)i * a.H;
-    w[F + f] = a.w13 + (size_t)(a.I + i) * a.H;
-  }
-  float sum[2 * F][T];
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-  for (int f = 0; f < 2 * F; ++f)
-#pragma unroll
-    for (int t = 0; t < T; ++t) sum[f][t] = 0.f;
+    for (int t = 0; t < T; ++t) sum[h][t] = 0.f;
   auto step = [&](int k) {
-    u32x4 x[T], v[2 * F];
+    u32x4 x[T], v[2];
 #pragma unroll
-    for (int f = 0; f < 2 * F; ++f) v[f] = load16(w[f] + k);
+    for (int h = 0; h < 2; ++h) v[h] = load16(w[h] + k);
 #pragma unroll
     for (int t = 0; t < T; ++t) x[t] = load16(a.x + (size_t)t * a.H + k);
 #pragma unroll
-    for (int f = 0; f < 2 * F; ++f)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          sum[f][t] = __builtin_fmaf(bf16_lo(x[t][j]), bf16_lo(v[f][j]), sum[f][t]);
-          sum[f][t] = __builtin_fmaf(bf16_hi(x[t][j]), bf16_hi(v[f][j]), sum[f][t]);
+          sum[h][t] = __builtin_fmaf(bf16_lo(x[t][j]), bf16_lo(v[h][j]), sum[h][t]);
+          sum[h][t] = __builtin_fmaf(bf16_hi(x[t][j]), bf16_hi(v[h][j]), sum[h][t]);
         }
   };
   int k = 0;
@@ -373,119 +367,9 @@ __global__ __launch_bounds__(512) void gated_gemv_kernel(moe_host::GatedArgs a) 
   for (; k + 512 <= a.H; k += 512) step(k + lane * 8);
   if (k + lane * 8 < a.H) step(k + lane * 8);
 #pragma unroll
-  for (int f = 0; f < F; ++f)
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const float g = wave_sum(sum[f][t]), u = wave_sum(sum[F + f][t]);
-      if (lane == 0 && f0 + f < a.I)
-        a.out[(size_t)t * a.I + f0 + f] = (uint16_t)f32_to_bf16(silu_mul(g, u));
-    }
-}
-
-// Up to 16 FM rows: a workgroup takes 16 FF features, its four waves every
-// fourth 128 elements of K each.  A wave copies its weight rows in runs of 256
-// bytes into LDS of its own (no barriers), two pieces of K ahead, and reads them
-// back as fragments; x comes from L2 straight into registers.  The waves' sums
-// meet in LDS, in wave order.  (2048 x 5632: 16 rows 13.5 us, 32 15.3, 64 19.2;
-// fragments straight from memory, 16 rows of 64 bytes an instruction: 16.7, 17.1
-// and 21.4.)  More than 16 rows take 32 features, since x comes from L2 once for
-// every workgroup: 64 rows 24.8 with 16.
-constexpr int kRowsWaves = 4;
-constexpr int kRowsK = 128;            // elements of K of a piece
-
-template <int FM, int FF>
-__global__ __launch_bounds__(64 * kRowsWaves, 1) void gated_rows_kernel(moe_host::GatedArgs a) {
-  constexpr int kRows = 32 * FF;                 // gate rows, then up rows
-  constexpr int kPiece = kRows * kRowsK * 2, kCopies = kRows / 4, kSteps = kRowsK / 32;
-  constexpr int kSums = kRowsWaves * 2 * FF * FM * 1024;
-  constexpr int kLds = kRowsWaves * 2 * kPiece;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds > kSums ? kLds : kSums];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int i = lane & 15, g = lane >> 4;
-  const int f0 = blockIdx.x * 16 * FF;
-  // copy q takes rows 4 q .. 4 q + 3; 16-byte piece c of row r lies at c ^ (r & 15)
-  const uint16_t* src[kCopies];
-  int at_k[kCopies];
-#pragma unroll
-  for (int q = 0; q < kCopies; ++q) {
-    const int r = 4 * q + g, f = min(f0 + r % (16 * FF), a.I - 1);
-    at_k[q] = 8 * (i ^ (r & 15));
-    src[q] = a.w13 + (size_t)(r < 16 * FF ? f : a.I + f) * a.H + at_k[q];
-  }
-  const uint16_t* x[FM];
-#pragma unroll
-  for (int j = 0; j < FM; ++j) x[j] = a.x + (size_t)min(16 * j + i, a.M - 1) * a.H + 8 * g;
-  uint8_t* mine = lds + wave * 2 * kPiece;
-  const uint32_t mine_at = (uint32_t)(uintptr_t)(lds_void_t*)mine;
-  const int pieces = ceil_div(a.H, kRowsK * kRowsWaves);
-  // piece p of this wave; past the end of K zeros
-  auto issue = [&](int p, u32x4 (&xv)[kSteps][FM]) {
-    const int k0 = (p * kRowsWaves + wave) * kRowsK;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-      for (int j = 0; j < FM; ++j)
-        xv[s][j] = load16_or_zero(x[j] + k0 + 32 * s, k0 + 32 * s + 8 * g < a.H);
-#pragma unroll
-    for (int q = 0; q < kCopies; ++q)
-      copy16(k0 + at_k[q] < a.H ? (const void*)(src[q] + k0) : (const void*)kZeroPage,
-             mine_at + (p & 1) * kPiece + q * 1024);
-  };
-  f32x4 acc[2 * FF][FM];
-#pragma unroll
-  for (int f = 0; f < 2 * FF; ++f)
-#pragma unroll
-    for (int j = 0; j < FM; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](int p, const u32x4 (&xv)[kSteps][FM]) {
-    // at most the next piece's copies are still on their way
-    wait_vmem<kCopies>();
-    asm volatile("" ::: "memory");
-    const uint8_t* at = mine + (p & 1) * kPiece + i * 256;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      u32x4 v[2 * FF];
-#pragma unroll
-      for (int f = 0; f < 2 * FF; ++f) v[f] = load16(at + f * 4096 + (((4 * s + g) ^ i) << 4));
-#pragma unroll
-      for (int j = 0; j < FM; ++j)
-#pragma unroll
-        for (int f = 0; f < 2 * FF; ++f) acc[f][j] = mfma_16x16x32(v[f], xv[s][j], acc[f][j]);
-    }
-    wait_lgkm0();                                // the piece's LDS is free
-    asm volatile("" ::: "memory");
-  };
-  u32x4 x0[kSteps][FM], x1[kSteps][FM];
-  issue(0, x0);
-  issue(1, x1);
-#pragma unroll 1
-  for (int p = 0; p < pieces; p += 2) {
-    multiply(p, x0);
-    issue(p + 2, x0);
-    multiply(p + 1, x1);
-    issue(p + 3, x1);
-  }
-  wait_vmem<0>();                                // the copies past the end
-  __syncthreads();
-  f32x4* red = reinterpret_cast<f32x4*>(lds);    // [wave][2 FF][FM][64]
-#pragma unroll
-  for (int f = 0; f < 2 * FF; ++f)
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
-      red[((wave * 2 * FF + f) * FM + j) * 64 + lane] = acc[f][j];
-  __syncthreads();
-#pragma unroll
-  for (int e = wave; e < FF * FM; e += kRowsWaves) {
-    const int f = e / FM, j = e % FM, m = 16 * j + i, n = f0 + f * 16 + 4 * g;
-    f32x4 sg = red[(f * FM + j) * 64 + lane], su = red[((FF + f) * FM + j) * 64 + lane];
-#pragma unroll
-    for (int q = 1; q < kRowsWaves; ++q) {
-      sg += red[((q * 2 * FF + f) * FM + j) * 64 + lane];
-      su += red[((q * 2 * FF + FF + f) * FM + j) * 64 + lane];
-    }
-    if (m < a.M && n < a.I)
-      *reinterpret_cast<u32x2*>(a.out + (size_t)m * a.I + n) =
-          u32x2{pack_bf16x2(silu_mul(sg[0], su[0]), silu_mul(sg[1], su[1])),
-                pack_bf16x2(silu_mul(sg[2], su[2]), silu_mul(sg[3], su[3]))};
+  for (int t = 0; t < T; ++t) {
+    const float g = wave_sum(sum[0][t]), u = wave_sum(sum[1][t]);
+    if (lane == 0) a.out[(size_t)t * a.I + f] = (uint16_t)f32_to_bf16(silu_mul(g, u));
   }
 }
 
@@ -518,53 +402,71 @@ constexpr int kMaxSplits = 16;
 constexpr int kSplitTiles = 1024;
 constexpr int kSmallSplitTiles = 256;   // 512 and 1024: 5 and 12 % slower at 509 x 2048 x 1408
 
-// Tile size and ranges of K of one product.  Tiles of 256 x 256 where half the
-// chip has one (128 x 128 re-reads twice as much from L2 and LDS), 64 x 128 with
-// stages of 64 k where 128 x 128 would leave half the chip without (2048 x 5632,
-// 128 rows: 18 us against 27), and a product whose sum is all it stores is cut
-// along K until every CU has a tile.  Stages of 64 k are whole 128-byte lines of
-// the rows and half the barriers, but at 128 KB a CU the rings hold two to
-// four of them: 64 x 128 tiles 18 us for 23 (eight stages of 32), 128 x 128 tiles
-// slower (1000 rows x 1408 features 33 us for 23, four stages 25), 256 x 256 as
-// well (4096 rows 175 for 168).  The waves of 64 x 128 are 64 x 64, two to each
-// half of a stage's k: a third less of LDS is read than by 32 x 64 (509 rows x
-// 1408 features 15.0 us for 16.3, 300 x 1024 of 4096 25.6 for 28.6;
-// three stages 16.1 and 27.6).
+// Tile size and ranges of K of one product.  Copies into LDS bound them all (9 to
+// 12 TB/s from L2 over the chip), and what they cost follows the lines that they
+// touch.
+//
+// Large: 256 x 256 where half the chip has one; whole 128-byte lines, two stages
+// of 64 k, hold too little in flight (4096 rows x 2048 x 5632 175 us for 168).
+// Sums shorter than kShortSum, which store more than they read, take 128 x 128
+// all the same, two workgroups to a CU: one stores while the other reads (200
+// rows' grad_w13 of 2 x 5632 x 2048 55 us for 51 with gate and up before it).
+// 128 x 128, gate and up: 64 x 64 a wave, four to each half of a stage's 64 k
+// (900 rows x 2048 x 1408 20.4 us; four waves, stages of 32 k 23.7).
+//
+// Gate and up of at most 64 rows, or where 128 x 128 would leave half the chip
+// without: tiles of 64 rows or fewer whose waves are 64 features wide (32 gates
+// and their ups) and share out a stage of 128 k, 256-byte runs of every row.
+// Each wave reads its k alone, so LDS is read once for all rows, and the sums
+// meet in LDS at the end.  Tiles 64 features wide while the chip holds them at once,
+// else 128.  2048 x 5632: 16 rows 11.0 us, 32 12.0, 64 14.1, 128 18; 200 x 2048 x
+// 1408 10.3, 300 x 4096 x 1024 16.6, 509 x 2048 x 1408 14.3 (waves side by side,
+// stages of 64 k: 23, 16.3, 28.6, 16.3; weights through LDS of each wave's own
+// and x straight to registers 13.5, 15, 19 for the first three).
+//
+// A product whose sum is all it stores is cut along K until every CU has a tile.
+constexpr int kShortSum = 512;
+
 struct Plan {
-  bool big;                  // 256 x 256 tiles, else bm x 128
-  int bm;
+  int bm, bn;                // tile
   int splits, k_per;
 };
-Plan plan_of(int rows, int n_rows, int K, bool can_split) {
-  Plan p{true, 128, 1, 0};
-  const int cu = kTileCus;
-  const long long big = (long long)ceil_div_host(rows, 256) * ceil_div_host(n_rows, 256);
-  p.big = big >= cu / 2;
-  const long long tiles =
-      p.big ? big : (long long)ceil_div_host(rows, 128) * ceil_div_host(n_rows, 128);
-  const int stages = ceil_div_host(K, 32);
-  if (can_split && tiles < cu) {
-    // whole stages, at least 8 to a range
-    const long long most = std::min(stages / 8, kMaxSplits), room = p.big ? kSplitTiles / 4 : kSmallSplitTiles;
-    p.splits = (int)std::max<long long>(1, std::min(room / tiles, most));
+Plan plan_of(bool gated, int rows, int n_rows, int K) {
+  auto tiles = [&](int bm, int bn) {
+    return (long long)ceil_div_host(rows, bm) * ceil_div_host(n_rows, bn);
+  };
+  const int cu = kTileCus, stages = ceil_div_host(K, 32);
+  Plan p{128, 128, 1, K};
+  if (gated && (rows <= 64 || tiles(128, 128) <= cu / 2)) {
+    p.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    p.bn = p.bm == 16 || tiles(64, 64) <= cu ? 64 : 128;
+    return p;
   }
-  p.k_per = ceil_div_host(stages, p.splits) * 32;
-  p.splits = ceil_div_host(K, p.k_per);
-  if (!can_split && !p.big && tiles <= cu / 2) p.bm = 64;
+  if (tiles(256, 256) >= cu / 2 && (gated || K >= kShortSum)) p.bm = p.bn = 256;
+  const long long all = tiles(p.bm, p.bn);
+  if (!gated && all < cu) {
+    // whole stages, at least 8 to a range
+    const long long most = std::min(stages / 8, kMaxSplits);
+    const long long room = p.bm == 256 ? kSplitTiles / 4 : kSmallSplitTiles;
+    p.splits = (int)std::max<long long>(1, std::min(room / all, most));
+    p.k_per = ceil_div_host(stages, p.splits) * 32;
+    p.splits = ceil_div_host(K, p.k_per);
+  }
   return p;
 }
 
 template <Op kOp>
-hipError_t launch_tiles(TileArgs a, int n_rows, bool can_split, hipStream_t s) {
-  const Plan p = plan_of(a.rows, n_rows, a.K, can_split);
+hipError_t launch_tiles(TileArgs a, int n_rows, hipStream_t s) {
+  constexpr bool kGated = kOp == kAct || kOp == kGradAct;
+  const Plan p = plan_of(kGated, a.rows, n_rows, a.K);
   a.splits = p.splits;
   a.k_per = p.k_per;
-  a.tiles_m = ceil_div_host(a.rows, p.big ? 256 : p.bm);
-  a.tiles_n = ceil_div_host(n_rows, p.big ? 256 : 128);
+  a.tiles_m = ceil_div_host(a.rows, p.bm);
+  a.tiles_n = ceil_div_host(n_rows, p.bn);
   TileArgs rest = a;
   const int last = a.tiles_m * a.tiles_n % kTileCus;
   const int whole = a.tiles_m * a.tiles_n / kTileCus * kTileCus / a.tiles_n;   // rows of tiles
-  if (p.big && p.splits == 1 && whole > 0 && last > 0 && last <= kTileCus / 2) {
+  if (p.bm == 256 && p.splits == 1 && whole > 0 && last > 0 && last <= kTileCus / 2) {
     // a last round that leaves half the chip idle: its rows are a product of
     // their own, of smaller tiles (4096 x 2048 x 5632, grad_w13: 352 tiles)
     a.tiles_m = whole;
@@ -578,13 +480,23 @@ hipError_t launch_tiles(TileArgs a, int n_rows, bool can_split, hipStream_t s) {
     rest.rows = 0;
   }
   const unsigned grid = (unsigned)ceil_div_host(a.tiles_m * a.tiles_n * a.splits, 8) * 8;
-  if (p.big) {
-    tile_kernel<256, 256, 32, 2, 4, 1, 4, kOp><<<grid, 512, 0, s>>>(a);
-  } else if (p.bm == 64) {
-    if constexpr (kOp == kAct || kOp == kGradAct)
-      tile_kernel<64, 128, 64, 1, 2, 2, 4, kOp><<<grid, 256, 0, s>>>(a);
+  auto run = [&](auto kernel, int waves) { kernel<<<grid, 64 * waves, 0, s>>>(a); };
+  if (p.bm == 256) {
+    run(tile_kernel<256, 256, 32, 2, 4, 1, 4, kOp>, 8);
+  } else if constexpr (kGated) {
+    if (p.bm == 128)
+      run(tile_kernel<128, 128, 64, 2, 2, 2, 4, kOp>, 8);
+    else if (p.bn == 128)
+      p.bm == 64 ? run(tile_kernel<64, 128, 128, 1, 2, 4, 3, kOp>, 8)
+                 : run(tile_kernel<32, 128, 128, 1, 2, 4, 3, kOp>, 8);
+    else if (p.bm == 64)
+      run(tile_kernel<64, 64, 128, 1, 1, 4, 4, kOp>, 4);
+    else if (p.bm == 32)
+      run(tile_kernel<32, 64, 128, 1, 1, 4, 4, kOp>, 4);
+    else
+      run(tile_kernel<16, 64, 128, 1, 1, 4, 4, kOp>, 4);
   } else {
-    tile_kernel<128, 128, 32, 2, 2, 1, 4, kOp><<<grid, 256, 0, s>>>(a);
+    run(tile_kernel<128, 128, 32, 2, 2, 1, 4, kOp>, 4);
   }
   if (p.splits > 1) {
     const size_t n = (size_t)a.rows * a.cols;
@@ -592,7 +504,7 @@ hipError_t launch_tiles(TileArgs a, int n_rows, bool can_split, hipStream_t s) {
     join_kernel<<<g, 256, 0, s>>>(a.partial, p.splits, n, a.out);
   }
   const hipError_t err = hipGetLastError();
-  return err != hipSuccess || rest.rows == 0 ? err : launch_tiles<kOp>(rest, n_rows, can_split, s);
+  return err != hipSuccess || rest.rows == 0 ? err : launch_tiles<kOp>(rest, n_rows, s);
 }
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -609,22 +521,13 @@ namespace moe_host {
 
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s) {
   if (a.M <= kGemvRows) {
-    const int grid = ceil_div_host(a.I, 8 * kGemvFeatures);
+    const int grid = ceil_div_host(a.I, kGemvWaves);
     switch (a.M) {
-      case 1: gated_gemv_kernel<1><<<grid, 512, 0, s>>>(a); break;
-      case 2: gated_gemv_kernel<2><<<grid, 512, 0, s>>>(a); break;
-      case 3: gated_gemv_kernel<3><<<grid, 512, 0, s>>>(a); break;
-      default: gated_gemv_kernel<4><<<grid, 512, 0, s>>>(a); break;
+      case 1: gated_gemv_kernel<1><<<grid, 64 * kGemvWaves, 0, s>>>(a); break;
+      case 2: gated_gemv_kernel<2><<<grid, 64 * kGemvWaves, 0, s>>>(a); break;
+      case 3: gated_gemv_kernel<3><<<grid, 64 * kGemvWaves, 0, s>>>(a); break;
+      default: gated_gemv_kernel<4><<<grid, 64 * kGemvWaves, 0, s>>>(a); break;
     }
-    return hipGetLastError();
-  }
-  if (a.M <= kFewRows) {
-    if (a.M <= 16)
-      gated_rows_kernel<1, 1><<<ceil_div_host(a.I, 16), 64 * kRowsWaves, 0, s>>>(a);
-    else if (a.M <= 32)
-      gated_rows_kernel<2, 2><<<ceil_div_host(a.I, 32), 64 * kRowsWaves, 0, s>>>(a);
-    else
-      gated_rows_kernel<4, 2><<<ceil_div_host(a.I, 32), 64 * kRowsWaves, 0, s>>>(a);
     return hipGetLastError();
   }
   TileArgs t{};
@@ -634,7 +537,7 @@ hipError_t launch_gated(const GatedArgs& a, hipStream_t s) {
   t.rows = a.M;
   t.cols = t.out_ld = a.I;
   t.out = a.out;
-  return launch_tiles<kAct>(t, 2 * a.I, false, s);
+  return launch_tiles<kAct>(t, 2 * a.I, s);
 }
 
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t s) {
@@ -663,7 +566,7 @@ hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s) {
   t.grad_out = a.grad_out;
   t.out = d;
   t.out_ld = 2 * a.I;
-  hipError_t err = launch_tiles<kGradAct>(t, 2 * a.I, false, s);
+  hipError_t err = launch_tiles<kGradAct>(t, 2 * a.I, s);
   if (err == hipSuccess && a.grad_x != nullptr) {
     TileArgs g{};
     g.m_side = d;
@@ -673,7 +576,7 @@ hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s) {
     g.rows = a.M;
     g.out = a.grad_x;
     g.partial = partial;
-    err = launch_tiles<kGradX>(g, a.H, true, s);
+    err = launch_tiles<kGradX>(g, a.H, s);
   }
   if (err == hipSuccess && a.grad_w13 != nullptr) {
     TileArgs g{};
@@ -684,7 +587,7 @@ hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s) {
     g.K = a.M;
     g.out = a.grad_w13;
     g.partial = partial;
-    err = launch_tiles<kGradW>(g, a.H, true, s);
+    err = launch_tiles<kGradW>(g, a.H, s);
   }
   return err;
 }

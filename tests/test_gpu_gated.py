@@ -97,6 +97,12 @@ def test_layer_sizes(M, H, I):
     check(M, H, I // 8 * 8, 3)
 
 
+@pytest.mark.parametrize("M", [4, 5, 16, 17, 32, 33, 64, 65, 128])
+@pytest.mark.parametrize("H,I", [(264, 8200), (136, 16648)])
+def test_few_rows_of_many_features(H, I, M):
+    check(M, H, I, M)
+
+
 @pytest.mark.parametrize("M", [2, 20, 70, 300])
 def test_a_row_that_is_not_finite_stays_alone(M):
     import torch
@@ -187,6 +193,12 @@ def test_gradient_batches(M):
                                  (1000, 1000), (2048, 40), (64, 2048)])
 def test_gradient_sizes(H, I, M):
     check_grad(M, H, I, H + I)
+
+
+@pytest.mark.parametrize("M,H,I", [(7, 72, 8200), (31, 136, 8264), (60, 72, 16648), (200, 2048, 4096),
+                                   (511, 2048, 4096), (513, 2048, 4096)])
+def test_gradient_of_many_features(M, H, I):
+    check_grad(M, H, I, 6)
 
 
 @pytest.mark.parametrize("need", [(True, False), (False, True)])

@@ -411,8 +411,9 @@ constexpr int kSmallSplitTiles = 256;   // 512 and 1024: 5 and 12 % slower at 50
 // Sums shorter than kShortSum, which store more than they read, take 128 x 128
 // all the same, two workgroups to a CU: one stores while the other reads (200
 // rows' grad_w13 of 2 x 5632 x 2048 55 us for 51 with gate and up before it).
-// 128 x 128, gate and up: 64 x 64 a wave, four to each half of a stage's 64 k
-// (900 rows x 2048 x 1408 20.4 us; four waves, stages of 32 k 23.7).
+// 128 x 128, but for grad_w13: 64 x 64 a wave, four to each half of a stage's 64 k
+// (900 rows x 2048 x 1408 20.4 us; four waves, stages of 32 k 23.7; 1500 x 2048 x
+// 5632 gate, up and grad_x 168 for 193, the same with grad_w13 164 for 159).
 //
 // Gate and up of at most 64 rows, or where 128 x 128 would leave half the chip
 // without: tiles of 64 rows or fewer whose waves are 64 features wide (32 gates
@@ -425,16 +426,20 @@ constexpr int kSmallSplitTiles = 256;   // 512 and 1024: 5 and 12 % slower at 50
 // and x straight to registers 13.5, 15, 19 for the first three).
 //
 // A product whose sum is all it stores is cut along K until every CU has a tile.
-constexpr int kShortSum = 512;
+// grad_x whose ranges would be kShortRange or less takes 64 x 128 and longer ones
+// (with gate and up 300 x 4096 x 1024 30.8 us for 34.3, 509 x 2048 x 1408 30.9 for
+// 32.8; 5632 features, ranges of 2816, 85 for 82).
+constexpr int kShortSum = 512, kShortRange = 1024;
 
 struct Plan {
   int bm, bn;                // tile
   int splits, k_per;
 };
-Plan plan_of(bool gated, int rows, int n_rows, int K) {
+Plan plan_of(Op op, int rows, int n_rows, int K) {
   auto tiles = [&](int bm, int bn) {
     return (long long)ceil_div_host(rows, bm) * ceil_div_host(n_rows, bn);
   };
+  const bool gated = op == kAct || op == kGradAct;
   const int cu = kTileCus, stages = ceil_div_host(K, 32);
   Plan p{128, 128, 1, K};
   if (gated && (rows <= 64 || tiles(128, 128) <= cu / 2)) {
@@ -443,14 +448,20 @@ Plan plan_of(bool gated, int rows, int n_rows, int K) {
     return p;
   }
   if (tiles(256, 256) >= cu / 2 && (gated || K >= kShortSum)) p.bm = p.bn = 256;
-  const long long all = tiles(p.bm, p.bn);
-  if (!gated && all < cu) {
+  auto cut = [&] {
+    const long long all = tiles(p.bm, p.bn);
+    if (all >= cu) return;
     // whole stages, at least 8 to a range
     const long long most = std::min(stages / 8, kMaxSplits);
     const long long room = p.bm == 256 ? kSplitTiles / 4 : kSmallSplitTiles;
     p.splits = (int)std::max<long long>(1, std::min(room / all, most));
     p.k_per = ceil_div_host(stages, p.splits) * 32;
     p.splits = ceil_div_host(K, p.k_per);
+  };
+  if (!gated) cut();
+  if (op == kGradX && p.bm == 128 && p.k_per <= kShortRange) {
+    p = Plan{64, 128, 1, K};
+    cut();
   }
   return p;
 }
@@ -458,7 +469,7 @@ Plan plan_of(bool gated, int rows, int n_rows, int K) {
 template <Op kOp>
 hipError_t launch_tiles(TileArgs a, int n_rows, hipStream_t s) {
   constexpr bool kGated = kOp == kAct || kOp == kGradAct;
-  const Plan p = plan_of(kGated, a.rows, n_rows, a.K);
+  const Plan p = plan_of(kOp, a.rows, n_rows, a.K);
   a.splits = p.splits;
   a.k_per = p.k_per;
   a.tiles_m = ceil_div_host(a.rows, p.bm);
@@ -495,6 +506,11 @@ hipError_t launch_tiles(TileArgs a, int n_rows, hipStream_t s) {
       run(tile_kernel<32, 64, 128, 1, 1, 4, 4, kOp>, 4);
     else
       run(tile_kernel<16, 64, 128, 1, 1, 4, 4, kOp>, 4);
+  } else if constexpr (kOp == kGradX) {
+    if (p.bm == 128)
+      run(tile_kernel<128, 128, 64, 2, 2, 2, 4, kOp>, 8);
+    else
+      run(tile_kernel<64, 128, 128, 1, 2, 4, 3, kOp>, 8);
   } else {
     run(tile_kernel<128, 128, 32, 2, 2, 1, 4, kOp>, 4);
   }

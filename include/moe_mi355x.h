@@ -585,9 +585,9 @@ size_t moe_linear_gated_backward_workspace_size(int M, int H, int I);
  *   x, w13, M, H, I as given to moe_linear_gated; grad_out [M, I] bf16
  *   grad_x [M, H], grad_w13 [2I, H] bf16 out, either may be NULL (not wanted)
  *   workspace  moe_linear_gated_backward_workspace_size(...) bytes
- * d_gate and d_up are rounded to bf16, the sums are fp32.  Outputs and
- * workspace overlap neither each other nor an input.  M = 0: grad_w13 is set
- * to 0.  Equal inputs give equal bits.
+ * d_gate and d_up are rounded to bf16 (M <= 16: kept as two bf16 numbers each),
+ * the sums are fp32.  Outputs and workspace overlap neither each other nor an
+ * input.  M = 0: grad_w13 is set to 0.  Equal inputs give equal bits.
  */
 int moe_linear_gated_backward(const uint16_t* x, const uint16_t* w13, const uint16_t* grad_out,
                               int M, int H, int I, uint16_t* grad_x, uint16_t* grad_w13,

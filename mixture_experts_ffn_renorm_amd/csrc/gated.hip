@@ -4,8 +4,11 @@
 //   d_up = d_act * gate * s,  d_gate = d_act * up * s * (1 + gate (1 - s))
 //   d_x = [d_gate d_up] w13,  d_w13 = [d_gate d_up]^T x
 //
-// Four products on one tile kernel.  d_gate and d_up are rounded to bf16 once,
-// as the matrix cores take them; every sum is fp32.
+// Four products on one tile kernel; every sum is fp32.  d_gate and d_up are
+// rounded to bf16, as the matrix cores take them: the gradients are then sqrt 2
+// as far off as their own rounding leaves them.  Of kFewRows rows or fewer each
+// is kept as two bf16 numbers, a high part and what it leaves, a row each: the
+// tiles have room for them (5632 features x 2048, 1 to 16 rows: 47 us either way).
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -36,7 +39,8 @@ struct TileArgs {
   const uint16_t* grad_out;  // kGradAct: [rows, cols]
   uint16_t* out;             // [rows, out_ld]
   int out_ld;
-  float* partial;            // splits > 1: [splits, rows, cols]
+  float* partial;            // splits * parts > 1: [splits, rows, cols]
+  int parts;                 // kGradX, kGradW: 2 where d is [high parts; low parts]
 };
 
 // Swizzles of the LDS tiles, in 16-byte pieces.  Rows of kK k: piece c of row r
@@ -69,10 +73,11 @@ struct Loader {
   int k[kInstr];             // k of the lane's piece within a stage
   size_t step;
   // row(r): the operand's row of tile row r (clamped to one that exists);
-  // across: the tile's first column and how many columns there are
+  // across: the tile's first column and how many columns there are; k from `wrap`
+  // on is k - wrap (one stage alone)
   template <class F>
   __device__ __forceinline__ void init(const uint16_t* p, int ld, int k0, F row, int c0, int ncols,
-                                       int wave, int lane) {
+                                       int wave, int lane, int wrap = 0x7fffffff) {
 #pragma unroll
     for (int i = 0; i < kInstr; ++i) {
       const int q = wave * kInstr + i;
@@ -81,7 +86,8 @@ struct Loader {
         k[i] = q * (64 / kPieces) + lane / kPieces;
         const int c = (lane % kPieces) ^ across_swizzle(k[i]);
         const int col = min(c0 + c * 8, ncols - 8);
-        src[i] = reinterpret_cast<const uint8_t*>(p + (size_t)(k0 + k[i]) * ld + col);
+        const int at = k0 + k[i];
+        src[i] = reinterpret_cast<const uint8_t*>(p + (size_t)(at < wrap ? at : at - wrap) * ld + col);
       } else {
         constexpr int kPieces = kK / 8;                   // per row
         const int r = q * (64 / kPieces) + lane / kPieces;
@@ -147,6 +153,13 @@ __device__ __forceinline__ void each(std::integer_sequence<int, i...>, const F& 
   (f(std::integral_constant<int, i>{}), ...);
 }
 
+constexpr int kFewRows = 16;
+
+// What a bf16 number leaves of v (nothing where it is not finite).
+__device__ __forceinline__ float left_of(float v, float high) {
+  return __builtin_fabsf(high) < INFINITY ? v - high : 0.f;
+}
+
 // Tiles of BM x BN in stages of kK k, a ring of kStages; WM x WN waves, KS times:
 // each such group takes its share of every stage's k.
 template <int BM, int BN, int kK, int WM, int WN, int KS, int kStages, Op kOp>
@@ -184,7 +197,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, BM < 128 && WN == 1 ? 1 : 2) voi
             const int f = min(n0 + r / TN * (TN / 2) + 8 * (i >> 2) + 4 * h + (i & 3), a.cols - 1);
             return q < TN / 2 ? f : a.cols + f;
           },
-          n0, a.cols, wave, lane);
+          n0, a.cols, wave, lane, kOp == kGradW && a.parts == 2 ? a.K / 2 : 0x7fffffff);
   const Reader<BM, kK, kMAcross> rm(wm * TM, lane);
   const Reader<BN, kK, kNAcross> rn(wn * TN, lane);
 
@@ -297,7 +310,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS, BM < 128 && WN == 1 ? 1 : 2) voi
         *reinterpret_cast<u32x4*>(a.out + at) = o;
       } else {
         const u32x4 d = load16(a.grad_out + (size_t)m * a.cols + n);
-        u32x4 og, ou;
+        constexpr bool kTwo = BM <= kFewRows;     // a low part as well
+        u32x4 og, ou, lg, lu;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const f32x4 g = acc[r >> 1][j], u = acc[2 + (r >> 1)][j];
@@ -307,9 +321,18 @@ __global__ __launch_bounds__(64 * WM * WN * KS, BM < 128 && WN == 1 ? 1 : 2) voi
           gated_grad(g[e + 1], u[e + 1], bf16_hi(d[r]), dg[1], du[1]);
           og[r] = pack_bf16x2(dg[0], dg[1]);
           ou[r] = pack_bf16x2(du[0], du[1]);
+          if (kTwo) {
+            lg[r] = pack_bf16x2(left_of(dg[0], bf16_lo(og[r])), left_of(dg[1], bf16_hi(og[r])));
+            lu[r] = pack_bf16x2(left_of(du[0], bf16_lo(ou[r])), left_of(du[1], bf16_hi(ou[r])));
+          }
         }
         *reinterpret_cast<u32x4*>(a.out + at) = og;
         *reinterpret_cast<u32x4*>(a.out + at + a.cols) = ou;
+        if (kTwo) {
+          const size_t low = at + (size_t)a.rows * a.out_ld;
+          *reinterpret_cast<u32x4*>(a.out + low) = lg;
+          *reinterpret_cast<u32x4*>(a.out + low + a.cols) = lu;
+        }
       }
     } else {
 #pragma unroll
@@ -317,7 +340,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, BM < 128 && WN == 1 ? 1 : 2) voi
         const int n = n0 + wn * TN + i * 16 + nq;
         if (n >= a.cols) continue;
         const f32x4 v = acc[i][j];
-        if (a.splits > 1)
+        if (a.splits > 1 || (kOp == kGradX && a.parts > 1))
           *reinterpret_cast<f32x4*>(a.partial + ((size_t)split * a.rows + m) * a.cols + n) = v;
         else
           *reinterpret_cast<u32x2*>(a.out + (size_t)m * a.out_ld + n) =
@@ -373,12 +396,14 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gated_gemv_kernel(moe_host::G
   }
 }
 
-// out = bf16(sum of the splits, in their order); n a multiple of 8
+// out = bf16(sum of the splits, and of a row's parts, in their order); n a multiple
+// of 8
 __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ partial, int splits,
                                                    size_t n, uint16_t* __restrict__ out) {
   for (size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; at < n;
        at += (size_t)gridDim.x * 2048) {
     f32x4 s[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 8
     for (int i = 0; i < splits; ++i) {
       const f32x4* p = reinterpret_cast<const f32x4*>(partial + (size_t)i * n + at);
       s[0] += p[0];
@@ -443,8 +468,8 @@ Plan plan_of(Op op, int rows, int n_rows, int K) {
   const int cu = kTileCus, stages = ceil_div_host(K, 32);
   Plan p{128, 128, 1, K};
   if (gated && (rows <= 64 || tiles(128, 128) <= cu / 2)) {
-    p.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    p.bn = p.bm == 16 || tiles(64, 64) <= cu ? 64 : 128;
+    p.bm = rows <= kFewRows ? kFewRows : rows <= 32 ? 32 : 64;
+    p.bn = p.bm == kFewRows || tiles(64, 64) <= cu ? 64 : 128;
     return p;
   }
   if (tiles(256, 256) >= cu / 2 && (gated || K >= kShortSum)) p.bm = p.bn = 256;
@@ -505,7 +530,7 @@ hipError_t launch_tiles(TileArgs a, int n_rows, hipStream_t s) {
     else if (p.bm == 32)
       run(tile_kernel<32, 64, 128, 1, 1, 4, 4, kOp>, 4);
     else
-      run(tile_kernel<16, 64, 128, 1, 1, 4, 4, kOp>, 4);
+      run(tile_kernel<kFewRows, 64, 128, 1, 1, 4, 4, kOp>, 4);
   } else if constexpr (kOp == kGradX) {
     if (p.bm == 128)
       run(tile_kernel<128, 128, 64, 2, 2, 2, 4, kOp>, 8);
@@ -514,10 +539,11 @@ hipError_t launch_tiles(TileArgs a, int n_rows, hipStream_t s) {
   } else {
     run(tile_kernel<128, 128, 32, 2, 2, 1, 4, kOp>, 4);
   }
-  if (p.splits > 1) {
-    const size_t n = (size_t)a.rows * a.cols;
+  const int parts = kOp == kGradX ? a.parts : 1;
+  if (p.splits * parts > 1) {
+    const size_t n = (size_t)a.rows / parts * a.cols;
     const unsigned g = (unsigned)std::min<size_t>((n / 8 + 255) / 256, 4096);
-    join_kernel<<<g, 256, 0, s>>>(a.partial, p.splits, n, a.out);
+    join_kernel<<<g, 256, 0, s>>>(a.partial, p.splits * parts, n, a.out);
   }
   const hipError_t err = hipGetLastError();
   return err != hipSuccess || rest.rows == 0 ? err : launch_tiles<kOp>(rest, n_rows, s);
@@ -563,16 +589,21 @@ hipError_t launch_zero(void* p, size_t bytes, hipStream_t s) {
   return hipGetLastError();
 }
 
-// [d_gate d_up] [M, 2I], then the larger of the two products' partial sums
+// Rows of d: its parts, and no fewer than a smaller batch has.
+static int rows_of_d(int M) { return std::max(M, std::min(2 * M, 2 * kFewRows)); }
+
+// [d_gate d_up] [rows_of_d(M), 2I], then the larger of the two products' partial sums
 size_t gated_backward_bytes(int M, int H, int I) {
-  return align256((size_t)M * 2 * I * 2) +
-         std::max(partial_bytes(M, H), partial_bytes(2 * I, H));
+  const int rows = rows_of_d(M);
+  return align256((size_t)rows * 2 * I * 2) +
+         std::max(partial_bytes(rows, H), partial_bytes(2 * I, H));
 }
 
 hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s) {
   uint16_t* d = static_cast<uint16_t*>(a.workspace);
   float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
-                                            align256((size_t)a.M * 2 * a.I * 2));
+                                            align256((size_t)rows_of_d(a.M) * 2 * a.I * 2));
+  const int parts = a.M <= kFewRows ? 2 : 1;
   TileArgs t{};
   t.m_side = a.x;
   t.n_side = a.w13;
@@ -589,9 +620,10 @@ hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s) {
     g.n_side = a.w13;
     g.m_ld = g.K = 2 * a.I;
     g.n_ld = g.cols = g.out_ld = a.H;
-    g.rows = a.M;
+    g.rows = a.M * parts;
     g.out = a.grad_x;
     g.partial = partial;
+    g.parts = parts;
     err = launch_tiles<kGradX>(g, a.H, s);
   }
   if (err == hipSuccess && a.grad_w13 != nullptr) {
@@ -600,9 +632,10 @@ hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s) {
     g.n_side = a.x;
     g.m_ld = g.rows = 2 * a.I;
     g.n_ld = g.cols = g.out_ld = a.H;
-    g.K = a.M;
+    g.K = a.M * parts;
     g.out = a.grad_w13;
     g.partial = partial;
+    g.parts = parts;
     err = launch_tiles<kGradW>(g, a.H, s);
   }
   return err;

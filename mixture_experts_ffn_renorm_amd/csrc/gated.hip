@@ -45,8 +45,9 @@ struct TileArgs {
 
 // Swizzles of the LDS tiles, in 16-byte pieces.  Rows of kK k: piece c of row r
 // lies at c ^ (r / 2 % pieces), c ^ (r % 16) where a row is 256 bytes, so that the
-// rows of one beat of a 16-byte read lie in different banks.  Rows of R columns: the pairs of pieces are exchanged
-// by the bits of k in which the lanes of a transposing read differ.
+// rows of one beat of a 16-byte read lie in different banks.  Rows of R columns:
+// the pairs of pieces are exchanged by the bits of k in which the lanes of a
+// transposing read differ.
 template <int kK>
 __device__ __forceinline__ int along_swizzle(int r) {
   return kK < 128 ? (r >> 1) & (kK / 8 - 1) : r & 15;
@@ -86,8 +87,8 @@ struct Loader {
         k[i] = q * (64 / kPieces) + lane / kPieces;
         const int c = (lane % kPieces) ^ across_swizzle(k[i]);
         const int col = min(c0 + c * 8, ncols - 8);
-        const int at = k0 + k[i];
-        src[i] = reinterpret_cast<const uint8_t*>(p + (size_t)(at < wrap ? at : at - wrap) * ld + col);
+        const int at = k0 + k[i] < wrap ? k0 + k[i] : k0 + k[i] - wrap;
+        src[i] = reinterpret_cast<const uint8_t*>(p + (size_t)at * ld + col);
       } else {
         constexpr int kPieces = kK / 8;                   // per row
         const int r = q * (64 / kPieces) + lane / kPieces;
@@ -163,7 +164,8 @@ __device__ __forceinline__ float left_of(float v, float high) {
 // Tiles of BM x BN in stages of kK k, a ring of kStages; WM x WN waves, KS times:
 // each such group takes its share of every stage's k.
 template <int BM, int BN, int kK, int WM, int WN, int KS, int kStages, Op kOp>
-__global__ __launch_bounds__(64 * WM * WN * KS, BM < 128 && WN == 1 ? 1 : 2) void tile_kernel(TileArgs a) {
+__global__ __launch_bounds__(64 * WM * WN * KS, BM < 128 && WN == 1 ? 1 : 2) void tile_kernel(
+    TileArgs a) {
   constexpr int W = WM * WN * KS, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr bool kGated = kOp == kAct || kOp == kGradAct;
   constexpr bool kMAcross = kOp == kGradW, kNAcross = kOp == kGradX || kOp == kGradW;
@@ -435,20 +437,20 @@ constexpr int kSmallSplitTiles = 256;   // 512 and 1024: 5 and 12 % slower at 50
 // of 64 k, hold too little in flight (4096 rows x 2048 x 5632 175 us for 168).
 // Sums shorter than kShortSum, which store more than they read, take 128 x 128
 // all the same, two workgroups to a CU: one stores while the other reads (200
-// rows' grad_w13 of 2 x 5632 x 2048 55 us for 51 with gate and up before it).
+// rows' grad_w13 of 2 x 5632 x 2048 51 us for 55 with gate and up before it).
 // 128 x 128, but for grad_w13: 64 x 64 a wave, four to each half of a stage's 64 k
 // (900 rows x 2048 x 1408 20.4 us; four waves, stages of 32 k 23.7; 1500 x 2048 x
 // 5632 gate, up and grad_x 168 for 193, the same with grad_w13 164 for 159).
 //
 // Gate and up of at most 64 rows, or where 128 x 128 would leave half the chip
-// without: tiles of 64 rows or fewer whose waves are 64 features wide (32 gates
-// and their ups) and share out a stage of 128 k, 256-byte runs of every row.
-// Each wave reads its k alone, so LDS is read once for all rows, and the sums
-// meet in LDS at the end.  Tiles 64 features wide while the chip holds them at once,
-// else 128.  2048 x 5632: 16 rows 11.0 us, 32 12.0, 64 14.1, 128 18; 200 x 2048 x
-// 1408 10.3, 300 x 4096 x 1024 16.6, 509 x 2048 x 1408 14.3 (waves side by side,
-// stages of 64 k: 23, 16.3, 28.6, 16.3; weights through LDS of each wave's own
-// and x straight to registers 13.5, 15, 19 for the first three).
+// without: tiles of 64 rows or fewer whose waves are 64 rows of w13 wide (32 gates
+// and their ups) and share out a stage of 128 k, 256-byte runs of every row.  So a
+// fragment of x is read from LDS once a tile, or twice; the sums meet in LDS at
+// the end.  Tiles 64 wide while the chip holds them at once, else 128.  2048 x
+// 5632: 16 rows 11.0 us, 32 12.0, 64 14.0 (weights through LDS of each wave's own
+// and x straight to registers 13.5, 15, 19), 128 rows 18.2; 200 x 2048 x 1408
+// 10.3, 300 x 4096 x 1024 16.6, 509 x 2048 x 1408 14.3 (64 x 128 by waves side by
+// side, stages of 64 k: 18.2, 16.2, 28.6, 16.3).
 //
 // A product whose sum is all it stores is cut along K until every CU has a tile.
 // grad_x whose ranges would be kShortRange or less takes 64 x 128 and longer ones

@@ -49,7 +49,7 @@ constexpr int kMaxChunks = 64;
 constexpr int kFill = 2048;         // workgroups that fill the chip: no more chunks than that
 constexpr int kKeep = 64;           // a longer list is cut back before it takes more
 constexpr int kList = kKeep + 64;
-constexpr int kFewLanes = 6;        // that hold a hit: their logits are dealt out one lane after another
+constexpr int kFewLanes = 6;        // with a hit: their logits are dealt out, a lane's at a time
 
 typedef unsigned long long u64;
 
@@ -268,8 +268,8 @@ __device__ __forceinline__ void finish(const moe_host::LogprobArgs& a, int m, co
 
 // ---- one chunk of a row ----
 template <bool kBf16, bool kTop>
-__global__ __launch_bounds__(kThreads, kMinWaves) void logprob_kernel(moe_host::LogprobArgs a, int chunks,
-                                                           int chunk_blocks) {
+__global__ __launch_bounds__(kThreads, kMinWaves) void logprob_kernel(
+    moe_host::LogprobArgs a, int chunks, int chunk_blocks) {
 #pragma clang fp contract(off)      // an anchor's product is the rounded one wherever it is used
   constexpr int kPer = Row<kBf16>::kPer;
   __shared__ float s_m[kWaves], s_a[kWaves], s_z[kWaves], s_s[kWaves];

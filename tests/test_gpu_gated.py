@@ -174,7 +174,8 @@ def check_grad(M, H, I, seed=0, data=None, need=(True, True)):
     assert (ws[-64:] == 255).all()
     # 16 rows or fewer: d_gate and d_up are two bf16 numbers each, off by 2^-8 of 2^-8
     ref = do.gated_backward(*(mo.widen_bf16(t).astype(np.float64) for t in (x, w, d)))
-    for b, out, g, wanted, (_, bound), want in zip(bufs, outs, got, need, grad_bounds(x, w, d, B * B if M <= 16 else B), ref):
+    bounds = grad_bounds(x, w, d, B * B if M <= 16 else B)
+    for b, out, g, wanted, (_, bound), want in zip(bufs, outs, got, need, bounds, ref):
         if not wanted:
             assert g is None and (b == -7.0).all()
             continue
@@ -203,8 +204,8 @@ def test_gradient_of_the_fewest_rows(H, I, M):
     check_grad(M, H, I, 9, need=(M % 2 == 0, M % 2 == 1))
 
 
-@pytest.mark.parametrize("M,H,I", [(7, 72, 8200), (31, 136, 8264), (60, 72, 16648), (200, 2048, 4096),
-                                   (511, 2048, 4096), (513, 2048, 4096)])
+@pytest.mark.parametrize("M,H,I", [(7, 72, 8200), (31, 136, 8264), (60, 72, 16648),
+                                   (200, 2048, 4096), (511, 2048, 4096), (513, 2048, 4096)])
 def test_gradient_of_many_features(M, H, I):
     check_grad(M, H, I, 6)
 

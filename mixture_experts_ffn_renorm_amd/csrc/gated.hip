@@ -40,7 +40,7 @@ struct TileArgs {
   uint16_t* out;             // [rows, out_ld]
   int out_ld;
   float* partial;            // splits * parts > 1: [splits, rows, cols]
-  int parts;                 // kGradX, kGradW: 2 where d is [high parts; low parts]
+  int parts;                 // gradients: 2 where d is [high parts; low parts]
 };
 
 // Swizzles of the LDS tiles, in 16-byte pieces.  Rows of kK k: piece c of row r
@@ -312,7 +312,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS, BM < 128 && WN == 1 ? 1 : 2) voi
         *reinterpret_cast<u32x4*>(a.out + at) = o;
       } else {
         const u32x4 d = load16(a.grad_out + (size_t)m * a.cols + n);
-        constexpr bool kTwo = BM <= kFewRows;     // a low part as well
+        // a low part as well (a large batch's last rows have such tiles too, and none)
+        const bool two = BM <= kFewRows && a.parts == 2;
         u32x4 og, ou, lg, lu;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -323,14 +324,14 @@ __global__ __launch_bounds__(64 * WM * WN * KS, BM < 128 && WN == 1 ? 1 : 2) voi
           gated_grad(g[e + 1], u[e + 1], bf16_hi(d[r]), dg[1], du[1]);
           og[r] = pack_bf16x2(dg[0], dg[1]);
           ou[r] = pack_bf16x2(du[0], du[1]);
-          if (kTwo) {
+          if (two) {
             lg[r] = pack_bf16x2(left_of(dg[0], bf16_lo(og[r])), left_of(dg[1], bf16_hi(og[r])));
             lu[r] = pack_bf16x2(left_of(du[0], bf16_lo(ou[r])), left_of(du[1], bf16_hi(ou[r])));
           }
         }
         *reinterpret_cast<u32x4*>(a.out + at) = og;
         *reinterpret_cast<u32x4*>(a.out + at + a.cols) = ou;
-        if (kTwo) {
+        if (two) {
           const size_t low = at + (size_t)a.rows * a.out_ld;
           *reinterpret_cast<u32x4*>(a.out + low) = lg;
           *reinterpret_cast<u32x4*>(a.out + low + a.cols) = lu;
@@ -615,6 +616,7 @@ hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s) {
   t.grad_out = a.grad_out;
   t.out = d;
   t.out_ld = 2 * a.I;
+  t.parts = parts;
   hipError_t err = launch_tiles<kGradAct>(t, 2 * a.I, s);
   if (err == hipSuccess && a.grad_x != nullptr) {
     TileArgs g{};

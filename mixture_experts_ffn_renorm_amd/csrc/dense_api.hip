@@ -138,6 +138,7 @@ int moe_linear_gated_backward(const uint16_t* x, const uint16_t* w13, const uint
   hipStream_t s = static_cast<hipStream_t>(stream);
   const size_t rows = (size_t)M * H * 2, weights = (size_t)I * H * 4;
   if (M == 0) {   // no rows: the weights' gradient is 0
+    if (overlap({grad_w13, weights}, {w13, weights})) return MOE_ERR_INVALID_ARG;
     if (grad_w13) MOE_TRY_LAUNCH(launch_zero(grad_w13, weights, s));
     return MOE_OK;
   }

@@ -1188,21 +1188,14 @@ def moe_token_logprobs(logits, tokens, top: int = 0, logprobs=None, entropy=None
                        (fp32, M, V, top), ws, dev, stream)
     f32, i32 = torch.float32, torch.int32
     outs = [logprobs, entropy, lse, top_ids if top else None, top_logprobs if top else None]
-    for k, name in enumerate(("logprobs", "entropy", "lse")):
+    # each a tensor of its own: views of one count a change of one as a change of all
+    for k, name, dtype, shape in ((0, "logprobs", f32, (M,)), (1, "entropy", f32, (M,)),
+                                  (2, "lse", f32, (M,)), (3, "top_ids", i32, (M, top)),
+                                  (4, "top_logprobs", f32, (M, top))):
         if outs[k] is not None:
-            _need(outs[k], name, f32, (M,), dev)
-    for k, name, dtype in ((3, "top_ids", i32), (4, "top_logprobs", f32)):
-        if outs[k] is not None:
-            _need(outs[k], name, dtype, (M, top), dev)
-        elif top:
-            outs[k] = _empty((M, top), dtype, dev, stream)
-    if logprobs is None and entropy is None and lse is None:
-        # one allocation; rows of whole 16 bytes, as every operand's start
-        outs[:3] = _empty((3, (M + 3) & ~3), f32, dev, stream)[:, :M].unbind(0)
-    else:
-        for k in range(3):
-            if outs[k] is None:
-                outs[k] = _empty((M,), f32, dev, stream)
+            _need(outs[k], name, dtype, shape, dev)
+        elif k < 3 or top:
+            outs[k] = _empty(shape, dtype, dev, stream)
     st = library().moe_token_logprobs(logits.data_ptr(), fp32, tokens.data_ptr(), M, V, top,
                                       *map(_ptr, outs), ws.data_ptr(), ws.numel(),
                                       _raw_stream(dev, stream))

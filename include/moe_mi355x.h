@@ -685,9 +685,10 @@ int moe_token_logprobs(const void* logits, int logits_fp32, const int32_t* token
  *   grad_logprobs, grad_entropy [M] fp32
  *   grad_logits  [M, V] of the logits' type out, 16-byte aligned; logits
  *                itself, or overlapping no input
- * A token outside [0, V) leaves its logprob without a gradient.  A row whose
- * lse is below -1e30 (no logit, or only a mask's lowest value, which fp32
- * cannot tell from its lse) has gradient 0.
+ * A token outside [0, V) leaves its logprob without a gradient.  p_v carries
+ * the rounding of lse, 2^-24 |lse| of itself.  A row whose lse is below -2^24
+ * (every token ruled out, by -inf or a large negative number: lse cannot tell
+ * how many there are) has gradient 0.
  */
 int moe_token_logprobs_backward(const void* logits, int logits_fp32, const int32_t* tokens,
                                 const float* lse, const float* entropy,

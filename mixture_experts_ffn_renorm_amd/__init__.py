@@ -1211,8 +1211,8 @@ def moe_token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs, gra
     that it gave and their gradients [M] fp32 (``grad_entropy`` None: the
     entropy has none, and ``entropy`` may be None).  ``grad_logits`` may be
     ``logits`` itself; else it overlaps no operand.  A token outside [0, V)
-    leaves its logprob without a gradient; a row whose lse is below -1e30
-    (every logit ruled out) has gradient 0."""
+    leaves its logprob without a gradient; a row whose lse is below -2^24
+    (every logit ruled out, by -inf or a large negative number) has gradient 0."""
     torch = _torch()
     M, V, fp32 = _logits_type("moe_token_logprobs_backward", logits)
     dev = logits.get_device()

@@ -593,9 +593,10 @@ void launch_rows(const moe_host::LogprobArgs& a, hipStream_t s) {
 // ---- gradient ----
 //
 // log p = l - lse; d = -p (g + h (log p + H)), g more at the token.  A row
-// whose lse is below kNone has no logit that fp32 can tell from its lse (all
-// are -inf or a mask's lowest value): its gradient is 0.
-constexpr float kNone = -1e30f;
+// whose lse is below kNone is ruled out from end to end (by -inf, the type's
+// lowest value or -1e9): fp32's step there is 2 or more, lse does not tell how
+// many logits share it, and p would be 1 for each of them.  Its gradient is 0.
+constexpr float kNone = -kFar;
 constexpr int kGradLoads = 4;       // blocks a thread
 
 template <bool kBf16>

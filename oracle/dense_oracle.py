@@ -42,7 +42,7 @@ def token_logprobs_backward(logits, tokens, lse, entropy, g, h) -> np.ndarray:
     l = logits.astype(np.float64)
     out = np.zeros_like(l)
     for m in range(l.shape[0]):
-        if lse[m] < -1e30:
+        if lse[m] < -2.0 ** 24:      # ruled out from end to end
             continue
         logp = l[m] - np.float64(lse[m])
         p = np.exp(logp)

@@ -664,8 +664,9 @@ size_t moe_token_logprobs_workspace_size(int logits_fp32, int M, int V, int top)
  * V <= 2^19, M*V <= 2^35, top <= min(V, 32).
  * Logits may be -inf (a token ruled out).  A row of -inf throughout has log
  * probabilities and lse -inf, entropy 0, and the lowest ids as alternatives.
- * A row with a NaN or +inf has NaN in all its fp32 outputs; its alternatives'
- * ids stay in order, NaN after -inf.  No sum depends on the other rows or on
+ * A row with a NaN or +inf has NaN in all its fp32 outputs (but 0 for a token
+ * outside [0, V), as in any row); its alternatives' ids stay in order, NaN
+ * after -inf.  No sum depends on the other rows or on
  * timing: equal inputs give equal bits.
  */
 int moe_token_logprobs(const void* logits, int logits_fp32, const int32_t* tokens, int M, int V,

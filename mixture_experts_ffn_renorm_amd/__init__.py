@@ -1171,8 +1171,8 @@ def moe_token_logprobs(logits, tokens, top: int = 0, logprobs=None, entropy=None
     lower id.  Returns (logprobs, entropy, lse, top_ids, top_logprobs), the
     last two None without ``top``.  Logits may be -inf (a token ruled out); a
     row that is -inf throughout has log probabilities and lse -inf and entropy
-    0.  A row with NaN or +inf gives NaN; its alternatives stay in order, NaN
-    last."""
+    0.  A row with NaN or +inf gives NaN (a token outside [0, V) 0 there too);
+    its alternatives stay in order, NaN last."""
     torch = _torch()
     M, V, fp32 = _logits_type("moe_token_logprobs", logits)
     top = int(top)

@@ -455,8 +455,11 @@ constexpr int kSmallSplitTiles = 256;   // 512 and 1024: 5 and 12 % slower at 50
 //
 // A product whose sum is all it stores is cut along K until every CU has a tile.
 // grad_x whose ranges would be kShortRange or less takes 64 x 128 and longer ones
-// (with gate and up 300 x 4096 x 1024 30.8 us for 34.3, 509 x 2048 x 1408 30.9 for
-// 32.8; 5632 features, ranges of 2816, 85 for 82).
+// where 128 x 128 would leave half the chip without (with gate and up 300 x 4096 x
+// 1024 30.2 us for 33.8, 509 x 2048 x 1408 30.2 for 31.7, 1000 x 2048 x 200 18.3 for
+// 20.1; 5632 features, ranges of 2816, 85 for 82; more tiles than half the chip: 300 x
+// 8192 x 248 40.0 for 37.2, 1800 x 2048 x 200 25.4 for 21.8, 4096 x 8192 x 200 132
+// for 101).
 constexpr int kShortSum = 512, kShortRange = 1024;
 
 struct Plan {
@@ -487,7 +490,7 @@ Plan plan_of(Op op, int rows, int n_rows, int K) {
     p.splits = ceil_div_host(K, p.k_per);
   };
   if (!gated) cut();
-  if (op == kGradX && p.bm == 128 && p.k_per <= kShortRange) {
+  if (op == kGradX && p.bm == 128 && p.k_per <= kShortRange && tiles(128, 128) <= cu / 2) {
     p = Plan{64, 128, 1, K};
     cut();
   }

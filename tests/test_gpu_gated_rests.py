@@ -1,5 +1,5 @@
 """The bf16 gated block where the last round of tiles leaves few rows, which
-become a product of their own."""
+become a product of their own, and gradients of few features."""
 
 from __future__ import annotations
 
@@ -41,3 +41,11 @@ def test_gradient_writes_no_row_behind_the_last(M):
     assert (ws[used:] == 255).all()
     # the rows themselves: a NaN left among them would reach every feature
     assert torch.isfinite(gw).all()
+
+
+@pytest.mark.parametrize("M,H,I", [(1000, 2048, 200), (1024, 2048, 64), (1030, 2048, 200),
+                                   (300, 8192, 248), (700, 4096, 496), (2100, 2048, 248),
+                                   (4099, 2048, 256), (1100, 8200, 104)])
+def test_gradient_of_few_features(M, H, I):
+    """grad_x whose sums are short, its tiles on both sides of half the chip."""
+    tg.check_grad(M, H, I, M, need=(True, False))

@@ -459,15 +459,24 @@ using moe_host::ceil_div_host;
 // and 46 us against 41 for 4096 tokens, 8192 columns, rank 64).
 constexpr int kManyTokens = 1024;
 
-// Tokens up to which each reads its adapter by itself: 128 tokens, 48 adapters of
-// rank 16, 2048 -> 11264 columns gated 12.6 us against 17.8 by units; 256 tokens
-// of rank 64 43 us against 31.
+// Tokens up to which each reads its adapter by itself, whatever the rank: where the
+// two meet depends little on how many adapters there are, more on rank and K.  2048
+// -> 8192 columns, 16 adapters, each by itself and by units: rank 16, 128 tokens 9.7
+// and 14.0 us, 256 13.6 and 15.2; rank 64, 100 tokens 20.6 and 23.5, 128 23.7 and
+// 24.0, 192 32 and 25; rank 128, 64 tokens 23.6 and 33.4, 100 33.7 and 34.0, 128 41
+// and 35, but 51 and 80 of 8192 -> 8192 columns.  One adapter for all: 7.7 and 12.6,
+// 22.5 and 21.8, 39 and 31 at 128 tokens.
 constexpr int kGemvTokens = 128;
 
-// One launch where an adapter's A has at most kOneLaunchA bytes (a wave then
-// reads its rows at once) and all workgroups' reading of it kOneLaunchAll: rank
-// 16, 2048 -> 2048 columns, 1 to 64 tokens 8.7 us a call against 11.4, 5.2 to
-// 5.6 on the GPU either way; rank 64 13.4 against 5.4.
+// One launch where an adapter's A has at most kOneLaunchA bytes and all workgroups'
+// reading of it is at most kOneLaunchAll.  It saves a launch's 2.7 us of the host
+// (rank 16, 2048 -> 2048 columns, 1 to 64 tokens 8.7 us a call against 11.4) and
+// costs time on the GPU, more with the passes of 16 rows over A.  -> 2048 columns, 1
+// to 32 tokens, one launch and two: rank 16 x 2048 5.3 to 5.6 and 5.0 to 5.2 us, rank
+// 32 x 1408 5.3 to 5.6 and 4.9 to 5.3, rank 128 x 256 9.4 to 9.9 and 6.1 to 6.4;
+// larger A: rank 16 x 2560 5.7 to 5.9 and 5.1 to 5.4, x 4096 7.5 to 8.7 and 5.4 to
+// 5.6, rank 64 x 1024 7.1 to 7.7 and 5.5 to 5.7; more reading: 64 tokens, rank 16,
+// 2048 -> 8192 columns 13.6 and 6.0.
 constexpr long long kOneLaunchA = 64 << 10, kOneLaunchAll = 64 << 20;
 
 struct Layout {

@@ -8,7 +8,8 @@
 // rounded to bf16, as the matrix cores take them: the gradients are then sqrt 2
 // as far off as their own rounding leaves them.  Of kFewRows rows or fewer each
 // is kept as two bf16 numbers, a high part and what it leaves, a row each: the
-// tiles have room for them (5632 features x 2048, 1 to 16 rows: 47 us either way).
+// tiles have room for them (5632 features x 2048, 1 to 16 rows: 48 to 51 us; with
+// one number each it took as long).
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -357,7 +358,9 @@ __global__ __launch_bounds__(64 * WM * WN * KS, BM < 128 && WN == 1 ? 1 : 2) voi
 //
 // Four waves a workgroup, so that 5632 features are 5.5 of them on every CU
 // (2048 x 5632, one row 9.7 us; eight waves of two features 11.6: 1.4 workgroups
-// a CU).  Four rows 11.9 us, by tiles 10.9; 4096 x 1024 7.9 and 10.5.
+// a CU).  Two to four rows 4.7 to 5.6 us (2048 x 1408), 6.4 to 7.5 (4096 x 1024),
+// 28 to 32 (8192 x 4096); by tiles 6.9, 10.1 and 31.6.  2048 x 5632 is the one size
+// measured where tiles are as fast: 10.1 to 10.6 and 9.8 to 10.0.
 constexpr int kGemvRows = 4;
 constexpr int kGemvWaves = 4;
 
@@ -434,11 +437,15 @@ constexpr int kSmallSplitTiles = 256;   // 512 and 1024: 5 and 12 % slower at 50
 // 12 TB/s from L2 over the chip), and what they cost follows the lines that they
 // touch.
 //
-// Large: 256 x 256 where half the chip has one; whole 128-byte lines, two stages
-// of 64 k, hold too little in flight (4096 rows x 2048 x 5632 175 us for 168).
-// Sums shorter than kShortSum, which store more than they read, take 128 x 128
-// all the same, two workgroups to a CU: one stores while the other reads (200
-// rows' grad_w13 of 2 x 5632 x 2048 51 us for 55 with gate and up before it).
+// Large: 256 x 256 where half the chip has one, however few the rows (16 rows'
+// gradient, 40000 x 1408, 182 us with grad_x alone, by 128 x 128 176); whole
+// 128-byte lines, two stages of 64 k, hold too little in flight (4096 rows x 2048 x
+// 5632 175 us for 168).
+// Sums of grad_x and grad_w13 shorter than kShortSum, which store more than they
+// read, take 128 x 128 all the same.  grad_w13's are two workgroups to a CU: one
+// stores while the other reads (200 rows' grad_w13 of 2 x 5632 x 2048 51 us for 55
+// with gate and up before it); grad_x's, one to a CU, gain with few tiles and lose
+// with many (4096 x 2048 x 248 33 us for 46, 4096 x 8192 x 200 100 for 81).
 // 128 x 128, but for grad_w13: 64 x 64 a wave, four to each half of a stage's 64 k
 // (900 rows x 2048 x 1408 20.4 us; four waves, stages of 32 k 23.7; 1500 x 2048 x
 // 5632 gate, up and grad_x 168 for 193, the same with grad_w13 164 for 159).
@@ -453,7 +460,9 @@ constexpr int kSmallSplitTiles = 256;   // 512 and 1024: 5 and 12 % slower at 50
 // 10.3, 300 x 4096 x 1024 16.6, 509 x 2048 x 1408 14.3 (64 x 128 by waves side by
 // side, stages of 64 k: 18.2, 16.2, 28.6, 16.3).
 //
-// A product whose sum is all it stores is cut along K until every CU has a tile.
+// A product whose sum is all it stores is cut along K until every CU has a tile,
+// in ranges of at least 8 times 32 k; one that ends inside a tile's stage of 64 or
+// 128 k is filled up with zeros.
 // grad_x whose ranges would be kShortRange or less takes 64 x 128 and longer ones
 // where 128 x 128 would leave half the chip without (with gate and up 300 x 4096 x
 // 1024 30.2 us for 33.8, 509 x 2048 x 1408 30.2 for 31.7, 1000 x 2048 x 200 18.3 for
@@ -471,7 +480,7 @@ Plan plan_of(Op op, int rows, int n_rows, int K) {
     return (long long)ceil_div_host(rows, bm) * ceil_div_host(n_rows, bn);
   };
   const bool gated = op == kAct || op == kGradAct;
-  const int cu = kTileCus, stages = ceil_div_host(K, 32);
+  const int cu = kTileCus, stages = ceil_div_host(K, 32);   // the shortest tiles' stages
   Plan p{128, 128, 1, K};
   if (gated && (rows <= 64 || tiles(128, 128) <= cu / 2)) {
     p.bm = rows <= kFewRows ? kFewRows : rows <= 32 ? 32 : 64;
@@ -482,7 +491,6 @@ Plan plan_of(Op op, int rows, int n_rows, int K) {
   auto cut = [&] {
     const long long all = tiles(p.bm, p.bn);
     if (all >= cu) return;
-    // whole stages, at least 8 to a range
     const long long most = std::min(stages / 8, kMaxSplits);
     const long long room = p.bm == 256 ? kSplitTiles / 4 : kSmallSplitTiles;
     p.splits = (int)std::max<long long>(1, std::min(room / all, most));

@@ -23,11 +23,14 @@
 // a key that exactly `top` entries reach (wave ballots), equal keys by their ids;
 // the last 64 entries or fewer are ranked against each other.
 //
-// 2048 rows of 131072 bf16 logits: 106 us without alternatives (5.1 TB/s, what
-// a large copy reaches), 116 us with 5, 154 us with 20; one row 5.4, 11 and 18
-// us, two launches and the searches' chains.  A threshold taken from the first
-// group alone: 136 and 166 us.  Without a prefetch a wave takes 64 registers and
-// a SIMD holds 8 of them, which hide the loads (4 waves at the least: 5 % more).
+// 2048 rows of 131072 bf16 logits: 104 to 108 us without alternatives (5.1 TB/s,
+// what a large copy reaches), 110 to 121 with 5, 154 with 20, 184 with 32; of fp32
+// 191, 199, 215 and 222 us.  One row 5.4 to 7, 11 to 13, 18 to 19.5 and 21 us, two
+// launches and the searches' chains.  From 20 on the lists take vector instructions,
+// which 5 alternatives keep busy for 90 % of the time already.  A threshold taken
+// from the first group alone: 136 us with 5, 166 with 20.  Without a prefetch a wave
+// takes 64 registers and a SIMD holds 8 of them, which hide the loads (4 waves at
+// the least: 5 % more).
 #include <algorithm>
 
 #include "dense.h"
